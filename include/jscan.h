@@ -410,6 +410,106 @@ jscan_status jscan_prefill_chunked_noalloc(const void *x, const void *delta, con
                                            float *h_final, int64_t batch, int64_t L, int64_t D,
                                            int64_t N, int64_t chunk, jscan_dtype dtype, void *stream);
 
+/*
+ * Gated recurrence: the linear recurrence without the expansion over d_state, its gate an input.
+ * One fp32 state per (sequence, channel):
+ *     JSCAN_GATE_DECAY     h_t = exp(g_t) h_{t-1} + u_t                          (g a log decay)
+ *     JSCAN_GATE_SIGMOID   h_t = sigmoid(g_t) h_{t-1} + (1 - sigmoid(g_t)) u_t   (g a gate logit)
+ *     y_t = h_t, rounded to nearest even to the dtype
+ * g = -inf drops the state before the token (a reset inside a row); gates that make the recurrence
+ * unstable (g > 0 in the decay form) are not checked.
+ *
+ * Scan over whole sequences.
+ *   g, u, y   batch * L token rows of D values in `dtype`; the row of token t of sequence b starts at
+ *             element (b * L + t) * ld (ld_g, ld_u, ld_y >= D).  So g and u may be the halves of one
+ *             [batch][L][2 D] projection.  Any D >= 0 and any ld; tensors whose rows all start on 4 bytes
+ *             (bf16: even D, ld and start) run faster.  Pointers are aligned to their elements.
+ *   h0        [batch][D] fp32 state before the first token, or NULL for zeros; may equal h_final
+ *   lengths   [batch] int32 in device memory, or NULL when every sequence has L tokens.  Sequence b
+ *             has lengths[b] tokens (taken into [0, L]); its later rows of g and u are not read, and
+ *             its later rows of y are set to zero
+ *   h_final   [batch][D] fp32 state after the last token (h0 for an empty sequence)
+ *   workspace device memory of jscan_gated_scan_workspace(batch, L, D) bytes, 16-byte aligned,
+ *             overlapping nothing else; may be NULL when that is 0.  Contents on entry do not
+ *             matter.  Calls that share a workspace must be ordered on one stream.
+ * A long axis is cut into segments that run side by side and are joined through their composed
+ * maps, so states agree with the decode-step chain to the fp32 rounding of that composition, not
+ * bit for bit.  Results are deterministic (fixed orders, no atomics).  With L == 0, g, u and y may
+ * be NULL.  Errors as for jscan_prefill_chunked, and JSCAN_ERR_FORM for an unknown form.
+ */
+typedef enum { JSCAN_GATE_DECAY = 0, JSCAN_GATE_SIGMOID = 1 } jscan_gate_form;
+
+jscan_status jscan_gated_scan(const void *g, const void *u, const float *h0, const int32_t *lengths,
+                              void *y, float *h_final, int64_t batch, int64_t L, int64_t D,
+                              int64_t ld_g, int64_t ld_u, int64_t ld_y, void *workspace,
+                              int64_t workspace_bytes, jscan_gate_form form, jscan_dtype dtype,
+                              void *stream);
+
+/* Workspace bytes of jscan_gated_scan and jscan_gated_scan_backward for this shape (the same for
+ * both, either form, either dtype), or -1 if the shape is invalid.  Host-only. */
+int64_t jscan_gated_scan_workspace(int64_t batch, int64_t L, int64_t D);
+
+/*
+ * Backward pass of jscan_gated_scan.  With G_t = dLoss/dh_t, c_t = a_t G_t and a_t the decay:
+ *     G_t = dy_t + c_{t+1}   (dh_final in place of c after the last token),   dh0 = c_1
+ *     JSCAN_GATE_DECAY     du_t = G_t               dg_t = c_t h_{t-1}
+ *     JSCAN_GATE_SIGMOID   du_t = (1 - a_t) G_t     dg_t = c_t (1 - a_t) (h_{t-1} - u_t)
+ * G and c are fp32; h_{t-1} is read from y, so for bf16 it carries y's one rounding (at most 2^-8 relative).
+ *   g, u, y, dy   token rows as above; u may be NULL (and is not read) in the decay form; y is the
+ *                 scan's output
+ *   h0            the scan's, NULL for zeros;   dh_final [batch][D] fp32, NULL for zeros
+ *   lengths       as for the scan; rows of padding are not read
+ *   dg, du        token rows out, in `dtype`; zero in rows of padding.  They may be the halves of one
+ *                 [batch][L][2 D] buffer
+ *   dh0           [batch][D] fp32 out, or NULL when it is not wanted; may equal dh_final
+ * Workspace, errors and determinism as for jscan_gated_scan.
+ */
+jscan_status jscan_gated_scan_backward(const void *g, const void *u, const void *y, const void *dy,
+                                       const float *h0, const float *dh_final,
+                                       const int32_t *lengths, void *dg, void *du, float *dh0,
+                                       int64_t batch, int64_t L, int64_t D, int64_t ld_g,
+                                       int64_t ld_u, int64_t ld_y, int64_t ld_dy, int64_t ld_dg,
+                                       int64_t ld_du, void *workspace, int64_t workspace_bytes,
+                                       jscan_gate_form form, jscan_dtype dtype, void *stream);
+
+/*
+ * One decode token of the gated recurrence for a batch: h [batch][D] fp32 in place; g_t, u_t and y_t
+ * are batch rows of D values with row strides ld_g, ld_u, ld_y >= D.
+ */
+jscan_status jscan_gated_step(float *h, const void *g_t, const void *u_t, void *y_t, int64_t batch,
+                              int64_t D, int64_t ld_g, int64_t ld_u, int64_t ld_y,
+                              jscan_gate_form form, jscan_dtype dtype, void *stream);
+
+/*
+ * A linear layer with weights and activations in 8-bit integers (the review page of Jamba-1.5,
+ * section 3-2.3, holds the model's expert weights in int8 for serving).
+ *
+ * Row quantiser: every row (token) of x gets a scale of its own,
+ *     scale[m] = max(max_k |x[m][k]| / 127, 2^-126),   q[m][k] = rint(x[m][k] * (1 / scale[m]))
+ * in fp32, ties to even.  A row that holds a NaN or an infinity gets scale NaN and q = 0, so the
+ * product's row is NaN and no other row is touched.
+ *   x      M rows of K values in `dtype`, row stride ld_x >= K elements; rows that start on 16 bytes
+ *          run faster
+ *   q      [M][K] int8 out, 16-byte aligned;   scale [M] fp32 out
+ * K a multiple of 16, 16 <= K <= 131056; 0 <= M <= 2^30.
+ */
+jscan_status jscan_quantize_rows(const void *x, int8_t *q, float *scale, int64_t M, int64_t K,
+                                 int64_t ld_x, jscan_dtype dtype, void *stream);
+
+/*
+ * Product with int8 weights, a scale for each token (row of q) and each output channel (row of w):
+ *     out[m][n] = (sum_k q[m][k] w[n][k]) * q_scale[m] * w_scale[n] + bias[n]
+ * The sum is int32 on the matrix cores and exact; scales and bias are applied in fp32 and the result
+ * is rounded once to `dtype`.
+ *   q [M][K], w [N][K]   int8, 16-byte aligned;   q_scale [M], w_scale [N] fp32
+ *   bias                 [N] fp32 or NULL
+ *   out                  M rows of N values in `dtype`, row stride ld_out >= N elements
+ * K a multiple of 16, 16 <= K <= 131056; 0 <= M <= 2^30; 0 <= N <= 2^24 (at most 2^30 tiles of 16 x 16).
+ */
+jscan_status jscan_matmul_i8(const int8_t *q, const float *q_scale, const int8_t *w,
+                             const float *w_scale, const float *bias, void *out, int64_t M, int64_t N,
+                             int64_t K, int64_t ld_out, jscan_dtype dtype, void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *jscan_status_string(jscan_status s);
 

@@ -64,11 +64,20 @@ def library():
                                                  i32, i32, vp]
     lib.jscan_step_mimo_trapezoid.argtypes = [fp, vp, vp, vp, vp, vp, fp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64,
                                               i64, i32, i32, vp]
+    lib.jscan_gated_scan.argtypes = [vp, vp, fp, vp, vp, fp, i64, i64, i64, i64, i64, i64, vp, i64, i32, i32, vp]
+    lib.jscan_gated_scan_backward.argtypes = [vp, vp, vp, vp, fp, fp, vp, vp, vp, fp, i64, i64, i64, i64, i64, i64, i64,
+                                              i64, i64, vp, i64, i32, i32, vp]
+    lib.jscan_gated_step.argtypes = [fp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i32, vp]
+    lib.jscan_gated_scan_workspace.argtypes = [i64, i64, i64]
+    lib.jscan_gated_scan_workspace.restype = i64
+    lib.jscan_quantize_rows.argtypes = [vp, vp, fp, i64, i64, i64, i32, vp]
+    lib.jscan_matmul_i8.argtypes = [vp, fp, vp, fp, fp, vp, i64, i64, i64, i64, i32, vp]
     lib.jscan_prefill_chunked_workspace.restype = i64
     for f in (lib.jscan_prefill, lib.jscan_prefill_resume, lib.jscan_step, lib.jscan_prefill_chunked,
               lib.jscan_prefill_scalar_a, lib.jscan_step_scalar_a, lib.jscan_prefill_complex, lib.jscan_step_complex,
               lib.jscan_prefill_trapezoid, lib.jscan_step_trapezoid, lib.jscan_prefill_mimo, lib.jscan_step_mimo,
-              lib.jscan_prefill_mimo_trapezoid, lib.jscan_step_mimo_trapezoid):
+              lib.jscan_prefill_mimo_trapezoid, lib.jscan_step_mimo_trapezoid, lib.jscan_gated_scan,
+              lib.jscan_gated_scan_backward, lib.jscan_gated_step, lib.jscan_quantize_rows, lib.jscan_matmul_i8):
         f.restype = i32
     lib.jscan_status_string.argtypes = [i32]
     lib.jscan_status_string.restype = ctypes.c_char_p
@@ -542,3 +551,194 @@ def step_mimo(h, x_t, delta_t, A, B_t, C_t, form="diagonal", y_t=None, _trap=Non
                                                _DTYPES[x_t.dtype], _stream(h.device))
     _check(st)
     return y_t
+
+
+# ---- gated recurrence ------------------------------------------------------------------------
+# jscan_gate_form values: how the gate makes the decay.
+GATE_FORMS = {"decay": 0, "sigmoid": 1}
+
+
+def _token_rows(name, t, like, shape):
+    """The token stride in elements of a [batch, L, D] tensor whose rows are contiguous and evenly
+    spaced (contiguous, or a slice of a wider last dimension)."""
+    _require(t.shape == shape, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _require(t.dtype == like.dtype and t.device == like.device, f"{name} must be {like.dtype} on {like.device}")
+    batch, L, D = shape
+    s_b, s_t, s_d = t.stride()
+    _require(s_d == 1 or D <= 1, f"{name} rows must be contiguous")
+    if L > 1:
+        _require(batch <= 1 or s_b == L * s_t, f"{name}: sequences must follow each other at the token stride")
+        return s_t
+    return s_b if batch > 1 else D
+
+
+def _check_state(name, t, batch, D, dev):
+    _require(t is None or (t.shape == (batch, D) and t.dtype == torch.float32 and t.device == dev
+                           and t.is_contiguous()), f"{name} must be a contiguous fp32 [batch, D] tensor on g's device")
+
+
+def _check_gated(g, form, lengths):
+    _require(form in GATE_FORMS, f"form must be one of {tuple(GATE_FORMS)}")
+    _require(g.is_cuda, "inputs must be CUDA (HIP) tensors")
+    _require(g.dtype in _DTYPES, "g must be bfloat16 or float32")
+    _require(g.dim() == 3, "g must be [batch, L, D]")
+    _require(lengths is None or (lengths.shape == (g.shape[0],) and lengths.dtype == torch.int32
+                                 and lengths.device == g.device and lengths.is_contiguous()),
+             "lengths must be a contiguous int32 [batch] tensor on g's device")
+
+
+def gated_scan_workspace_bytes(batch: int, L: int, D: int) -> int:
+    """Bytes of workspace ``gated_scan`` and ``gated_scan_backward`` need (0 for most shapes)."""
+    n = library().jscan_gated_scan_workspace(batch, L, D)
+    if n < 0:
+        raise ValueError(f"invalid shape: batch={batch} L={L} D={D}")
+    return n
+
+
+def _gated_workspace(workspace, batch, L, D, dev):
+    need = gated_scan_workspace_bytes(batch, L, D)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace, (0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, workspace=None):
+    """Gated recurrence over whole sequences (``jscan_gated_scan``).  g, u ``[batch, L, D]`` (bf16 or
+    fp32; rows may be slices of a wider projection): ``h_t = a h_{t-1} + u_t`` with ``a = exp(g_t)``
+    (form "decay"), or ``h_t = a h_{t-1} + (1 - a) u_t`` with ``a = sigmoid(g_t)`` (form "sigmoid").  h0
+    ``[batch, D]`` fp32; ``lengths`` int32 ``[batch]`` for padded sequences (y is zero in the padding).
+    Returns ``(y [batch, L, D] in g's dtype, h_final [batch, D] fp32)``; ``h_final`` may be ``h0``."""
+    _check_gated(g, form, lengths)
+    batch, L, D = g.shape
+    dev = g.device
+    ld_g, ld_u = _token_rows("g", g, g, g.shape), _token_rows("u", u, g, g.shape)
+    _check_state("h0", h0, batch, D, dev)
+    _check_state("h_final", h_final, batch, D, dev)
+    if y is None:
+        y = torch.empty((batch, L, D), dtype=g.dtype, device=dev)
+    ld_y = _token_rows("y", y, g, g.shape)
+    if h_final is None:
+        h_final = torch.empty((batch, D), dtype=torch.float32, device=dev)
+    workspace, ws_bytes = _gated_workspace(workspace, batch, L, D, dev)
+    lib = library()
+    with torch.cuda.device(dev):
+        st = lib.jscan_gated_scan(_ptr(g), _ptr(u), _ptr(h0), _ptr(lengths), _ptr(y), _ptr(h_final), batch, L, D, ld_g,
+                                  ld_u, ld_y, _ptr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype],
+                                  _stream(dev))
+    _check(st)
+    return y, h_final
+
+
+def gated_scan_backward(g, u, y, dy, h0=None, dh_final=None, lengths=None, form="decay", dg=None, du=None, dh0=None,
+                        workspace=None):
+    """Gradients of :func:`gated_scan` (``jscan_gated_scan_backward``): g, u, h0, lengths and form as given
+    to it, y as it returned, dy ``[batch, L, D]`` and optionally dh_final ``[batch, D]`` fp32 the gradients of
+    its results.  The decay form does not read u (it may be None).  Returns ``(dg, du, dh0)``; dg and du
+    may be given as the halves of one wider gradient."""
+    _check_gated(g, form, lengths)
+    batch, L, D = g.shape
+    dev = g.device
+    _require(u is not None or form == "decay", "u is needed by the sigmoid form")
+    ld_g, ld_y, ld_dy = (_token_rows(n, t, g, g.shape) for n, t in (("g", g), ("y", y), ("dy", dy)))
+    ld_u = D if u is None else _token_rows("u", u, g, g.shape)
+    for name, t in (("h0", h0), ("dh_final", dh_final), ("dh0", dh0)):
+        _check_state(name, t, batch, D, dev)
+    dg = torch.empty((batch, L, D), dtype=g.dtype, device=dev) if dg is None else dg
+    du = torch.empty((batch, L, D), dtype=g.dtype, device=dev) if du is None else du
+    ld_dg, ld_du = _token_rows("dg", dg, g, g.shape), _token_rows("du", du, g, g.shape)
+    dh0 = torch.empty((batch, D), dtype=torch.float32, device=dev) if dh0 is None else dh0
+    workspace, ws_bytes = _gated_workspace(workspace, batch, L, D, dev)
+    lib = library()
+    with torch.cuda.device(dev):
+        st = lib.jscan_gated_scan_backward(_ptr(g), _ptr(u), _ptr(y), _ptr(dy), _ptr(h0), _ptr(dh_final), _ptr(lengths),
+                                           _ptr(dg), _ptr(du), _ptr(dh0), batch, L, D, ld_g, ld_u, ld_y, ld_dy, ld_dg,
+                                           ld_du, _ptr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype],
+                                           _stream(dev))
+    _check(st)
+    return dg, du, dh0
+
+
+def gated_step(h, g_t, u_t, y_t=None, form="decay"):
+    """One decode token of the gated recurrence (``jscan_gated_step``): h ``[batch, D]`` fp32 is updated in
+    place; g_t, u_t ``[batch, D]`` may be strided views, e.g. ``g[:, t]``.  Returns y_t ``[batch, D]``."""
+    _require(form in GATE_FORMS, f"form must be one of {tuple(GATE_FORMS)}")
+    _require(h.is_cuda and h.dtype == torch.float32 and h.dim() == 2 and h.is_contiguous(),
+             "h must be a contiguous fp32 [batch, D] CUDA tensor")
+    batch, D = h.shape
+    _require(g_t.dtype in _DTYPES, "g_t must be bfloat16 or float32")
+    lds = []
+    for name, t in (("g_t", g_t), ("u_t", u_t)):
+        _require(t.shape == h.shape and t.dtype == g_t.dtype and t.device == h.device,
+                 f"{name} must be {tuple(h.shape)} of dtype {g_t.dtype} on {h.device}")
+        _require(D <= 1 or t.stride(1) == 1, f"{name} rows must be contiguous")
+        lds.append(t.stride(0) if batch > 1 else D)
+    y_t, ld_y = _step_output(y_t, (batch, D), g_t.dtype, h.device)
+    lib = library()
+    with torch.cuda.device(h.device):
+        st = lib.jscan_gated_step(_ptr(h), _ptr(g_t), _ptr(u_t), _ptr(y_t), batch, D, lds[0], lds[1], ld_y,
+                                  GATE_FORMS[form], _DTYPES[g_t.dtype], _stream(h.device))
+    _check(st)
+    return y_t
+
+
+# ---- int8 projection -------------------------------------------------------------------------
+
+
+def _row_stride(name, t):
+    """The stride in elements of the rows of ``[..., K]``: contiguous rows, evenly spaced over all leading
+    dimensions (contiguous, or a slice of a wider last dimension)."""
+    K = t.shape[-1]
+    _require(K <= 1 or t.stride(-1) == 1, f"{name} rows must be contiguous")
+    lead = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
+    for (_, outer), (n, inner) in zip(lead, lead[1:]):
+        _require(outer == n * inner or t.numel() == 0, f"{name} rows must be evenly spaced")
+    return lead[-1][1] if lead and t.numel() else K
+
+
+def quantize_rows(x, q=None, scale=None):
+    """Rows of x ``[..., K]`` (bf16 or fp32, K a multiple of 16; a slice of a wider tensor too) to int8, each
+    with a scale of its own (``jscan_quantize_rows``).  Returns ``(q [..., K] int8, scale [...] fp32)``: the
+    first input of :func:`matmul_i8`."""
+    _require(x.is_cuda and x.dtype in _DTYPES, "x must be a bfloat16 or float32 CUDA tensor")
+    _require(x.dim() >= 1, "x must have a last dimension")
+    K, lead = x.shape[-1], x.shape[:-1]
+    ld_x = _row_stride("x", x)
+    M = lead.numel()
+    q = torch.empty(x.shape, dtype=torch.int8, device=x.device) if q is None else q
+    scale = torch.empty(lead, dtype=torch.float32, device=x.device) if scale is None else scale
+    for name, t, shape, dt in (("q", q, x.shape, torch.int8), ("scale", scale, lead, torch.float32)):
+        _require(t.shape == shape and t.dtype == dt and t.device == x.device and t.is_contiguous(),
+                 f"{name} must be a contiguous {dt} tensor of shape {tuple(shape)} on x's device")
+    with torch.cuda.device(x.device):
+        st = library().jscan_quantize_rows(_ptr(x), _ptr(q), _ptr(scale), M, K, ld_x, _DTYPES[x.dtype],
+                                           _stream(x.device))
+    _check(st)
+    return q, scale
+
+
+def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloat16):
+    """``out = (q @ w.T) * q_scale * w_scale + bias`` from int8 q ``[..., K]`` and w ``[N, K]`` with fp32 scales
+    ``[...]`` (a token each) and ``[N]`` (an output channel each) and an optional fp32 bias ``[N]``
+    (``jscan_matmul_i8``).  Returns out ``[..., N]`` in out_dtype; a given ``out`` may be a slice of a wider
+    tensor."""
+    _require(q.is_cuda and q.dtype == torch.int8 and q.is_contiguous() and q.dim() >= 1,
+             "q must be a contiguous int8 CUDA tensor")
+    K, lead, dev = q.shape[-1], q.shape[:-1], q.device
+    _require(w.dim() == 2 and w.shape[1] == K and w.dtype == torch.int8 and w.is_contiguous() and w.device == dev,
+             f"w must be a contiguous int8 [N, {K}] tensor on q's device")
+    N, M = w.shape[0], lead.numel()
+    for name, t, shape in (("q_scale", q_scale, lead), ("w_scale", w_scale, (N,)), ("bias", bias, (N,))):
+        _require((t is None and name == "bias") or (t.shape == shape and t.dtype == torch.float32 and t.device == dev
+                                                    and t.is_contiguous()),
+                 f"{name} must be a contiguous fp32 tensor of shape {tuple(shape)} on q's device")
+    if out is None:
+        _require(out_dtype in _DTYPES, "out_dtype must be bfloat16 or float32")
+        out = torch.empty((*lead, N), dtype=out_dtype, device=dev)
+    _require(out.dtype in _DTYPES and out.shape == (*lead, N) and out.device == dev,
+             f"out must be a bfloat16 or float32 tensor of shape {(*lead, N)} on q's device")
+    ld_out = _row_stride("out", out)
+    with torch.cuda.device(dev):
+        st = library().jscan_matmul_i8(_ptr(q), _ptr(q_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(out), M, N, K,
+                                       ld_out, _DTYPES[out.dtype], _stream(dev))
+    _check(st)
+    return out

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "../../include/jscan.h"
+#include "host_common.h"
 #include "prefill_lane_kernel.h"
 #include "prefill_rows_kernel.h"
 #include "chunk_carry_kernel.h"
@@ -16,42 +17,12 @@
 #include "mimo_kernels.h"
 #include "prefill_mimo_rows_kernel.h"
 
+thread_local int jscan::host::g_last_hip_error = 0;
+using namespace jscan::host;
+
 namespace {
 
-thread_local int g_last_hip_error = 0;
-
-struct Span {
-    uintptr_t lo = 0, hi = 0;  // [lo, hi), empty when lo == hi
-};
-
-Span span(const void *p, int64_t bytes) {
-    Span s;
-    if (p && bytes > 0) {
-        s.lo = reinterpret_cast<uintptr_t>(p);
-        s.hi = s.lo + static_cast<uintptr_t>(bytes);
-    }
-    return s;
-}
-
-bool overlaps(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t elem_bytes(jscan_dtype dt) { return dt == JSCAN_BF16 ? 2 : 4; }
-
-jscan_status launch_status() {
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) {
-        g_last_hip_error = static_cast<int>(e);
-        return JSCAN_ERR_HIP;
-    }
-    return JSCAN_OK;
-}
-
 // ---- prefill ----------------------------------------------------------------------------
-
-// Largest grid the launchers accept (work-group counts and row indices are 32-bit ints).
-constexpr int64_t kMaxBlocks = (int64_t)1 << 30;
 
 // Scans `nrows` rows (see Segments) with the row-mapped kernel when it applies, otherwise
 // with one lane per (row, channel).  AF: the form of A; kTrap: the trapezoidal rule (inputs tr).

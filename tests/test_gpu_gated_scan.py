@@ -1,0 +1,337 @@
+"""The gated recurrence on the GPU (scan, backward pass, decode step) against the fp64 oracle.
+
+Tolerances come from the oracle's running error analysis of an fp32 evaluation (oracle/gated.py), element
+by element, plus half a step of the output type: torch.finfo(dtype).eps / 2 of the value."""
+import numpy as np
+import pytest
+import torch
+
+import mamba_selective_scan_03_amd as jscan
+from gpu_util import bits, f64, say
+from oracle import gated as O
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+TINY = 1e-30   # results below fp32's normal range may be flushed to zero
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def make(batch, L, D, dtype, form, seed, memory="mixed"):
+    r = torch.Generator().manual_seed(seed)
+    z = torch.randn(batch, L, D, generator=r)
+    rate = torch.exp(torch.rand(D, generator=r) * 6 - 7)
+    if memory == "long":     # decays within about 1e-4 of one
+        rate = torch.full((D,), 1e-4)
+    g = -rate * torch.exp(z) if form == "decay" else (2 + 1.5 * z if memory == "mixed" else 9 + z)
+    u, dy = torch.randn(batch, L, D, generator=r), torch.randn(batch, L, D, generator=r)
+    h0, dh = torch.randn(batch, D, generator=r), torch.randn(batch, D, generator=r)
+    return [v.to(DT[dtype]).cuda() for v in (g, u, dy)] + [h0.cuda(), dh.cuda()]
+
+
+def assert_within(got, want, bound, dtype, what):
+    got = f64(got)
+    tol = bound + half_step(dtype) * (np.abs(want) + bound) + TINY
+    bad = ~(np.abs(got - want) <= tol)
+    if bad.any():
+        i = tuple(np.argwhere(bad)[0])
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.size} outside, first at {i}: {got[i]} against {want[i]}, "
+                             f"tolerance {tol[i]}")
+
+
+def check(g, u, dy, h0, dh, form, lengths=None):
+    """Scan, then backward from the scan's own y, both against the oracle (backward: from that y)."""
+    y, h = jscan.gated_scan(g, u, h0=h0, lengths=lengths, form=form)
+    dg, du, dh0 = jscan.gated_scan_backward(g, u, y, dy, h0=h0, dh_final=dh, lengths=lengths, form=form)
+    want_y, want_h = O.scan(g, u, h0, lengths, form)
+    E, _ = O.scan_error(g, u, h0, lengths, form)
+    assert_within(y, want_y, E, y.dtype, "y")
+    if g.shape[1]:
+        n = np.full(g.shape[0], g.shape[1]) if lengths is None else np.clip(f64(lengths).astype(int), 0, g.shape[1])
+        Eh = np.where((n > 0)[:, None], E[np.arange(len(n)), np.maximum(n, 1) - 1], 0.0)
+    else:
+        Eh = np.zeros(h.shape)
+    assert_within(h, want_h, Eh, torch.float32, "h_final")
+    dg_w, du_w, dh0_w, _ = O.backward(g, u, y, dy, h0, dh, lengths, form)
+    Eg, Eu, E0 = O.backward_error(g, u, y, dy, h0, dh, lengths, form)
+    assert_within(dg, dg_w, Eg, dg.dtype, "dg")
+    assert_within(du, du_w, Eu, du.dtype, "du")
+    assert_within(dh0, dh0_w, E0, torch.float32, "dh0")
+    return y, h, dg, du, dh0
+
+
+@pytest.mark.parametrize("form", ["decay", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("batch,L,D", [
+    (1, 1, 1), (1, 2, 3), (2, 3, 64), (1, 15, 7), (3, 16, 130), (2, 17, 33), (1, 31, 127), (1, 64, 128), (2, 65, 129),
+    (1, 255, 66), (1, 256, 32), (2, 257, 31), (1, 300, 1000), (5, 77, 257), (1, 1025, 96), (40, 5, 1024),
+    (300, 3, 260), (1, 4099, 34),
+])
+def test_scan_and_backward_match_the_oracle(batch, L, D, dtype, form):
+    check(*make(batch, L, D, dtype, form, 1000 * L + D), form)
+
+
+@pytest.mark.parametrize("form", ["decay", "sigmoid"])
+@pytest.mark.parametrize("dtype,batch,L,D", [
+    ("bf16", 1, 20000, 64), ("f32", 1, 9001, 48), ("bf16", 2, 6001, 250), ("f32", 1, 12345, 17), ("bf16", 1, 2049, 2048),
+])
+@pytest.mark.parametrize("memory", ["mixed", "long"])
+def test_long_sequences_match_the_oracle(dtype, batch, L, D, form, memory):
+    check(*make(batch, L, D, dtype, form, L + D, memory), form)
+
+
+@pytest.mark.parametrize("form", ["decay", "sigmoid"])
+@pytest.mark.parametrize("dtype,batch,L,D,lengths", [
+    ("f32", 4, 20, 40, [0, 1, 20, 7]), ("bf16", 3, 513, 66, [512, 0, 513]), ("bf16", 2, 9000, 64, [8191, 4500]),
+    ("f32", 3, 3000, 24, [2999, 1, 0]), ("bf16", 2, 300, 31, [-5, 1000]), ("bf16", 70, 33, 128, None),
+    ("f32", 1, 5000, 16, [0]),
+])
+def test_padded_batches(dtype, batch, L, D, lengths, form):
+    """Padding holds NaN in every input and is neither read nor left unwritten."""
+    g, u, dy, h0, dh = make(batch, L, D, dtype, form, 5 * L + D)
+    n = torch.tensor([(7 * b) % (L + 1) for b in range(batch)] if lengths is None else lengths, dtype=torch.int32).cuda()
+    for b in range(batch):
+        for t in (g, u, dy):
+            t[b, max(0, min(L, int(n[b]))):] = float("nan")
+    y, h, dg, du, dh0 = check(*(torch.nan_to_num(t) for t in (g, u, dy)), h0, dh, form, n)
+    y2, h2 = jscan.gated_scan(g, u, h0=h0, lengths=n, form=form)
+    dg2, du2, dh02 = jscan.gated_scan_backward(g, u, y2, dy, h0=h0, dh_final=dh, lengths=n, form=form)
+    for a, b in ((y, y2), (h, h2), (dg, dg2), (du, du2), (dh0, dh02)):
+        assert torch.equal(bits(a), bits(b))
+
+
+@pytest.mark.parametrize("form", ["decay", "sigmoid"])
+def test_without_starting_state_or_final_gradient(form):
+    g, u, dy, h0, dh = make(2, 700, 72, "f32", form, 3)
+    y, h = jscan.gated_scan(g, u, form=form)
+    y0, hz = jscan.gated_scan(g, u, h0=torch.zeros_like(h0), form=form)
+    assert torch.equal(bits(y), bits(y0)) and torch.equal(bits(h), bits(hz))
+    got = jscan.gated_scan_backward(g, u, y, dy, form=form)
+    want = jscan.gated_scan_backward(g, u, y, dy, h0=torch.zeros_like(h0), dh_final=torch.zeros_like(h0), form=form)
+    for a, b in zip(got, want):
+        assert torch.equal(bits(a), bits(b))
+
+
+@pytest.mark.parametrize("L", [0, 1, 40, 6000])
+@pytest.mark.parametrize("form", ["decay", "sigmoid"])
+def test_states_in_place(L, form):
+    """h_final over h0 and dh0 over dh_final; a sequence without tokens passes both through."""
+    g, u, dy, h0, dh = make(2, L, 40, "bf16", form, 8)
+    y, h = jscan.gated_scan(g, u, h0=h0, form=form)
+    dg, du, dh0 = jscan.gated_scan_backward(g, u, y, dy, h0=h0, dh_final=dh, form=form)
+    if L == 0:
+        assert torch.equal(h, h0) and torch.equal(dh0, dh)
+    s, ds = h0.clone(), dh.clone()
+    y2, h2 = jscan.gated_scan(g, u, h0=s, h_final=s, form=form)
+    dg2, du2, dh02 = jscan.gated_scan_backward(g, u, y, dy, h0=h0, dh_final=ds, dh0=ds, form=form)
+    assert h2 is s and dh02 is ds
+    for a, b in ((y, y2), (h, s), (dg, dg2), (du, du2), (dh0, ds)):
+        assert torch.equal(bits(a), bits(b))
+
+
+@pytest.mark.parametrize("dtype,L,D,pad", [("bf16", 700, 66, 0), ("bf16", 700, 33, 1), ("f32", 3000, 50, 6), ("bf16", 9000, 128, 2)])
+def test_strided_halves_and_guard_columns(dtype, L, D, pad):
+    """g and u, dg and du as column ranges of wider buffers, off the 4-byte grid too: the same bits as
+    contiguous tensors, and nothing written beside the ranges."""
+    g, u, dy, h0, dh = make(2, L, D, dtype, "sigmoid", 21)
+    y, h = jscan.gated_scan(g, u, h0=h0, form="sigmoid")
+    want = jscan.gated_scan_backward(g, u, y, dy, h0=h0, dh_final=dh, form="sigmoid")
+    wide = torch.full((2, L, 2 * D + 3 * pad), 9.0, dtype=g.dtype, device="cuda")
+    lo, hi = slice(pad, pad + D), slice(D + 2 * pad, 2 * D + 2 * pad)
+    wide[..., lo], wide[..., hi] = g, u
+    out, grads = torch.full_like(wide, 7.0), torch.full_like(wide, 7.0)
+    y2, h2 = jscan.gated_scan(wide[..., lo], wide[..., hi], h0=h0, form="sigmoid", y=out[..., hi])
+    got = jscan.gated_scan_backward(wide[..., lo], wide[..., hi], out[..., hi], dy, h0=h0, dh_final=dh, form="sigmoid",
+                                    dg=grads[..., lo], du=grads[..., hi])
+    # another vector width may join segments in another order, so against the oracle's bound, not bit for bit
+    E, _ = O.scan_error(g, u, h0, None, "sigmoid")
+    assert_within(y2, O.scan(g, u, h0, None, "sigmoid")[0], E, y2.dtype, "strided y")
+    Eg, Eu, E0 = O.backward_error(g, u, y2, dy, h0, dh, None, "sigmoid")
+    w = O.backward(g, u, y2, dy, h0, dh, None, "sigmoid")
+    for a, b, e, t in zip(got, w, (Eg, Eu, E0), (g.dtype, g.dtype, torch.float32)):
+        assert_within(a, b, e, t, "strided gradient")
+    assert len(want) == 3 and torch.isfinite(h2).all()
+    keep = torch.ones(2 * D + 3 * pad, dtype=torch.bool, device="cuda")
+    keep[hi] = False
+    assert (out[..., keep] == 7.0).all()
+    keep[lo] = False
+    assert (grads[..., keep] == 7.0).all()
+
+
+@pytest.mark.parametrize("form", ["decay", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_and_extreme_gates(form, dtype):
+    """-inf and the type's lowest value drop the state exactly; the sigmoid's +inf and largest value keep it
+    exactly; a NaN stays in its channel and its sequence."""
+    g, u, dy, h0, dh = make(2, 400, 24, dtype, form, 31)
+    low, high = torch.finfo(g.dtype).min, torch.finfo(g.dtype).max
+    g[0, 100], g[0, 250, ::2], g[1, 0] = -float("inf"), low, low
+    if form == "sigmoid":
+        g[1, 50:60], g[1, 300] = float("inf"), high
+    y, h, dg, du, dh0 = check(g, u, dy, h0, dh, form)
+    tail, _ = jscan.gated_scan(g[:1, 100:].contiguous(), u[:1, 100:].contiguous(), form=form)
+    assert_within(y[:1, 100:], f64(tail), O.scan_error(g[:1, 100:], u[:1, 100:], None, None, form)[0] * 2
+                  + half_step(g.dtype) * np.abs(f64(tail)), g.dtype, "after a reset")
+    assert not dh0[1].any() and not dg[0, 100].any() and not dg[1, 0].any()
+    g2 = g.clone()
+    g2[1, 200, 5] = float("nan")
+    y2, h2 = jscan.gated_scan(g2, u, h0=h0, form=form)
+    same = torch.ones_like(y2, dtype=torch.bool)
+    same[1, 200:, 5] = False
+    assert torch.isnan(y2[1, 200:, 5]).all() and torch.isnan(h2[1, 5])
+    assert torch.equal(bits(y2)[same.cpu()], bits(y)[same.cpu()])
+
+
+@pytest.mark.parametrize("form", ["decay", "sigmoid"])
+@pytest.mark.parametrize("dtype,batch,D,stride", [("bf16", 1, 1, 0), ("bf16", 3, 64, 0), ("f32", 5, 129, 3), ("bf16", 257, 1000, 0),
+                                                  ("bf16", 7, 33, 1), ("f32", 1, 8192, 0), ("bf16", 64, 4096, 8)])
+def test_step_matches_the_oracle(dtype, batch, D, stride, form):
+    g, u, _, h0, _ = make(batch, 1, D + stride, dtype, form, 7)
+    g, u, h0 = g[:, 0, :D], u[:, 0, :D], h0[:, :D].contiguous()
+    h = h0.clone()
+    y = jscan.gated_step(h, g, u, form=form)
+    want, _ = O.scan(g[:, None], u[:, None], h0, None, form)
+    E, _ = O.scan_error(g[:, None], u[:, None], h0, None, form)
+    assert_within(y, want[:, 0], E[:, 0], y.dtype, "y_t")
+    assert_within(h, want[:, 0], E[:, 0], torch.float32, "h")
+    out = torch.full((batch, 2, D), 5.0, dtype=y.dtype, device="cuda")
+    h2 = h0.clone()
+    jscan.gated_step(h2, g, u, y_t=out[:, 1], form=form)
+    assert torch.equal(bits(out[:, 1]), bits(y)) and (out[:, 0] == 5).all() and torch.equal(bits(h2), bits(h))
+
+
+@pytest.mark.parametrize("form", ["decay", "sigmoid"])
+def test_prefill_then_decode_steps(form):
+    """A prompt through the scan, then tokens through the step: the states of one longer scan."""
+    g, u, _, h0, _ = make(3, 1100, 200, "bf16", form, 13)
+    y, h = jscan.gated_scan(g, u, h0=h0, form=form)
+    E, _ = O.scan_error(g, u, h0, None, form)
+    want, want_h = O.scan(g, u, h0, None, form)
+    _, s = jscan.gated_scan(g[:, :1090].contiguous(), u[:, :1090].contiguous(), h0=h0, form=form)
+    for t in range(1090, 1100):
+        y_t = jscan.gated_step(s, g[:, t], u[:, t], form=form)
+        assert_within(y_t, want[:, t], E[:, t], y_t.dtype, f"token {t}")
+    assert_within(s, want_h, E[:, -1], torch.float32, "state")
+    assert_within(h, want_h, E[:, -1], torch.float32, "state of the scan")
+
+
+@pytest.mark.parametrize("dtype,batch,L,D", [("f32", 2, 50, 40), ("bf16", 1, 30000, 128), ("bf16", 64, 300, 1024)])
+def test_two_runs_give_the_same_bits(dtype, batch, L, D):
+    g, u, dy, h0, dh = make(batch, L, D, dtype, "decay", 17)
+    runs = []
+    for _ in range(3):
+        y, h = jscan.gated_scan(g, u, h0=h0)
+        runs.append((y, h, *jscan.gated_scan_backward(g, None, y, dy, h0=h0, dh_final=dh)))
+    for r in runs[1:]:
+        for a, b in zip(runs[0], r):
+            assert torch.equal(bits(a), bits(b))
+
+
+def test_offsets_beyond_32_bits():
+    """Column ranges of a buffer of more than 2^32 elements, far sequences at far offsets."""
+    batch, L, D, wide = 3, 1500, 72, 1 << 20
+    g, u, dy, h0, dh = make(batch, L, D, "bf16", "decay", 19)
+    buf = torch.empty((batch, L, wide), dtype=torch.bfloat16, device="cuda")
+    lo, hi = slice(8, 8 + D), slice(wide - D, wide)
+    buf[..., lo], buf[..., hi] = g, u
+    y, h = jscan.gated_scan(g, u, h0=h0)
+    y2, h2 = jscan.gated_scan(buf[..., lo], buf[..., hi], h0=h0)
+    assert torch.equal(bits(y), bits(y2)) and torch.equal(bits(h), bits(h2))
+    want = jscan.gated_scan_backward(g, u, y, dy, h0=h0, dh_final=dh)
+    got = jscan.gated_scan_backward(buf[..., lo], None, y, dy, h0=h0, dh_final=dh, dg=buf[..., lo.start + 2 * D:lo.stop + 2 * D],
+                                    du=buf[..., lo.start + 4 * D:lo.stop + 4 * D])
+    for a, b in zip(want, got):
+        assert torch.equal(bits(a), bits(b))
+
+
+def _layer(g, u, dy, h0, dh, form, ws):
+    y, h = jscan.gated_scan(g, u, h0=h0, form=form, workspace=ws)
+    return (y, h, *jscan.gated_scan_backward(g, u, y, dy, h0=h0, dh_final=dh, form=form, workspace=ws))
+
+
+@pytest.mark.parametrize("batch,L,D", [(2, 130, 72), (1, 20000, 64)])
+def test_captured_and_replayed(batch, L, D):
+    """Scan and backward in one graph, sharing one workspace in stream order, between eager runs."""
+    args = make(batch, L, D, "bf16", "sigmoid", 23)
+    ws = torch.empty(max(16, jscan.gated_scan_workspace_bytes(batch, L, D)), dtype=torch.uint8, device="cuda")
+    eager = _layer(*args, "sigmoid", None)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _layer(*args, "sigmoid", ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = _layer(*args, "sigmoid", ws)
+    for replay in range(4):
+        for t in out:
+            t.fill_(float("nan"))
+        ws.fill_(0xFF if replay % 2 else 0)
+        torch.cuda.synchronize()
+        graph.replay()
+        again = _layer(*args, "sigmoid", None)
+        torch.cuda.synchronize()
+        for a, b, c in zip(out, eager, again):
+            assert torch.equal(bits(a), bits(b)) and torch.equal(bits(a), bits(c)), f"replay {replay}"
+
+
+def test_calls_on_other_streams():
+    args = [make(1, 9000, 96, "bf16", "decay", s) for s in (41, 42, 43)]
+    want = [_layer(*a, "decay", None) for a in args]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in args], []
+    for a, s in zip(args, streams):
+        with torch.cuda.stream(s):
+            got.append(_layer(*a, "decay", None))
+    torch.cuda.synchronize()
+    for x, y in zip(want, got):
+        for a, b in zip(x, y):
+            assert torch.equal(bits(a), bits(b))
+
+
+def test_gradients_match_differences_of_the_gpu_scan():
+    """Directional differences of the fp32 scan's own loss.  With 300 x 40 values of order one the loss's
+    fp32 noise is below 1e-5 * sqrt(12000) ~ 1e-3 absolute (summed in fp64 from y's 2^-24 roundings), the step
+    2^-6 divides it, and the second-order term of a central difference is 2^-12 relative."""
+    for form in ("decay", "sigmoid"):
+        g, u, dy, h0, dh = make(1, 300, 40, "f32", form, 51)
+        y, h = jscan.gated_scan(g, u, h0=h0, form=form)
+        dg, du, dh0 = jscan.gated_scan_backward(g, u, y, dy, h0=h0, dh_final=dh, form=form)
+
+        def loss(g, u, h0):
+            y, h = jscan.gated_scan(g, u, h0=h0, form=form)
+            return float((y.double() * dy.double()).sum() + (h.double() * dh.double()).sum())
+
+        eps = 2.0 ** -6
+        for k, grad in ((0, dg), (1, du), (2, dh0)):
+            v = torch.randn(grad.shape, generator=torch.Generator().manual_seed(k)).cuda() * (g.abs() if k == 0 else 1)
+            at = [g, u, h0]
+            up, dn = [list(at) for _ in range(2)]
+            up[k], dn[k] = at[k] + eps * v, at[k] - eps * v
+            num = (loss(*up) - loss(*dn)) / (2 * eps)
+            ana = float((grad.double() * v.double()).sum())
+            scale = float((grad.double() * v.double()).abs().sum())
+            say(f"{form} argument {k}: {num:.6g} against {ana:.6g}")
+            assert abs(num - ana) <= 1e-3 / (2 * eps) + 2.0 ** -9 * scale
+
+
+def test_binding_refusals_on_the_gpu():
+    g, u, dy, h0, dh = make(2, 6, 8, "bf16", "decay", 1)
+    bad = [dict(u=u.float()), dict(u=u[:, :5]), dict(h0=h0.double()), dict(h0=h0[:1]), dict(form="exp"),
+           dict(lengths=torch.tensor([1, 2]).cuda()), dict(lengths=torch.tensor([1, 2], dtype=torch.int32)),
+           dict(y=torch.empty(2, 6, 9, dtype=u.dtype, device="cuda")), dict(g=g.transpose(0, 1)), dict(g=g.half())]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            jscan.gated_scan(**{**dict(g=g, u=u, h0=h0), **kw})
+    with pytest.raises(jscan.JScanError):
+        jscan.gated_scan(g, u, y=u)
+    y, _ = jscan.gated_scan(g, u)
+    with pytest.raises(ValueError):
+        jscan.gated_scan_backward(g, None, y, dy, form="sigmoid")
+    with pytest.raises(jscan.JScanError):
+        jscan.gated_scan_backward(g, u, y, dy, dg=dy)
+    with pytest.raises(ValueError):
+        jscan.gated_step(h0, g[:, 0], u[:, 0].float())
