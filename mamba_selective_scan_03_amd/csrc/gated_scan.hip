@@ -38,33 +38,147 @@ template <int NO, int NI> bool any_overlap(const Rows (&out)[NO], const Rows (&i
     return false;
 }
 
-template <typename E> TokenRows<const typename E::store_t> in_rows(const void *p, int64_t ld) {
-    return {static_cast<const typename E::store_t *>(p), ld};
-}
-template <typename E> TokenRows<typename E::store_t> out_rows(void *p, int64_t ld) {
-    return {static_cast<typename E::store_t *>(p), ld};
+// How a call is laid out: strips of `lanes` lanes, `waves` waves a work-group, n_seg segments of seg_len tokens.
+struct Plan {
+    int lanes, waves;
+    int64_t n_seg, seg_len;
+};
+
+constexpr int kRun = 8;   // tokens a thread takes of a block
+// Work-groups that keep the chip busy: below this a strip is made narrower or the tokens are cut.  1 x 4096 x 8192 bf16
+// scan: 64-lane strips (64 work-groups) 149 us, 16-lane ones (256) 59 us.
+constexpr int64_t kEnough = 160;
+
+// Narrower strips and segments both make more work-groups.  Narrow strips read every byte once but in pieces of 64 or
+// 128 bytes a row; segments read the gate and the input twice (the maps first) in pieces of 256 bytes, with a
+// second launch.  So the widest strip that makes enough work-groups is taken, and the tokens are cut where none does.
+// The backward pass reads only two of its five or six tensors twice, so on long sequences cutting wins over narrow strips
+// (2 x 4096 x 4096 sigmoid: 94 us against 115 us; forward 65 us against 61 us).  Sequences of a few tokens take
+// few waves (256 x 8 x 4096: one wave 10.8 us, four 23 us, eight 44 us; 64 x 32 x 2048: 7.3, 5.6, 8.8 us).
+// channels: per lane.  narrow: whether the lane offsets of narrow strips fit 32 bits.
+Plan plan_for(int64_t batch, int64_t L, int64_t D, int channels, bool backward, bool narrow) {
+    auto groups = [&](int lanes) { return batch * ((D + lanes * channels - 1) / (lanes * channels)); };
+    if (L <= kRun) return {64, 1, 1, L};
+    if (L <= 4 * kRun) return {64, 4, 1, L};
+    const int widths[] = {64, 32, 16};
+    for (int lanes : widths) {
+        if (lanes < 64 && (!narrow || (backward && L >= 2048))) break;
+        if (groups(lanes) >= kEnough) return {lanes, 8, 1, L};
+    }
+    // cut: segments of at least 256 tokens, whole blocks, at most 512 work-groups (two on every CU)
+    const int lanes = !narrow || groups(64) * (L / 256) >= 256 ? 64 : 16;
+    const int64_t block = (int64_t)(64 / lanes) * 8 * kRun;
+    int64_t n = 512 / groups(lanes);
+    n = n < L / 256 ? n : L / 256;
+    if (n <= 1) return {lanes, 8, 1, L};
+    const int64_t seg = ((L + n - 1) / n + block - 1) / block * block;
+    return {lanes, 8, (L + seg - 1) / seg, seg};
 }
 
-template <typename E, GateForm F>
-jscan_status launch_scan(const void *g, const void *u, const float *h0, const int32_t *lengths, void *y,
-                         float *h_final, int64_t batch, int64_t L, int64_t D, int64_t ld_g, int64_t ld_u,
-                         int64_t ld_y, hipStream_t s) {
-    const int strips = (int)((D + 63) / 64);
-    hipLaunchKernelGGL((jscan::gated_lane_kernel<E, F>), dim3((unsigned)(batch * strips)), dim3(64), 0, s,
-                       in_rows<E>(g, ld_g), in_rows<E>(u, ld_u), h0, lengths, out_rows<E>(y, ld_y), h_final, L,
-                       (int)D, strips);
-    return launch_status();
+int64_t plan_workspace(const Plan &p, int64_t batch, int64_t D) {
+    return p.n_seg > 1 ? batch * D * (p.n_seg * 8 + 4) : 0;
 }
 
-template <typename E, GateForm F>
-jscan_status launch_backward(const void *g, const void *u, const void *y, const void *dy, const float *h0,
-                             const float *dh_final, const int32_t *lengths, void *dg, void *du, float *dh0,
-                             int64_t batch, int64_t L, int64_t D, int64_t ld_g, int64_t ld_u, int64_t ld_y,
-                             int64_t ld_dy, int64_t ld_dg, int64_t ld_du, hipStream_t s) {
-    const int strips = (int)((D + 63) / 64);
-    hipLaunchKernelGGL((jscan::gated_lane_backward_kernel<E, F>), dim3((unsigned)(batch * strips)), dim3(64), 0, s,
-                       in_rows<E>(g, ld_g), in_rows<E>(u, ld_u), in_rows<E>(y, ld_y), in_rows<E>(dy, ld_dy), h0,
-                       dh_final, lengths, out_rows<E>(dg, ld_dg), out_rows<E>(du, ld_du), dh0, L, (int)D, strips);
+jscan::SegSplit split_of(const Plan &p, int64_t batch, int64_t D, void *workspace) {
+    float2 *sums = static_cast<float2 *>(workspace);
+    return {(int)p.n_seg, p.seg_len, sums, reinterpret_cast<float *>(sums + batch * D * p.n_seg)};
+}
+
+template <typename V> TokenRows<const typename V::store_t> in_rows(Pair t) {
+    return {static_cast<const typename V::store_t *>(t.p), t.ld};
+}
+template <typename V> TokenRows<typename V::store_t> out_rows(Pair t) {
+    return {static_cast<typename V::store_t *>(const_cast<void *>(t.p)), t.ld};
+}
+
+struct ScanArgs {
+    Pair g, u, y;
+    const float *h0;
+    const int32_t *lengths;
+    float *h_final;
+    int64_t batch, L, D;
+    void *workspace;
+    hipStream_t stream;
+};
+
+struct BackwardArgs {
+    Pair g, u, y, dy, dg, du;
+    const float *h0, *dh_final;
+    const int32_t *lengths;
+    float *dh0;
+    int64_t batch, L, D;
+    void *workspace;
+    hipStream_t stream;
+};
+
+template <typename V, GateForm F, int LC, int NW, bool kRev>
+void launch_summary(Pair g, Pair x, const float *s0, const int32_t *lengths, const jscan::SegSplit &sp, int64_t batch,
+                    int64_t L, int64_t D, hipStream_t stream) {
+    const int strips = (int)((D + LC * V::n - 1) / (LC * V::n));
+    hipLaunchKernelGGL((jscan::gated_summary_kernel<V, F, LC, NW, kRun, kRev>),
+                       dim3((unsigned)(batch * strips * (sp.n_seg - 1))), dim3(NW * 64), 0, stream, in_rows<V>(g),
+                       in_rows<V>(x), s0, lengths, sp, L, (int)D, strips);
+}
+
+template <typename V, GateForm F, int LC, int NW> void launch_as(const ScanArgs &a, const Plan &p) {
+    const int strips = (int)((a.D + LC * V::n - 1) / (LC * V::n));
+    const jscan::SegSplit sp = split_of(p, a.batch, a.D, a.workspace);
+    if constexpr (NW == 8 && LC != 32) {
+        if (p.n_seg > 1)
+            launch_summary<V, F, LC, NW, false>(a.g, a.u, a.h0, a.lengths, sp, a.batch, a.L, a.D, a.stream);
+    }
+    hipLaunchKernelGGL((jscan::gated_scan_kernel<V, F, LC, NW, kRun>), dim3((unsigned)(a.batch * strips * p.n_seg)),
+                       dim3(NW * 64), 0, a.stream, in_rows<V>(a.g), in_rows<V>(a.u), a.h0, a.lengths,
+                       out_rows<V>(a.y), a.h_final, sp, a.L, (int)a.D, strips);
+}
+
+template <typename V, GateForm F, int LC, int NW> void launch_as(const BackwardArgs &a, const Plan &p) {
+    const int strips = (int)((a.D + LC * V::n - 1) / (LC * V::n));
+    const jscan::SegSplit sp = split_of(p, a.batch, a.D, a.workspace);
+    if constexpr (NW == 8 && LC != 32) {
+        if (p.n_seg > 1)
+            launch_summary<V, F, LC, NW, true>(a.g, a.dy, a.dh_final, a.lengths, sp, a.batch, a.L, a.D, a.stream);
+    }
+    hipLaunchKernelGGL((jscan::gated_backward_kernel<V, F, LC, NW, kRun>), dim3((unsigned)(a.batch * strips * p.n_seg)),
+                       dim3(NW * 64), 0, a.stream, in_rows<V>(a.g), in_rows<V>(a.u), in_rows<V>(a.y), in_rows<V>(a.dy),
+                       a.h0, a.dh_final, a.lengths, out_rows<V>(a.dg), out_rows<V>(a.du), a.dh0, sp, a.L, (int)a.D,
+                       strips);
+}
+
+template <typename V, GateForm F, typename Args> void launch_plan(const Args &a, const Plan &p) {
+    if (p.waves == 1) launch_as<V, F, 64, 1>(a, p);
+    else if (p.waves == 4) launch_as<V, F, 64, 4>(a, p);
+    else if (p.lanes == 64) launch_as<V, F, 64, 8>(a, p);
+    else if (p.lanes == 32) launch_as<V, F, 32, 8>(a, p);
+    else launch_as<V, F, 16, 8>(a, p);
+}
+
+// Whether every row of a call's tensors starts on 4 bytes and holds an even number of bf16 values.
+template <int N> bool two_channels(const Pair (&t)[N], int64_t D) {
+    if (D % 2) return false;
+    for (const Pair &r : t)
+        if (r.p && (r.ld % 2 || !aligned(r.p, 4))) return false;
+    return true;
+}
+// Whether the lane offsets of narrow strips (three runs of kRun rows, and the row itself) fit 32 bits.
+template <int N> bool narrow_ok(const Pair (&t)[N], int64_t es) {
+    for (const Pair &r : t)
+        if (r.p && r.ld * es > ((int64_t)1 << 31) / (4 * kRun)) return false;
+    return true;
+}
+
+template <typename Args, int N>
+jscan_status launch_args(const Args &a, const Pair (&t)[N], jscan_dtype dtype, jscan_gate_form form, bool backward) {
+    const bool two = dtype == JSCAN_BF16 && two_channels(t, a.D);
+    const Plan p = plan_for(a.batch, a.L, a.D, two ? 2 : 1, backward, narrow_ok(t, elem_bytes(dtype)));
+    auto with_form = [&](auto v) {
+        using V = decltype(v);
+        if (form == JSCAN_GATE_DECAY) launch_plan<V, GateForm::Decay>(a, p);
+        else launch_plan<V, GateForm::Sigmoid>(a, p);
+    };
+    if (two) with_form(jscan::Bf16x2{});
+    else if (dtype == JSCAN_BF16) with_form(jscan::Bf16x1{});
+    else with_form(jscan::F32x1{});
     return launch_status();
 }
 
@@ -93,7 +207,14 @@ extern "C" {
 
 int64_t jscan_gated_scan_workspace(int64_t batch, int64_t L, int64_t D) {
     if (!shape_ok(batch, L, D)) return -1;
-    return 0;
+    if (batch == 0 || D == 0) return 0;
+    int64_t most = 0;
+    for (int channels = 1; channels <= 2; ++channels)
+        for (int k = 0; k < 4; ++k) {
+            const int64_t n = plan_workspace(plan_for(batch, L, D, channels, k & 1, k & 2), batch, D);
+            most = n > most ? n : most;
+        }
+    return most;
 }
 
 jscan_status jscan_gated_scan(const void *g, const void *u, const float *h0, const int32_t *lengths, void *y,
@@ -117,11 +238,9 @@ jscan_status jscan_gated_scan(const void *g, const void *u, const float *h0, con
     const Rows in[] = {rows_of({g, ld_g}, tokens, D, es), rows_of({u, ld_u}, tokens, D, es),
                        flat(h0 == h_final ? nullptr : h0, state), flat(lengths, batch * 4)};
     if (any_overlap(out, in)) return JSCAN_ERR_ALIAS;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    return dispatch(dtype, form, [&](auto e, auto f) {
-        return launch_scan<decltype(e), decltype(f)::value>(g, u, h0, lengths, y, h_final, batch, L, D, ld_g, ld_u,
-                                                            ld_y, s);
-    });
+    const Pair t[] = {{g, ld_g}, {u, ld_u}, {y, ld_y}};
+    const ScanArgs a{t[0], t[1], t[2], h0, lengths, h_final, batch, L, D, workspace, static_cast<hipStream_t>(stream)};
+    return launch_args(a, t, dtype, form, false);
 }
 
 jscan_status jscan_gated_scan_backward(const void *g, const void *u, const void *y, const void *dy, const float *h0,
@@ -158,11 +277,10 @@ jscan_status jscan_gated_scan_backward(const void *g, const void *u, const void 
                        flat(h0, state),                     flat(dh_final == dh0 ? nullptr : dh_final, state),
                        flat(lengths, batch * 4)};
     if (any_overlap(out, in)) return JSCAN_ERR_ALIAS;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    return dispatch(dtype, form, [&](auto e, auto f) {
-        return launch_backward<decltype(e), decltype(f)::value>(g, u, y, dy, h0, dh_final, lengths, dg, du, dh0, batch,
-                                                                L, D, ld_g, ld_u, ld_y, ld_dy, ld_dg, ld_du, s);
-    });
+    const Pair t[] = {{g, ld_g}, {sig ? u : nullptr, ld_u}, {y, ld_y}, {dy, ld_dy}, {dg, ld_dg}, {du, ld_du}};
+    const BackwardArgs a{t[0], t[1], t[2], t[3], t[4], t[5], h0, dh_final, lengths, dh0, batch, L, D, workspace,
+                         static_cast<hipStream_t>(stream)};
+    return launch_args(a, t, dtype, form, true);
 }
 
 jscan_status jscan_gated_step(float *h, const void *g_t, const void *u_t, void *y_t, int64_t batch, int64_t D,

@@ -1,6 +1,24 @@
 // gated_scan_kernels.h - the gated recurrence over whole sequences, its backward pass and its
 // decode step (gated_update.h has the mathematics).
+//
+// Both directions are the affine scan s <- a s + x of one fp32 state per channel:
+//     forward    s = h,  x = b u,     tokens in order
+//     backward   s = c,  x = a dy,    tokens from the last to the first (c_t = a_t (dy_t + c_{t+1}))
+// They move 6 (fp32: 12) and 10 to 12 (20 to 24) bytes per element for a dozen instructions, so memory bounds
+// them: every byte should move once, and enough of them at a time, although one channel's tokens
+// depend on each other.
+//
+// Work-group: a strip of LC lanes x V::n channels over all tokens of one sequence (or of one segment of it, see
+// below).  Its S = 64 NW / LC thread rows take consecutive runs of TT tokens, a block of S TT tokens at a
+// time, and the next block's words are on their way while one block is computed:
+//   1. every thread composes its run's map s -> A s + H, keeping the maps (A_i, H_i) of its prefixes;
+//   2. the runs' maps go through LDS; a thread carries the block's starting state through the maps
+//      of the runs before its own (through lane shuffles first for the runs inside a wave);
+//   3. the states are s_i = A_i s_in + H_i, independent of each other.
+// Every order is fixed, so results repeat bit for bit.
 #pragma once
+
+#include <type_traits>
 
 #include "gated_update.h"
 
@@ -19,59 +37,567 @@ __device__ __forceinline__ int64_t tokens_of(const int32_t *lengths, int64_t b, 
     return n < 0 ? 0 : (n > L ? L : n);
 }
 
-// One lane per (sequence, channel), tokens in order.
-template <typename E, GateForm F>
-__global__ __launch_bounds__(64) void gated_lane_kernel(TokenRows<const typename E::store_t> g,
-                                                        TokenRows<const typename E::store_t> u,
-                                                        const float *__restrict__ h0,
-                                                        const int32_t *__restrict__ lengths,
-                                                        TokenRows<typename E::store_t> y, float *h_final, int64_t L,
-                                                        int D, int strips) {
-    const int64_t b = blockIdx.x / strips;
-    const int d = (int)(blockIdx.x % strips) * 64 + threadIdx.x;
-    if (d >= D) return;
-    const int64_t n = tokens_of(lengths, b, L);
-    float h = h0 ? h0[b * D + d] : 0.0f;
-    for (int64_t t = 0; t < n; ++t) {
-        const int64_t row = b * L + t;
-        const Gate k = gate<F>(E::load(g.p + row * g.ld + d));
-        h = gated_advance(h, k.a, gated_input<F>(k, E::load(u.p + row * u.ld + d)));
-        E::store(y.p + row * y.ld + d, h);
+// What a lane loads and stores at a time: n channels in one word.  The two-channel bf16 word needs rows
+// that start on 4 bytes and an even D; the one-channel word takes the rest.
+struct Bf16x2 {
+    using store_t = uint16_t;
+    using word = uint32_t;
+    static constexpr int n = 2;
+    static __device__ __forceinline__ void unpack(word w, float (&f)[2]) {
+        f[0] = bf16_lo(w);
+        f[1] = bf16_hi(w);
     }
-    for (int64_t t = n; t < L; ++t) E::store(y.p + (b * L + t) * y.ld + d, 0.0f);
-    h_final[b * D + d] = h;
-}
+    static __device__ __forceinline__ word pack(const float (&f)[2]) { return pack_bf16x2(f[0], f[1]); }
+};
+struct Bf16x1 {
+    using store_t = uint16_t;
+    using word = uint16_t;
+    static constexpr int n = 1;
+    static __device__ __forceinline__ void unpack(word w, float (&f)[1]) { f[0] = bf16_bits_to_f32(w); }
+    static __device__ __forceinline__ word pack(const float (&f)[1]) { return f32_to_bf16_bits(f[0]); }
+};
+struct F32x1 {
+    using store_t = float;
+    using word = float;
+    static constexpr int n = 1;
+    static __device__ __forceinline__ void unpack(word w, float (&f)[1]) { f[0] = w; }
+    static __device__ __forceinline__ word pack(const float (&f)[1]) { return f[0]; }
+};
 
-template <typename E, GateForm F>
-__global__ __launch_bounds__(64) void gated_lane_backward_kernel(
-    TokenRows<const typename E::store_t> g, TokenRows<const typename E::store_t> u,
-    TokenRows<const typename E::store_t> y, TokenRows<const typename E::store_t> dy, const float *__restrict__ h0,
-    const float *dh_final, const int32_t *__restrict__ lengths, TokenRows<typename E::store_t> dg,
-    TokenRows<typename E::store_t> du, float *dh0, int64_t L, int D, int strips) {
-    const int64_t b = blockIdx.x / strips;
-    const int d = (int)(blockIdx.x % strips) * 64 + threadIdx.x;
-    if (d >= D) return;
-    const int64_t n = tokens_of(lengths, b, L);
-    float c = dh_final ? dh_final[b * D + d] : 0.0f;
-    for (int64_t t = L - 1; t >= n; --t) {
-        E::store(dg.p + (b * L + t) * dg.ld + d, 0.0f);
-        E::store(du.p + (b * L + t) * du.ld + d, 0.0f);
+// A sequence's tokens cut into n_seg segments of seg_len tokens of scan order (n_seg = 1: not cut).
+// sums[b][seg][D] holds the segments' maps (A, H), start[b][D] a copy of the scan's starting state (the caller's
+// own array may be overwritten by the final one while late segments still need it).
+struct SegSplit {
+    int n_seg;
+    int64_t seg_len;
+    float2 *sums;
+    float *start;
+};
+
+namespace strip {
+
+// A wave's place in its work-group and a lane's in its strip.
+template <typename V, int LC, int NW, int TT> struct Place {
+    static constexpr int kSub = 64 / LC;         // runs per wave
+    static constexpr int kRuns = kSub * NW;      // runs per work-group
+    static constexpr int kBlock = kRuns * TT;    // tokens per block
+    static constexpr int kChannels = LC * V::n;  // channels per strip
+};
+
+// One tensor's rows as a strip walks them in scan order (kRev: from the last token down).  A row's address is
+// a wave-uniform part and a 32-bit lane part (channel, and the lane's run inside the wave).
+template <typename V, int LC, int TT, bool kRev> struct Stream {
+    using word = typename V::word;
+    char *base;          // row of token 0 of the sequence, channel 0
+    int64_t ld;          // bytes between rows
+    uint32_t lane_off;   // channel and run part of the address
+    uint32_t chan_off;   // channel part alone
+
+    template <typename T>
+    __device__ __forceinline__ Stream(TokenRows<T> r, int64_t b, int64_t L, int sub, uint32_t channel_word) {
+        base = reinterpret_cast<char *>(const_cast<typename V::store_t *>(r.p)) + b * L * r.ld * (int64_t)sizeof(typename V::store_t);
+        ld = r.ld * (int64_t)sizeof(typename V::store_t);
+        chan_off = channel_word * (uint32_t)sizeof(word);
+        const int runs_down = kRev ? 64 / LC - 1 - sub : sub;
+        lane_off = chan_off + (uint32_t)(runs_down * TT) * (uint32_t)ld;
     }
-    for (int64_t t = n - 1; t >= 0; --t) {
-        const int64_t row = b * L + t;
-        const Gate k = gate<F>(E::load(g.p + row * g.ld + d));
-        const float h = t > 0 ? E::load(y.p + (row - 1) * y.ld + d) : (h0 ? h0[b * D + d] : 0.0f);
-        const float G = E::load(dy.p + row * dy.ld + d) + c;
-        c = k.a * G;
-        if constexpr (F == GateForm::Decay) {
-            E::store(dg.p + row * dg.ld + d, c * h);
-            E::store(du.p + row * du.ld + d, G);
-        } else {
-            E::store(dg.p + row * dg.ld + d, c * k.b * (h - E::load(u.p + row * u.ld + d)));
-            E::store(du.p + row * du.ld + d, k.b * G);
+    // Row address of step i of the wave's runs, which start at scan position tau (of n): the lowest
+    // token among the wave's lanes.
+    __device__ __forceinline__ char *row(int64_t tau, int64_t n, int i) const {
+        const int64_t t = kRev ? n - 1 - tau - i - (64 / LC - 1) * TT : tau + i;
+        return base + t * ld;
+    }
+    __device__ __forceinline__ void load(word (&w)[TT], int64_t tau, int64_t n, int shift) const {
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+            w[i] = __builtin_nontemporal_load(reinterpret_cast<const word *>(row(tau, n, i) + shift * ld + lane_off));
+    }
+    // The same near the ends: token by token, tokens outside [lo, hi] taken at the nearer end.
+    __device__ __forceinline__ void load_clamped(word (&w)[TT], int64_t lane_tau, int64_t n, int shift, int64_t lo,
+                                                 int64_t hi) const {
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            int64_t t = (kRev ? n - 1 - lane_tau - i : lane_tau + i) + shift;
+            t = t < lo ? lo : (t > hi ? hi : t);
+            w[i] = *reinterpret_cast<const word *>(base + t * ld + chan_off);
         }
     }
-    if (dh0) dh0[b * D + d] = c;
+    __device__ __forceinline__ void store(word v, int64_t tau, int64_t n, int i) const {
+        __builtin_nontemporal_store(v, reinterpret_cast<word *>(row(tau, n, i) + lane_off));
+    }
+    __device__ __forceinline__ void store_at(word v, int64_t t) const {
+        *reinterpret_cast<word *>(base + t * ld + chan_off) = v;
+    }
+};
+
+// Maps s -> A s + H of a thread's channels.
+template <int N> struct Map {
+    float A[N], H[N];
+};
+template <int N> __device__ __forceinline__ void compose_after(Map<N> &later, const float (&A)[N], const float (&H)[N]) {
+#pragma unroll
+    for (int v = 0; v < N; ++v) {   // later o (A, H)
+        later.H[v] = __builtin_fmaf(later.A[v], H[v], later.H[v]);
+        later.A[v] *= A[v];
+    }
+}
+
+// Joins the runs of a block (step 2 above).  run: this thread's map.  Returns the state before its run in
+// s_in; carry[parity] holds the state before the block, carry[parity ^ 1] receives the one after it.  One barrier
+// a block suffices: arrays of one parity are written again only two barriers later.
+template <typename V, int LC, int NW> struct Join {
+    static constexpr int N = V::n, kSub = 64 / LC;
+    float2 maps[2][NW][LC * N];
+    float carry[2][LC * N];
+
+    __device__ __forceinline__ void operator()(Map<N> run, float (&s_in)[N], float (&s_out)[N], int wave, int lane, int parity) {
+        const int c = lane % LC, sub = lane / LC;
+        Map<N> before;   // the runs of this wave before this one
+#pragma unroll
+        for (int v = 0; v < N; ++v) before.A[v] = 1.0f, before.H[v] = 0.0f;
+        if constexpr (kSub > 1) {
+            float A[N], H[N];
+#pragma unroll
+            for (int dist = LC; dist < 64; dist *= 2) {
+#pragma unroll
+                for (int v = 0; v < N; ++v) {
+                    A[v] = __shfl_up(run.A[v], dist);
+                    H[v] = __shfl_up(run.H[v], dist);
+                }
+                if (lane >= dist) compose_after(run, A, H);
+            }
+#pragma unroll
+            for (int v = 0; v < N; ++v) {
+                const float a = __shfl_up(run.A[v], LC), h = __shfl_up(run.H[v], LC);
+                before.A[v] = sub > 0 ? a : 1.0f;
+                before.H[v] = sub > 0 ? h : 0.0f;
+            }
+        }
+        if (sub == kSub - 1) {
+#pragma unroll
+            for (int v = 0; v < N; ++v) maps[parity][wave][c * N + v] = make_float2(run.A[v], run.H[v]);
+        }
+        __syncthreads();
+        float s[N];
+#pragma unroll
+        for (int v = 0; v < N; ++v) s[v] = carry[parity][c * N + v];
+#pragma unroll 4
+        for (int w = 0; w < wave; ++w) {
+#pragma unroll
+            for (int v = 0; v < N; ++v) {
+                const float2 m = maps[parity][w][c * N + v];
+                s[v] = __builtin_fmaf(m.x, s[v], m.y);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+            s_in[v] = kSub > 1 ? __builtin_fmaf(before.A[v], s[v], before.H[v]) : s[v];
+            s_out[v] = __builtin_fmaf(run.A[v], s[v], run.H[v]);
+        }
+        if (wave == NW - 1 && sub == kSub - 1) {
+#pragma unroll
+            for (int v = 0; v < N; ++v) carry[parity ^ 1][c * N + v] = s_out[v];
+        }
+    }
+};
+
+// Work-group id -> (sequence, segment, strip).  Neighbouring strips share 128-byte lines when they are narrow, so
+// consecutive strips go to work-groups of one XCD (ids 8 apart).
+struct Where {
+    int64_t b;
+    int seg, strip;
+};
+__device__ __forceinline__ Where where(int strips, int n_seg) {
+    const uint32_t n = gridDim.x, per = n / 8, id = blockIdx.x;
+    const uint32_t v = id < per * 8 ? (id % 8) * per + id / 8 : id;
+    const uint32_t row = v / (uint32_t)strips;
+    return Where{(int64_t)(row / (uint32_t)n_seg), (int)(row % (uint32_t)n_seg), (int)(v % (uint32_t)strips)};
+}
+
+// This thread row's share of the maps before segment seg of a cut sequence, composed: the join of all shares
+// carries the scan's starting state to the segment's.
+template <typename V, int LC, int NW>
+__device__ __forceinline__ Map<V::n> share_before(const SegSplit &sp, int64_t b, int seg, int D, int d, int run) {
+    constexpr int N = V::n, kRuns = 64 / LC * NW;
+    const int per = (sp.n_seg - 1 + kRuns - 1) / kRuns;
+    Map<N> m;
+#pragma unroll
+    for (int v = 0; v < N; ++v) m.A[v] = 1.0f, m.H[v] = 0.0f;
+    const float2 *p = sp.sums + b * sp.n_seg * D + d;
+    const int k0 = run * per, k1 = min(k0 + per, seg);
+#pragma unroll 4
+    for (int k = k0; k < k1; ++k) {
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+            const float2 s = p[(int64_t)k * D + v];
+            m.H[v] = __builtin_fmaf(s.x, m.H[v], s.y);
+            m.A[v] *= s.x;
+        }
+    }
+    return m;
+}
+
+// The decay and input of one word of the scan: from (g, u) forward, from (g, dy) backward.
+template <typename V, GateForm F, bool kRev>
+__device__ __forceinline__ void scan_terms(typename V::word gw, typename V::word xw, Gate (&k)[V::n], float (&x)[V::n]) {
+    float g[V::n], in[V::n];
+    V::unpack(gw, g);
+    V::unpack(xw, in);
+#pragma unroll
+    for (int v = 0; v < V::n; ++v) {
+        k[v] = gate<F>(g[v]);
+        x[v] = kRev ? k[v].a * in[v] : gated_input<F>(k[v], in[v]);
+    }
+}
+
+}  // namespace strip
+
+// The maps of all segments but the last of a cut sequence, which must be whole.  Each thread takes one long run of the
+// segment, so nothing is joined until its end.
+template <typename V, GateForm F, int LC, int NW, int TT, bool kRev>
+__global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const typename V::store_t> g,
+                                                                TokenRows<const typename V::store_t> x,
+                                                                const float *s0, const int32_t *__restrict__ lengths,
+                                                                SegSplit sp, int64_t L, int D, int strips) {
+    using namespace strip;
+    using P = Place<V, LC, NW, TT>;
+    using word = typename V::word;
+    constexpr int N = V::n;
+    __shared__ float2 maps[P::kRuns][LC * N];
+    const Where at = where(strips, sp.n_seg - 1);
+    const int64_t n = tokens_of(lengths, at.b, L);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int c = lane % LC, sub = lane / LC, words = D / N;
+    const int cw = at.strip * LC + c;
+    const bool live = cw < words;
+    if (at.seg == 0 && threadIdx.x < LC && live) {
+#pragma unroll
+        for (int v = 0; v < N; ++v) sp.start[at.b * D + cw * N + v] = s0 ? s0[at.b * D + cw * N + v] : 0.0f;
+    }
+    const int64_t tau0 = at.seg * sp.seg_len;
+    if (tau0 + sp.seg_len > n) return;   // never read: no token lies behind a segment that is not whole
+    const int64_t per = sp.seg_len / P::kRuns;   // tokens per thread, a multiple of TT
+    const uint32_t cl = (uint32_t)(live ? cw : words - 1);
+    Stream<V, LC, TT, kRev> gs(g, at.b, L, sub, cl), xs(x, at.b, L, sub, cl);
+    const int64_t lane_tau = tau0 + (wave * P::kSub + sub) * per;
+
+    Map<N> run;
+#pragma unroll
+    for (int v = 0; v < N; ++v) run.A[v] = 1.0f, run.H[v] = 0.0f;
+    // rows of a lane: runs lie `per` tokens apart here
+    const int64_t step = kRev ? -1 : 1, t0 = kRev ? n - 1 - lane_tau : lane_tau;
+    const char *gp = gs.base + t0 * gs.ld + gs.chan_off, *xp = xs.base + t0 * xs.ld + xs.chan_off;
+    word gw[TT], xw[TT], gn[TT], xn[TT];
+    auto load = [&](word(&gd)[TT], word(&xd)[TT], int64_t i0) {
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            gd[i] = *reinterpret_cast<const word *>(gp + (i0 + i) * step * gs.ld);
+            xd[i] = *reinterpret_cast<const word *>(xp + (i0 + i) * step * xs.ld);
+        }
+    };
+    load(gw, xw, 0);
+    for (int64_t i0 = 0; i0 < per; i0 += TT) {
+        load(gn, xn, i0 + TT < per ? i0 + TT : i0);
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            Gate k[N];
+            float in[N];
+            scan_terms<V, F, kRev>(gw[i], xw[i], k, in);
+#pragma unroll
+            for (int v = 0; v < N; ++v) {
+                run.H[v] = __builtin_fmaf(k[v].a, run.H[v], in[v]);
+                run.A[v] *= k[v].a;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < TT; ++i) gw[i] = gn[i], xw[i] = xn[i];
+    }
+#pragma unroll
+    for (int v = 0; v < N; ++v) maps[wave * P::kSub + sub][c * N + v] = make_float2(run.A[v], run.H[v]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < LC * N; i += NW * 64) {
+        float A = 1.0f, H = 0.0f;
+#pragma unroll 8
+        for (int r = 0; r < P::kRuns; ++r) {
+            const float2 m = maps[r][i];
+            H = __builtin_fmaf(m.x, H, m.y);
+            A *= m.x;
+        }
+        const int d = at.strip * LC * N + i;
+        if (d < D) sp.sums[(at.b * sp.n_seg + at.seg) * D + d] = make_float2(A, H);
+    }
+}
+
+// Forward scan of a strip.
+template <typename V, GateForm F, int LC, int NW, int TT>
+__global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typename V::store_t> g,
+                                                             TokenRows<const typename V::store_t> u, const float *h0,
+                                                             const int32_t *__restrict__ lengths,
+                                                             TokenRows<typename V::store_t> y, float *h_final,
+                                                             SegSplit sp, int64_t L, int D, int strips) {
+    using namespace strip;
+    using P = Place<V, LC, NW, TT>;
+    using word = typename V::word;
+    constexpr int N = V::n;
+    __shared__ Join<V, LC, NW> join;
+    const Where at = where(strips, sp.n_seg);
+    const int64_t n = tokens_of(lengths, at.b, L);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int c = lane % LC, sub = lane / LC, words = D / N;
+    const int cw = at.strip * LC + c;
+    const bool live = cw < words;
+    const uint32_t cl = (uint32_t)(live ? cw : words - 1);
+    const int64_t seg0 = at.seg * sp.seg_len, seg_end = min(seg0 + sp.seg_len, L);
+    const int64_t end = min(seg_end, n);   // tokens [seg0, end) are scanned, [max(seg0, n), seg_end) cleared
+    Stream<V, LC, TT, false> gs(g, at.b, L, sub, cl), us(u, at.b, L, sub, cl), ys(y, at.b, L, sub, cl);
+
+    // the segment's starting state; the segment with the last token (the first one of an empty sequence) ends with
+    // the final state
+    float s_end[N];
+#pragma unroll
+    for (int v = 0; v < N; ++v) s_end[v] = 0.0f;
+    const bool writes_final = seg0 < n ? seg_end >= n : (n == 0 && at.seg == 0);
+    const float *begin = sp.n_seg > 1 ? sp.start : h0;
+    if (wave == NW - 1 || threadIdx.x < LC) {
+#pragma unroll
+        for (int v = 0; v < N; ++v) s_end[v] = begin ? begin[at.b * D + (int)cl * N + v] : 0.0f;
+        if (threadIdx.x < LC) {
+#pragma unroll
+            for (int v = 0; v < N; ++v) join.carry[at.seg > 0][c * N + v] = s_end[v];
+        }
+    }
+    if (at.seg > 0 && seg0 < end) {
+        float unused[N];
+        join(share_before<V, LC, NW>(sp, at.b, at.seg, D, (int)cl * N, wave * P::kSub + sub), unused, s_end, wave, lane, 1);
+    }
+
+    const int64_t wave_run = (int64_t)wave * P::kSub * TT, lane_run = wave_run + sub * TT;
+    struct Block {
+        word g[TT], u[TT];
+    } blocks[2];
+    auto load = [&](Block &w, int64_t t) {   // the whole block at token t
+        gs.load(w.g, t + wave_run, n, 0);
+        us.load(w.u, t + wave_run, n, 0);
+    };
+    auto scan_block = [&](const Block &w, int64_t t, int parity, auto is_whole) {
+        constexpr bool whole = decltype(is_whole)::value;
+        float A[TT][N], H[TT][N];
+        Map<N> run;
+#pragma unroll
+        for (int v = 0; v < N; ++v) run.A[v] = 1.0f, run.H[v] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            Gate k[N];
+            float in[N];
+            scan_terms<V, F, false>(w.g[i], w.u[i], k, in);
+            const bool on = whole || t + lane_run + i < end;
+#pragma unroll
+            for (int v = 0; v < N; ++v) {
+                const float a = on ? k[v].a : 1.0f, x = on ? in[v] : 0.0f;
+                run.H[v] = __builtin_fmaf(a, run.H[v], x);
+                run.A[v] *= a;
+                A[i][v] = run.A[v];
+                H[i][v] = run.H[v];
+            }
+        }
+        float s_in[N];
+        join(run, s_in, s_end, wave, lane, parity);
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            float s[N];
+#pragma unroll
+            for (int v = 0; v < N; ++v) s[v] = __builtin_fmaf(A[i][v], s_in[v], H[i][v]);
+            if (whole) {
+                if (live) ys.store(V::pack(s), t + wave_run, n, i);
+            } else if (live && t + lane_run + i < end) {
+                ys.store_at(V::pack(s), t + lane_run + i);
+            }
+        }
+    };
+    const int64_t blocks_n = end > seg0 ? (end - seg0) / P::kBlock : 0, tail = seg0 + blocks_n * P::kBlock;
+    if (blocks_n > 0) load(blocks[0], seg0);
+    for (int64_t t = seg0; t < tail; t += 2 * P::kBlock) {
+        if (t + P::kBlock < tail) load(blocks[1], t + P::kBlock);
+        __builtin_amdgcn_sched_barrier(0);   // the next block's loads go out before this block's arithmetic
+        scan_block(blocks[0], t, 0, std::true_type{});
+        if (t + P::kBlock >= tail) break;
+        if (t + 2 * P::kBlock < tail) load(blocks[0], t + 2 * P::kBlock);
+        __builtin_amdgcn_sched_barrier(0);
+        scan_block(blocks[1], t + P::kBlock, 1, std::true_type{});
+    }
+    if (tail < end) {
+        Block &w = blocks[0];
+        if (tail + wave_run < end) {   // waves behind the end have nothing to load
+            gs.load_clamped(w.g, tail + lane_run, n, 0, 0, n - 1);
+            us.load_clamped(w.u, tail + lane_run, n, 0, 0, n - 1);
+        }
+        scan_block(w, tail, (int)(blocks_n & 1), std::false_type{});
+    }
+    if (writes_final && wave == NW - 1 && sub == P::kSub - 1 && live) {
+#pragma unroll
+        for (int v = 0; v < N; ++v) h_final[at.b * D + cw * N + v] = s_end[v];
+    }
+    if (live) {
+        float zero[N];
+#pragma unroll
+        for (int v = 0; v < N; ++v) zero[v] = 0.0f;
+        for (int64_t t = max(seg0, n) + wave * P::kSub + sub; t < seg_end; t += P::kRuns) ys.store_at(V::pack(zero), t);
+    }
+}
+
+// Backward pass of a strip: the scan of c from the last token down, then the gradients of each token from c of
+// the token after it and h of the token before it.
+template <typename V, GateForm F, int LC, int NW, int TT>
+__global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
+    TokenRows<const typename V::store_t> g, TokenRows<const typename V::store_t> u,
+    TokenRows<const typename V::store_t> y, TokenRows<const typename V::store_t> dy, const float *__restrict__ h0,
+    const float *dh_final, const int32_t *__restrict__ lengths, TokenRows<typename V::store_t> dg,
+    TokenRows<typename V::store_t> du, float *dh0, SegSplit sp, int64_t L, int D, int strips) {
+    using namespace strip;
+    using P = Place<V, LC, NW, TT>;
+    using word = typename V::word;
+    constexpr int N = V::n;
+    constexpr bool kSig = F == GateForm::Sigmoid;
+    __shared__ Join<V, LC, NW> join;
+    const Where at = where(strips, sp.n_seg);
+    const int64_t n = tokens_of(lengths, at.b, L);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int c = lane % LC, sub = lane / LC, words = D / N;
+    const int cw = at.strip * LC + c;
+    const bool live = cw < words;
+    const uint32_t cl = (uint32_t)(live ? cw : words - 1);
+    // tau counts tokens from the sequence's last one; padding is cleared by token index
+    const int64_t seg0 = at.seg * sp.seg_len, seg_end = min(seg0 + sp.seg_len, L);
+    const int64_t end = min(seg_end, n);
+    Stream<V, LC, TT, true> gs(g, at.b, L, sub, cl), us(kSig ? u : g, at.b, L, sub, cl), hs(y, at.b, L, sub, cl),
+        ds(dy, at.b, L, sub, cl), dgs(dg, at.b, L, sub, cl), dus(du, at.b, L, sub, cl);
+
+    float s_end[N];
+#pragma unroll
+    for (int v = 0; v < N; ++v) s_end[v] = 0.0f;
+    const bool writes_final = seg0 < n ? seg_end >= n : (n == 0 && at.seg == 0);
+    const float *begin = sp.n_seg > 1 ? sp.start : dh_final;
+    if (wave == NW - 1 || threadIdx.x < LC) {
+#pragma unroll
+        for (int v = 0; v < N; ++v) s_end[v] = begin ? begin[at.b * D + (int)cl * N + v] : 0.0f;
+        if (threadIdx.x < LC) {
+#pragma unroll
+            for (int v = 0; v < N; ++v) join.carry[at.seg > 0][c * N + v] = s_end[v];
+        }
+    }
+    if (at.seg > 0 && seg0 < end) {
+        float unused[N];
+        join(share_before<V, LC, NW>(sp, at.b, at.seg, D, (int)cl * N, wave * P::kSub + sub), unused, s_end, wave, lane, 1);
+    }
+
+    const int64_t wave_run = (int64_t)wave * P::kSub * TT, lane_run = wave_run + sub * TT;
+    struct Block {
+        word g[TT], d[TT], h[TT], u[kSig ? TT : 1];
+    } blocks[2];
+    auto load = [&](Block &w, int64_t tau) {   // the whole block at tau
+        gs.load(w.g, tau + wave_run, n, 0);
+        ds.load(w.d, tau + wave_run, n, 0);
+        hs.load(w.h, tau + wave_run, n, -1);
+        if constexpr (kSig) us.load(w.u, tau + wave_run, n, 0);
+    };
+    auto scan_block = [&](const Block &w, int64_t tau, int parity, auto is_whole) {
+        constexpr bool whole = decltype(is_whole)::value;
+        float A[TT][N], H[TT][N], b[TT][N];
+        Map<N> run;
+#pragma unroll
+        for (int v = 0; v < N; ++v) run.A[v] = 1.0f, run.H[v] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            Gate k[N];
+            float in[N];
+            scan_terms<V, F, true>(w.g[i], w.d[i], k, in);
+            const bool on = whole || tau + lane_run + i < end;
+#pragma unroll
+            for (int v = 0; v < N; ++v) {
+                const float a = on ? k[v].a : 1.0f, x = on ? in[v] : 0.0f;
+                run.H[v] = __builtin_fmaf(a, run.H[v], x);
+                run.A[v] *= a;
+                A[i][v] = run.A[v];
+                H[i][v] = run.H[v];
+                if constexpr (kSig) b[i][v] = k[v].b;
+            }
+        }
+        float s_in[N];
+        join(run, s_in, s_end, wave, lane, parity);
+        float after[N];   // c of the token after this one
+#pragma unroll
+        for (int v = 0; v < N; ++v) after[v] = s_in[v];
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            float h[N], d[N], uu[N], out_g[N], out_u[N];
+            V::unpack(w.h[i], h);
+            V::unpack(w.d[i], d);
+            if constexpr (kSig) V::unpack(w.u[i], uu);
+            const int64_t t = n - 1 - (tau + lane_run + i);
+            if (!whole && t == 0) {
+#pragma unroll
+                for (int v = 0; v < N; ++v) h[v] = h0 ? h0[at.b * D + (int)cl * N + v] : 0.0f;
+            }
+#pragma unroll
+            for (int v = 0; v < N; ++v) {
+                const float cc = __builtin_fmaf(A[i][v], s_in[v], H[i][v]), G = d[v] + after[v];
+                after[v] = cc;
+                if constexpr (kSig) {
+                    out_g[v] = cc * b[i][v] * (h[v] - uu[v]);
+                    out_u[v] = b[i][v] * G;
+                } else {
+                    out_g[v] = cc * h[v];
+                    out_u[v] = G;
+                }
+            }
+            if (whole) {
+                if (live) {
+                    dgs.store(V::pack(out_g), tau + wave_run, n, i);
+                    dus.store(V::pack(out_u), tau + wave_run, n, i);
+                }
+            } else if (live && tau + lane_run + i < end) {
+                dgs.store_at(V::pack(out_g), t);
+                dus.store_at(V::pack(out_u), t);
+            }
+        }
+    };
+    // A block is whole when all its tokens, and the one before each, exist.
+    int64_t blocks_n = end > seg0 ? (end - seg0) / P::kBlock : 0;
+    if (blocks_n > 0 && seg0 + blocks_n * P::kBlock == n) --blocks_n;
+    const int64_t tail = seg0 + blocks_n * P::kBlock;
+    if (blocks_n > 0) load(blocks[0], seg0);
+    for (int64_t tau = seg0; tau < tail; tau += 2 * P::kBlock) {
+        if (tau + P::kBlock < tail) load(blocks[1], tau + P::kBlock);
+        __builtin_amdgcn_sched_barrier(0);
+        scan_block(blocks[0], tau, 0, std::true_type{});
+        if (tau + P::kBlock >= tail) break;
+        if (tau + 2 * P::kBlock < tail) load(blocks[0], tau + 2 * P::kBlock);
+        __builtin_amdgcn_sched_barrier(0);
+        scan_block(blocks[1], tau + P::kBlock, 1, std::true_type{});
+    }
+    if (tail < end) {
+        Block &w = blocks[0];
+        if (tail + wave_run < end) {
+            gs.load_clamped(w.g, tail + lane_run, n, 0, 0, n - 1);
+            ds.load_clamped(w.d, tail + lane_run, n, 0, 0, n - 1);
+            hs.load_clamped(w.h, tail + lane_run, n, -1, 0, n - 1);
+            if constexpr (kSig) us.load_clamped(w.u, tail + lane_run, n, 0, 0, n - 1);
+        }
+        scan_block(w, tail, (int)(blocks_n & 1), std::false_type{});
+    }
+    if (writes_final && dh0 && wave == NW - 1 && sub == P::kSub - 1 && live) {
+#pragma unroll
+        for (int v = 0; v < N; ++v) dh0[at.b * D + cw * N + v] = s_end[v];
+    }
+    if (live) {
+        float zero[N];
+#pragma unroll
+        for (int v = 0; v < N; ++v) zero[v] = 0.0f;
+        for (int64_t t = max(seg0, n) + wave * P::kSub + sub; t < seg_end; t += P::kRuns) {
+            dgs.store_at(V::pack(zero), t);
+            dus.store_at(V::pack(zero), t);
+        }
+    }
 }
 
 // One decode token: one thread per (sequence, channel), the state in place.

@@ -43,7 +43,7 @@ def scan(g, u, h0=None, lengths=None, form="decay"):
 def backward(g, u, y, dy, h0=None, dh_final=None, lengths=None, form="decay"):
     """(dg, du, dh0, c) with h_{t-1} taken from y; c_t = a_t dL/dh_t."""
     a, b = gates(g, form)
-    y, dy = _f64(y), _f64(dy)
+    y, dy, u = _f64(y), _f64(dy), None if u is None else _f64(u)
     batch, L, D = y.shape
     n = _lengths(lengths, batch, L)
     c = np.zeros((batch, D)) if dh_final is None else _f64(dh_final).copy()
@@ -56,7 +56,7 @@ def backward(g, u, y, dy, h0=None, dh_final=None, lengths=None, form="decay"):
         c[on] = a[on, t] * G
         cs[on, t] = c[on]
         du[on, t] = b[on, t] * G
-        dg[on, t] = c[on] * before if form == "decay" else c[on] * b[on, t] * (before - _f64(u)[on, t])
+        dg[on, t] = c[on] * before if form == "decay" else c[on] * b[on, t] * (before - u[on, t])
     return dg, du, c, cs
 
 
@@ -98,7 +98,7 @@ def backward_error(g, u, y, dy, h0=None, dh_final=None, lengths=None, form="deca
     before the rounding of the outputs: c is a scan from the last token to the first with gates a
     and inputs a dy, so scan_error's argument holds for it."""
     a, b = gates(g, form)
-    y, dy = _f64(y), _f64(dy)
+    y, dy, u = _f64(y), _f64(dy), None if u is None else _f64(u)
     batch, L, D = y.shape
     n = _lengths(lengths, batch, L)
     start = np.zeros((batch, D)) if h0 is None else _f64(h0)
@@ -116,7 +116,7 @@ def backward_error(g, u, y, dy, h0=None, dh_final=None, lengths=None, form="deca
             Eu[on, t] = EG
             Eg[on, t] = (E[on] + 2 * r * M[on]) * before
         else:
-            span = before + np.abs(_f64(u)[on, t])
+            span = before + np.abs(u[on, t])
             Eu[on, t] = b[on, t] * EG + (e[on, t] + r) * b[on, t] * G
             Eg[on, t] = b[on, t] * span * (E[on] + (e[on, t] + 4 * r) * M[on])
     return Eg, Eu, E
