@@ -13,6 +13,92 @@ bool dims_ok(int64_t M, int64_t K) {
     return M >= 0 && M <= ((int64_t)1 << 30) && K >= 0 && K % 16 == 0 && K <= kMaxK;
 }
 
+// Rows on 16 bytes stay in registers: one wave for short ones, four up to 1024 chunks of 16 bytes (8192 bf16
+// values), sixteen up to 4096; the rest is read twice.
+template <typename E>
+void launch_quantize(const void *x, int8_t *q, float *scale, int64_t M, int64_t K, int64_t ld_x, hipStream_t s) {
+    const auto *xt = static_cast<const typename E::store_t *>(x);
+    const int64_t per = 16 / (int64_t)sizeof(typename E::store_t), chunks = K / per;
+    const dim3 grid((unsigned)M);
+    if (!aligned16(x) || ld_x % per != 0 || chunks > 4096)
+        hipLaunchKernelGGL(jscan::quantize_any_rows_kernel<E>, grid, dim3(256), 0, s, xt, q, scale, (int)K, ld_x);
+    else if (chunks <= 128)
+        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 1, 2>), grid, dim3(64), 0, s, xt, q, scale, (int)K, ld_x);
+    else if (chunks <= 512)
+        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 4, 2>), grid, dim3(256), 0, s, xt, q, scale, (int)K, ld_x);
+    else if (chunks <= 1024)
+        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 4, 4>), grid, dim3(256), 0, s, xt, q, scale, (int)K, ld_x);
+    else
+        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 16, 4>), grid, dim3(1024), 0, s, xt, q, scale, (int)K, ld_x);
+}
+
+// The tiles of the product and what they take, measured on this chip (us, bf16 output): `fixed` of a call, `round`
+// between two stages of one work-group that is alone on its CU, `stage` of one tile's stage on a CU that has
+// enough of them.
+struct Tile {
+    int bm, bn, groups;
+    float fixed, round, stage;
+};
+constexpr Tile kTiles[] = {
+    {16, 16, 8, 3.0f, 0.30f, 0.105f}, {16, 32, 4, 3.0f, 0.26f, 0.14f},  {32, 32, 4, 3.0f, 0.45f, 0.14f},
+    {32, 64, 4, 3.0f, 0.60f, 0.20f},  {64, 64, 1, 4.0f, 0.30f, 0.20f},  {128, 128, 1, 5.0f, 0.62f, 0.56f},
+    {256, 192, 1, 8.0f, 1.45f, 1.45f}, {256, 256, 1, 9.0f, 1.60f, 1.60f}};
+
+int64_t tiles_of(const Tile &t, int64_t M, int64_t N) { return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn); }
+
+// The tile that is expected to take least: large ones read least per product, small ones fill the chip when
+// rows and columns are few, and the 192 columns leave less of a tile empty for some widths.  The larger of the
+// time along one work-group's stages and the time of a CU's share of all stages, on 256 CUs:
+//     1 x 4096 x 8192 (M x N x K): 16 x 16 tiles 5.8 us, 16 x 32 7.9, 64 x 64 22
+//     77 x 4096 x 8192: 32 x 64 12 us, 32 x 32 18, 64 x 64 20, 128 x 128 40
+//     512 x 16384 x 4096: 128 x 128 37 us, 256 x 192 49, 256 x 256 55, 64 x 64 52
+//     65536 x 288 x 8192: 256 x 192 206 us, 128 x 128 231, 256 x 256 237
+int choose_tile(int64_t M, int64_t N, int64_t K) {
+    const int64_t stages = (K + 127) / 128;
+    int best = 0;
+    float least = 0.0f;
+    for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+        const Tile &t = kTiles[i];
+        const float along = (float)((stages + t.groups - 1) / t.groups) * t.round;
+        const float all = (float)((tiles_of(t, M, N) + 255) / 256) * (float)stages * t.stage;
+        const float us = t.fixed + (along > all ? along : all);
+        if (i == 0 || us < least) best = i, least = us;
+    }
+    return best;
+}
+
+struct MatmulArgs {
+    const int8_t *q;
+    const float *sq;
+    const int8_t *w;
+    const float *sw, *bias;
+    void *out;
+    int64_t M, N, K, ld_out;
+    hipStream_t stream;
+};
+
+template <typename E, int BM, int BN, int WR, int WC, int KG, int kBufs> void launch_tiled(const MatmulArgs &a) {
+    using T = typename E::store_t;
+    const int m_tiles = (int)((a.M + BM - 1) / BM), n_tiles = (int)((a.N + BN - 1) / BN);
+    const int wide = aligned16(a.out) && a.ld_out * (int64_t)sizeof(T) % 16 == 0;
+    hipLaunchKernelGGL((jscan::matmul_i8_tiled_kernel<E, BM, BN, WR, WC, KG, kBufs>),
+                       dim3((unsigned)((int64_t)m_tiles * n_tiles)), dim3(KG * WR * WC * 64), 0, a.stream, a.q, a.sq,
+                       a.w, a.sw, a.bias, static_cast<T *>(a.out), a.M, a.N, a.K, a.ld_out, m_tiles, n_tiles, wide);
+}
+
+template <typename E> void launch_matmul(const MatmulArgs &a) {
+    switch (choose_tile(a.M, a.N, a.K)) {
+    case 0: launch_tiled<E, 16, 16, 1, 1, 8, 3>(a); break;
+    case 1: launch_tiled<E, 16, 32, 1, 2, 4, 3>(a); break;
+    case 2: launch_tiled<E, 32, 32, 2, 1, 4, 4>(a); break;
+    case 3: launch_tiled<E, 32, 64, 1, 2, 4, 3>(a); break;
+    case 4: launch_tiled<E, 64, 64, 2, 2, 1, 3>(a); break;
+    case 5: launch_tiled<E, 128, 128, 2, 2, 1, 2>(a); break;
+    case 6: launch_tiled<E, 256, 192, 4, 2, 1, 2>(a); break;
+    default: launch_tiled<E, 256, 256, 2, 4, 1, 2>(a); break;
+    }
+}
+
 }  // namespace
 
 extern "C" {
@@ -29,12 +115,8 @@ jscan_status jscan_quantize_rows(const void *x, int8_t *q, float *scale, int64_t
     const Span sx = span(Rows{x, M, K * es, ld_x * es}), sq = span(q, M * K), ss = span(scale, M * 4);
     if (overlaps(sx, sq) || overlaps(sx, ss) || overlaps(sq, ss)) return JSCAN_ERR_ALIAS;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (dtype == JSCAN_BF16)
-        hipLaunchKernelGGL(jscan::quantize_rows_kernel<jscan::BF16>, dim3((unsigned)M), dim3(jscan::quant::kThreads), 0,
-                           s, static_cast<const uint16_t *>(x), q, scale, K, ld_x);
-    else
-        hipLaunchKernelGGL(jscan::quantize_rows_kernel<jscan::F32>, dim3((unsigned)M), dim3(jscan::quant::kThreads), 0,
-                           s, static_cast<const float *>(x), q, scale, K, ld_x);
+    if (dtype == JSCAN_BF16) launch_quantize<jscan::BF16>(x, q, scale, M, K, ld_x, s);
+    else launch_quantize<jscan::F32>(x, q, scale, M, K, ld_x, s);
     return launch_status();
 }
 
@@ -56,15 +138,9 @@ jscan_status jscan_matmul_i8(const int8_t *q, const float *q_scale, const int8_t
                        span(bias, bias ? N * 4 : 0)};
     for (const Span &i : in)
         if (overlaps(so, i)) return JSCAN_ERR_ALIAS;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t m_tiles = (M + 15) / 16, n_tiles = (N + 15) / 16;
-    const dim3 grid((unsigned)(m_tiles * n_tiles));
-    if (dtype == JSCAN_BF16)
-        hipLaunchKernelGGL(jscan::matmul_i8_kernel<jscan::BF16>, grid, dim3(64), 0, s, q, q_scale, w, w_scale, bias,
-                           static_cast<uint16_t *>(out), M, N, K, ld_out, (int)n_tiles);
-    else
-        hipLaunchKernelGGL(jscan::matmul_i8_kernel<jscan::F32>, grid, dim3(64), 0, s, q, q_scale, w, w_scale, bias,
-                           static_cast<float *>(out), M, N, K, ld_out, (int)n_tiles);
+    const MatmulArgs a{q, q_scale, w, w_scale, bias, out, M, N, K, ld_out, static_cast<hipStream_t>(stream)};
+    if (dtype == JSCAN_BF16) launch_matmul<jscan::BF16>(a);
+    else launch_matmul<jscan::F32>(a);
     return launch_status();
 }
 
