@@ -485,8 +485,8 @@ jscan_status jscan_gated_step(float *h, const void *g_t, const void *u_t, void *
  * section 3-2.3, holds the model's expert weights in int8 for serving).
  *
  * Row quantiser: every row (token) of x gets a scale of its own,
- *     scale[m] = max(max_k |x[m][k]| / 127, 2^-126),   q[m][k] = rint(x[m][k] * (1 / scale[m]))
- * in fp32, ties to even.  A row that holds a NaN or an infinity gets scale NaN and q = 0, so the
+ *     scale[m] = max(max_k |x[m][k]| * (1 / 127), 2^-126),   q[m][k] = rint(x[m][k] * (1 / scale[m]))
+ * in fp32 (each bracket rounded first), ties to even.  A row that holds a NaN or an infinity gets scale NaN and q = 0, so the
  * product's row is NaN and no other row is touched.
  *   x      M rows of K values in `dtype`, row stride ld_x >= K elements; rows that start on 16 bytes
  *          run faster

@@ -557,34 +557,70 @@ def step_mimo(h, x_t, delta_t, A, B_t, C_t, form="diagonal", y_t=None, _trap=Non
 # jscan_gate_form values: how the gate makes the decay.
 GATE_FORMS = {"decay": 0, "sigmoid": 1}
 
+# A decode token's kernels take a few microseconds, as much as a handful of Python calls: the checks below
+# build their messages only when they fail, and a launch asks for the raw stream and changes the current
+# device only where it has to.
+
+
+def _launch(fn, dev, *args):
+    """``fn(*args, stream)`` on dev's current stream, with dev current; raises on an error status."""
+    index = dev.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != 0:
+        _check(status)
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _bad(msg: str):
+    raise ValueError(msg)
+
+
+def _check_like(name, t, shape, dtype, dev):
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        _bad(f"{name} must have shape {tuple(shape)} and be {dtype} on {dev}, got {tuple(t.shape)}, {t.dtype}, {t.device}")
+
+
+def _check_flat(name, t, shape, dtype, dev):
+    """t is None or a contiguous tensor of this shape and dtype on dev."""
+    if t is not None:
+        _check_like(name, t, shape, dtype, dev)
+        if not t.is_contiguous():
+            _bad(f"{name} must be contiguous")
+
 
 def _token_rows(name, t, like, shape):
     """The token stride in elements of a [batch, L, D] tensor whose rows are contiguous and evenly
     spaced (contiguous, or a slice of a wider last dimension)."""
-    _require(t.shape == shape, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _require(t.dtype == like.dtype and t.device == like.device, f"{name} must be {like.dtype} on {like.device}")
+    _check_like(name, t, shape, like.dtype, like.device)
     batch, L, D = shape
     s_b, s_t, s_d = t.stride()
-    _require(s_d == 1 or D <= 1, f"{name} rows must be contiguous")
+    if s_d != 1 and D > 1:
+        _bad(f"{name} rows must be contiguous")
     if L > 1:
-        _require(batch <= 1 or s_b == L * s_t, f"{name}: sequences must follow each other at the token stride")
+        if batch > 1 and s_b != L * s_t:
+            _bad(f"{name}: sequences must follow each other at the token stride")
         return s_t
     return s_b if batch > 1 else D
 
 
-def _check_state(name, t, batch, D, dev):
-    _require(t is None or (t.shape == (batch, D) and t.dtype == torch.float32 and t.device == dev
-                           and t.is_contiguous()), f"{name} must be a contiguous fp32 [batch, D] tensor on g's device")
-
-
 def _check_gated(g, form, lengths):
-    _require(form in GATE_FORMS, f"form must be one of {tuple(GATE_FORMS)}")
-    _require(g.is_cuda, "inputs must be CUDA (HIP) tensors")
-    _require(g.dtype in _DTYPES, "g must be bfloat16 or float32")
-    _require(g.dim() == 3, "g must be [batch, L, D]")
-    _require(lengths is None or (lengths.shape == (g.shape[0],) and lengths.dtype == torch.int32
-                                 and lengths.device == g.device and lengths.is_contiguous()),
-             "lengths must be a contiguous int32 [batch] tensor on g's device")
+    if form not in GATE_FORMS:
+        _bad(f"form must be one of {tuple(GATE_FORMS)}")
+    if not g.is_cuda:
+        _bad("inputs must be CUDA (HIP) tensors")
+    if g.dtype not in _DTYPES:
+        _bad("g must be bfloat16 or float32")
+    if g.dim() != 3:
+        _bad("g must be [batch, L, D]")
+    _check_flat("lengths", lengths, g.shape[:1], torch.int32, g.device)
 
 
 def gated_scan_workspace_bytes(batch: int, L: int, D: int) -> int:
@@ -599,7 +635,11 @@ def _gated_workspace(workspace, batch, L, D, dev):
     need = gated_scan_workspace_bytes(batch, L, D)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    return workspace, (0 if workspace is None else workspace.numel() * workspace.element_size())
+    if workspace is None:
+        return None, 0
+    if workspace.device != dev:
+        _bad(f"workspace must be on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, workspace=None):
@@ -609,23 +649,23 @@ def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, 
     ``[batch, D]`` fp32; ``lengths`` int32 ``[batch]`` for padded sequences (y is zero in the padding).
     Returns ``(y [batch, L, D] in g's dtype, h_final [batch, D] fp32)``; ``h_final`` may be ``h0``."""
     _check_gated(g, form, lengths)
-    batch, L, D = g.shape
-    dev = g.device
-    ld_g, ld_u = _token_rows("g", g, g, g.shape), _token_rows("u", u, g, g.shape)
-    _check_state("h0", h0, batch, D, dev)
-    _check_state("h_final", h_final, batch, D, dev)
+    shape, dev = g.shape, g.device
+    batch, L, D = shape
+    ld_g, ld_u = _token_rows("g", g, g, shape), _token_rows("u", u, g, shape)
+    state = (batch, D)
+    _check_flat("h0", h0, state, torch.float32, dev)
     if y is None:
-        y = torch.empty((batch, L, D), dtype=g.dtype, device=dev)
-    ld_y = _token_rows("y", y, g, g.shape)
+        y, ld_y = torch.empty(shape, dtype=g.dtype, device=dev), D
+    else:
+        ld_y = _token_rows("y", y, g, shape)
     if h_final is None:
-        h_final = torch.empty((batch, D), dtype=torch.float32, device=dev)
+        h_final = torch.empty(state, dtype=torch.float32, device=dev)
+    else:
+        _check_flat("h_final", h_final, state, torch.float32, dev)
     workspace, ws_bytes = _gated_workspace(workspace, batch, L, D, dev)
-    lib = library()
-    with torch.cuda.device(dev):
-        st = lib.jscan_gated_scan(_ptr(g), _ptr(u), _ptr(h0), _ptr(lengths), _ptr(y), _ptr(h_final), batch, L, D, ld_g,
-                                  ld_u, ld_y, _ptr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype],
-                                  _stream(dev))
-    _check(st)
+    _launch(library().jscan_gated_scan, dev, g.data_ptr(), u.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
+            h_final.data_ptr(), batch, L, D, ld_g, ld_u, ld_y, _addr(workspace), ws_bytes, GATE_FORMS[form],
+            _DTYPES[g.dtype])
     return y, h_final
 
 
@@ -636,48 +676,57 @@ def gated_scan_backward(g, u, y, dy, h0=None, dh_final=None, lengths=None, form=
     its results.  The decay form does not read u (it may be None).  Returns ``(dg, du, dh0)``; dg and du
     may be given as the halves of one wider gradient."""
     _check_gated(g, form, lengths)
-    batch, L, D = g.shape
-    dev = g.device
-    _require(u is not None or form == "decay", "u is needed by the sigmoid form")
-    ld_g, ld_y, ld_dy = (_token_rows(n, t, g, g.shape) for n, t in (("g", g), ("y", y), ("dy", dy)))
-    ld_u = D if u is None else _token_rows("u", u, g, g.shape)
-    for name, t in (("h0", h0), ("dh_final", dh_final), ("dh0", dh0)):
-        _check_state(name, t, batch, D, dev)
-    dg = torch.empty((batch, L, D), dtype=g.dtype, device=dev) if dg is None else dg
-    du = torch.empty((batch, L, D), dtype=g.dtype, device=dev) if du is None else du
-    ld_dg, ld_du = _token_rows("dg", dg, g, g.shape), _token_rows("du", du, g, g.shape)
-    dh0 = torch.empty((batch, D), dtype=torch.float32, device=dev) if dh0 is None else dh0
+    shape, dev = g.shape, g.device
+    batch, L, D = shape
+    if u is None and form != "decay":
+        _bad("u is needed by the sigmoid form")
+    ld_g, ld_y, ld_dy = _token_rows("g", g, g, shape), _token_rows("y", y, g, shape), _token_rows("dy", dy, g, shape)
+    ld_u = D if u is None else _token_rows("u", u, g, shape)
+    state = (batch, D)
+    _check_flat("h0", h0, state, torch.float32, dev)
+    _check_flat("dh_final", dh_final, state, torch.float32, dev)
+    if dg is None:
+        dg, ld_dg = torch.empty(shape, dtype=g.dtype, device=dev), D
+    else:
+        ld_dg = _token_rows("dg", dg, g, shape)
+    if du is None:
+        du, ld_du = torch.empty(shape, dtype=g.dtype, device=dev), D
+    else:
+        ld_du = _token_rows("du", du, g, shape)
+    if dh0 is None:
+        dh0 = torch.empty(state, dtype=torch.float32, device=dev)
+    else:
+        _check_flat("dh0", dh0, state, torch.float32, dev)
     workspace, ws_bytes = _gated_workspace(workspace, batch, L, D, dev)
-    lib = library()
-    with torch.cuda.device(dev):
-        st = lib.jscan_gated_scan_backward(_ptr(g), _ptr(u), _ptr(y), _ptr(dy), _ptr(h0), _ptr(dh_final), _ptr(lengths),
-                                           _ptr(dg), _ptr(du), _ptr(dh0), batch, L, D, ld_g, ld_u, ld_y, ld_dy, ld_dg,
-                                           ld_du, _ptr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype],
-                                           _stream(dev))
-    _check(st)
+    _launch(library().jscan_gated_scan_backward, dev, g.data_ptr(), _addr(u), y.data_ptr(), dy.data_ptr(), _addr(h0),
+            _addr(dh_final), _addr(lengths), dg.data_ptr(), du.data_ptr(), dh0.data_ptr(), batch, L, D, ld_g, ld_u, ld_y,
+            ld_dy, ld_dg, ld_du, _addr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype])
     return dg, du, dh0
 
 
 def gated_step(h, g_t, u_t, y_t=None, form="decay"):
     """One decode token of the gated recurrence (``jscan_gated_step``): h ``[batch, D]`` fp32 is updated in
-    place; g_t, u_t ``[batch, D]`` may be strided views, e.g. ``g[:, t]``.  Returns y_t ``[batch, D]``."""
-    _require(form in GATE_FORMS, f"form must be one of {tuple(GATE_FORMS)}")
-    _require(h.is_cuda and h.dtype == torch.float32 and h.dim() == 2 and h.is_contiguous(),
-             "h must be a contiguous fp32 [batch, D] CUDA tensor")
-    batch, D = h.shape
-    _require(g_t.dtype in _DTYPES, "g_t must be bfloat16 or float32")
+    place; g_t, u_t ``[batch, D]`` may be strided views, e.g. ``g[:, t]``.  Returns y_t ``[batch, D]``: a new
+    contiguous tensor, or the given ``y_t``, whose rows may be strided too."""
+    if form not in GATE_FORMS:
+        _bad(f"form must be one of {tuple(GATE_FORMS)}")
+    if not h.is_cuda or h.dtype != torch.float32 or h.dim() != 2 or not h.is_contiguous():
+        _bad("h must be a contiguous fp32 [batch, D] CUDA tensor")
+    shape, dev, dtype = h.shape, h.device, g_t.dtype
+    batch, D = shape
+    if dtype not in _DTYPES:
+        _bad("g_t must be bfloat16 or float32")
+    if y_t is None:
+        y_t = torch.empty(shape, dtype=dtype, device=dev)
     lds = []
-    for name, t in (("g_t", g_t), ("u_t", u_t)):
-        _require(t.shape == h.shape and t.dtype == g_t.dtype and t.device == h.device,
-                 f"{name} must be {tuple(h.shape)} of dtype {g_t.dtype} on {h.device}")
-        _require(D <= 1 or t.stride(1) == 1, f"{name} rows must be contiguous")
-        lds.append(t.stride(0) if batch > 1 else D)
-    y_t, ld_y = _step_output(y_t, (batch, D), g_t.dtype, h.device)
-    lib = library()
-    with torch.cuda.device(h.device):
-        st = lib.jscan_gated_step(_ptr(h), _ptr(g_t), _ptr(u_t), _ptr(y_t), batch, D, lds[0], lds[1], ld_y,
-                                  GATE_FORMS[form], _DTYPES[g_t.dtype], _stream(h.device))
-    _check(st)
+    for name, t in (("g_t", g_t), ("u_t", u_t), ("y_t", y_t)):
+        _check_like(name, t, shape, dtype, dev)
+        ld, step = t.stride()
+        if step != 1 and D > 1:
+            _bad(f"{name} rows must be contiguous")
+        lds.append(ld if batch > 1 else D)
+    _launch(library().jscan_gated_step, dev, h.data_ptr(), g_t.data_ptr(), u_t.data_ptr(), y_t.data_ptr(), batch, D, *lds,
+            GATE_FORMS[form], _DTYPES[dtype])
     return y_t
 
 
@@ -688,31 +737,38 @@ def _row_stride(name, t):
     """The stride in elements of the rows of ``[..., K]``: contiguous rows, evenly spaced over all leading
     dimensions (contiguous, or a slice of a wider last dimension)."""
     K = t.shape[-1]
-    _require(K <= 1 or t.stride(-1) == 1, f"{name} rows must be contiguous")
+    if t.is_contiguous():
+        return K
+    if K > 1 and t.stride(-1) != 1:
+        _bad(f"{name} rows must be contiguous")
     lead = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
     for (_, outer), (n, inner) in zip(lead, lead[1:]):
-        _require(outer == n * inner or t.numel() == 0, f"{name} rows must be evenly spaced")
-    return lead[-1][1] if lead and t.numel() else K
+        if outer != n * inner:
+            _bad(f"{name} rows must be evenly spaced")
+    return lead[-1][1] if lead else K
 
 
 def quantize_rows(x, q=None, scale=None):
     """Rows of x ``[..., K]`` (bf16 or fp32, K a multiple of 16; a slice of a wider tensor too) to int8, each
     with a scale of its own (``jscan_quantize_rows``).  Returns ``(q [..., K] int8, scale [...] fp32)``: the
     first input of :func:`matmul_i8`."""
-    _require(x.is_cuda and x.dtype in _DTYPES, "x must be a bfloat16 or float32 CUDA tensor")
-    _require(x.dim() >= 1, "x must have a last dimension")
-    K, lead = x.shape[-1], x.shape[:-1]
+    if not x.is_cuda or x.dtype not in _DTYPES:
+        _bad("x must be a bfloat16 or float32 CUDA tensor")
+    if x.dim() < 1:
+        _bad("x must have a last dimension")
+    shape, dev = x.shape, x.device
+    K, lead = shape[-1], shape[:-1]
     ld_x = _row_stride("x", x)
-    M = lead.numel()
-    q = torch.empty(x.shape, dtype=torch.int8, device=x.device) if q is None else q
-    scale = torch.empty(lead, dtype=torch.float32, device=x.device) if scale is None else scale
-    for name, t, shape, dt in (("q", q, x.shape, torch.int8), ("scale", scale, lead, torch.float32)):
-        _require(t.shape == shape and t.dtype == dt and t.device == x.device and t.is_contiguous(),
-                 f"{name} must be a contiguous {dt} tensor of shape {tuple(shape)} on x's device")
-    with torch.cuda.device(x.device):
-        st = library().jscan_quantize_rows(_ptr(x), _ptr(q), _ptr(scale), M, K, ld_x, _DTYPES[x.dtype],
-                                           _stream(x.device))
-    _check(st)
+    if q is None:
+        q = torch.empty(shape, dtype=torch.int8, device=dev)
+    else:
+        _check_flat("q", q, shape, torch.int8, dev)
+    if scale is None:
+        scale = torch.empty(lead, dtype=torch.float32, device=dev)
+    else:
+        _check_flat("scale", scale, lead, torch.float32, dev)
+    _launch(library().jscan_quantize_rows, dev, x.data_ptr(), q.data_ptr(), scale.data_ptr(), lead.numel(), K, ld_x,
+            _DTYPES[x.dtype])
     return q, scale
 
 
@@ -721,24 +777,25 @@ def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
     ``[...]`` (a token each) and ``[N]`` (an output channel each) and an optional fp32 bias ``[N]``
     (``jscan_matmul_i8``).  Returns out ``[..., N]`` in out_dtype; a given ``out`` may be a slice of a wider
     tensor."""
-    _require(q.is_cuda and q.dtype == torch.int8 and q.is_contiguous() and q.dim() >= 1,
-             "q must be a contiguous int8 CUDA tensor")
-    K, lead, dev = q.shape[-1], q.shape[:-1], q.device
-    _require(w.dim() == 2 and w.shape[1] == K and w.dtype == torch.int8 and w.is_contiguous() and w.device == dev,
-             f"w must be a contiguous int8 [N, {K}] tensor on q's device")
-    N, M = w.shape[0], lead.numel()
-    for name, t, shape in (("q_scale", q_scale, lead), ("w_scale", w_scale, (N,)), ("bias", bias, (N,))):
-        _require((t is None and name == "bias") or (t.shape == shape and t.dtype == torch.float32 and t.device == dev
-                                                    and t.is_contiguous()),
-                 f"{name} must be a contiguous fp32 tensor of shape {tuple(shape)} on q's device")
+    if not q.is_cuda or q.dtype != torch.int8 or q.dim() < 1 or not q.is_contiguous():
+        _bad("q must be a contiguous int8 CUDA tensor")
+    dev, K, lead = q.device, q.shape[-1], q.shape[:-1]
+    if w.dim() != 2 or w.shape[1] != K:
+        _bad(f"w must be [N, {K}], got {tuple(w.shape)}")
+    N = w.shape[0]
+    _check_flat("w", w, (N, K), torch.int8, dev)
+    _check_flat("q_scale", q_scale, lead, torch.float32, dev)
+    _check_flat("w_scale", w_scale, (N,), torch.float32, dev)
+    _check_flat("bias", bias, (N,), torch.float32, dev)
     if out is None:
-        _require(out_dtype in _DTYPES, "out_dtype must be bfloat16 or float32")
-        out = torch.empty((*lead, N), dtype=out_dtype, device=dev)
-    _require(out.dtype in _DTYPES and out.shape == (*lead, N) and out.device == dev,
-             f"out must be a bfloat16 or float32 tensor of shape {(*lead, N)} on q's device")
-    ld_out = _row_stride("out", out)
-    with torch.cuda.device(dev):
-        st = library().jscan_matmul_i8(_ptr(q), _ptr(q_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(out), M, N, K,
-                                       ld_out, _DTYPES[out.dtype], _stream(dev))
-    _check(st)
+        if out_dtype not in _DTYPES:
+            _bad("out_dtype must be bfloat16 or float32")
+        out, ld_out = torch.empty((*lead, N), dtype=out_dtype, device=dev), N
+    else:
+        if out.dtype not in _DTYPES:
+            _bad("out must be bfloat16 or float32")
+        _check_like("out", out, (*lead, N), out.dtype, dev)
+        ld_out = _row_stride("out", out)
+    _launch(library().jscan_matmul_i8, dev, q.data_ptr(), q_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+            _addr(bias), out.data_ptr(), lead.numel(), N, K, ld_out, _DTYPES[out.dtype])
     return out

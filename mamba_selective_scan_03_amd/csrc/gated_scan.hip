@@ -46,29 +46,33 @@ struct Plan {
 
 constexpr int kRun = 8;   // tokens a thread takes of a block
 // Work-groups that keep the chip busy: below this a strip is made narrower or the tokens are cut.  1 x 4096 x 8192 bf16
-// scan: 64-lane strips (64 work-groups) 149 us, 16-lane ones (256) 59 us.
+// scan: 64-lane strips (64 work-groups) 149 us, 16-lane ones (256) 52 us.
 constexpr int64_t kEnough = 160;
 
 // Narrower strips and segments both make more work-groups.  Narrow strips read every byte once but in pieces of 64 or
 // 128 bytes a row; segments read the gate and the input twice (the maps first) in pieces of 256 bytes, with a
-// second launch.  So the widest strip that makes enough work-groups is taken, and the tokens are cut where none does.
+// second launch.  So the widest strip that makes enough work-groups is taken, and the tokens are cut where none does,
+// into about one work-group per CU (1 x 65536 x 1024: 256 work-groups 118 us, 512 121 us; backward 158 and 164 us).
 // The backward pass reads only two of its five or six tensors twice, so on long sequences cutting wins over narrow strips
-// (2 x 4096 x 4096 sigmoid: 94 us against 115 us; forward 65 us against 61 us).  Sequences of a few tokens take
-// few waves (256 x 8 x 4096: one wave 10.8 us, four 23 us, eight 44 us; 64 x 32 x 2048: 7.3, 5.6, 8.8 us).
+// (2 x 4096 x 4096 sigmoid: 96 us against 115 us; forward 60 us against 54 us).  Where even 32 lanes make thousands of
+// work-groups they are shorter and even out better (16 x 4096 x 8192: 32 lanes 580 us, 64 lanes 621 us; 8 x 4096 x
+// 8192, half as many: 309 and 307 us).  Sequences of a few tokens take few waves (256 x 8 x 4096: one wave 10.8 us, four
+// 23 us, eight 42 us; 64 x 32 x 2048: 6.2, 5.4, 8.8 us).
 // channels: per lane.  narrow: whether the lane offsets of narrow strips fit 32 bits.
 Plan plan_for(int64_t batch, int64_t L, int64_t D, int channels, bool backward, bool narrow) {
     auto groups = [&](int lanes) { return batch * ((D + lanes * channels - 1) / (lanes * channels)); };
     if (L <= kRun) return {64, 1, 1, L};
     if (L <= 4 * kRun) return {64, 4, 1, L};
+    if (narrow && groups(32) >= 2048) return {32, 8, 1, L};
     const int widths[] = {64, 32, 16};
     for (int lanes : widths) {
         if (lanes < 64 && (!narrow || (backward && L >= 2048))) break;
         if (groups(lanes) >= kEnough) return {lanes, 8, 1, L};
     }
-    // cut: segments of at least 256 tokens, whole blocks, at most 512 work-groups (two on every CU)
+    // cut: segments of at least 256 tokens, whole blocks
     const int lanes = !narrow || groups(64) * (L / 256) >= 256 ? 64 : 16;
     const int64_t block = (int64_t)(64 / lanes) * 8 * kRun;
-    int64_t n = 512 / groups(lanes);
+    int64_t n = (256 + groups(lanes) / 2) / groups(lanes);
     n = n < L / 256 ? n : L / 256;
     if (n <= 1) return {lanes, 8, 1, L};
     const int64_t seg = ((L + n - 1) / n + block - 1) / block * block;
@@ -182,14 +186,25 @@ jscan_status launch_args(const Args &a, const Pair (&t)[N], jscan_dtype dtype, j
     return launch_status();
 }
 
+// Four channels a thread where D, the strides and the addresses allow it (256 x 8192 bf16 4.8 us, 6.1 TB/s), or one
+// (256 x 8191: 6.9 us).
 template <typename E, GateForm F>
 jscan_status launch_step(float *h, const void *g, const void *u, void *y, int64_t batch, int64_t D, int64_t ld_g,
                          int64_t ld_u, int64_t ld_y, hipStream_t s) {
     using T = typename E::store_t;
-    const int blocks = (int)((D + 255) / 256);
-    hipLaunchKernelGGL((jscan::gated_step_kernel<E, F>), dim3((unsigned)(batch * blocks)), dim3(256), 0, s, h,
-                       static_cast<const T *>(g), static_cast<const T *>(u), static_cast<T *>(y), (int)D, blocks,
-                       ld_g, ld_u, ld_y);
+    constexpr int64_t kVec = 4, kBytes = kVec * (int64_t)sizeof(T);
+    const T *gt = static_cast<const T *>(g), *ut = static_cast<const T *>(u);
+    T *yt = static_cast<T *>(y);
+    if (D % kVec == 0 && ld_g % kVec == 0 && ld_u % kVec == 0 && ld_y % kVec == 0 && aligned(g, kBytes) &&
+        aligned(u, kBytes) && aligned(y, kBytes) && aligned16(h)) {
+        const int blocks = (int)((D / kVec + 255) / 256);
+        hipLaunchKernelGGL((jscan::gated_step_kernel<E, F, (int)kVec>), dim3((unsigned)(batch * blocks)), dim3(256), 0,
+                           s, h, gt, ut, yt, (int)D, blocks, ld_g, ld_u, ld_y);
+    } else {
+        const int blocks = (int)((D + 255) / 256);
+        hipLaunchKernelGGL((jscan::gated_step_kernel<E, F, 1>), dim3((unsigned)(batch * blocks)), dim3(256), 0, s, h,
+                           gt, ut, yt, (int)D, blocks, ld_g, ld_u, ld_y);
+    }
     return launch_status();
 }
 

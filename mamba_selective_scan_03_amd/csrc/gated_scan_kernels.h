@@ -201,6 +201,41 @@ template <typename V, int LC, int NW> struct Join {
     }
 };
 
+// Runs `count` blocks with one block of loads in flight: load(k, i) starts the loads of block i into buffer k,
+// scan(k, i) works on it.  Every path to a scan has the same operations behind the loads that it waits for (the other
+// buffer's loads and the stores of one block), so that the wait the compiler places there leaves all of them in
+// flight; a load under a condition would make it wait for everything.
+template <typename Load, typename Scan>
+__device__ __forceinline__ void pipelined(int64_t count, Load load, Scan scan) {
+    using B0 = IntConst<0>;
+    using B1 = IntConst<1>;
+    if (count <= 0) return;
+    load(B0{}, 0);
+    if (count == 1) {
+        scan(B0{}, 0);
+        return;
+    }
+    auto step = [&](auto next, auto current, int64_t i) {   // block i, with the loads of block i + 1 on their way
+        load(next, i + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        scan(current, i);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    step(B1{}, B0{}, 0);
+    for (int64_t i = 1;; i += 2) {
+        if (i + 1 >= count) {
+            scan(B1{}, i);
+            return;
+        }
+        step(B0{}, B1{}, i);
+        if (i + 2 >= count) {
+            scan(B0{}, i + 1);
+            return;
+        }
+        step(B1{}, B0{}, i + 1);
+    }
+}
+
 // Work-group id -> (sequence, segment, strip).  Neighbouring strips share 128-byte lines when they are narrow, so
 // consecutive strips go to work-groups of one XCD (ids 8 apart).
 struct Where {
@@ -345,8 +380,7 @@ __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typ
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int c = lane % LC, sub = lane / LC, words = D / N;
     const int cw = at.strip * LC + c;
-    const bool live = cw < words;
-    const uint32_t cl = (uint32_t)(live ? cw : words - 1);
+    const uint32_t cl = (uint32_t)min(cw, words - 1);   // lanes behind the last channel repeat it, bit for bit
     const int64_t seg0 = at.seg * sp.seg_len, seg_end = min(seg0 + sp.seg_len, L);
     const int64_t end = min(seg_end, n);   // tokens [seg0, end) are scanned, [max(seg0, n), seg_end) cleared
     Stream<V, LC, TT, false> gs(g, at.b, L, sub, cl), us(u, at.b, L, sub, cl), ys(y, at.b, L, sub, cl);
@@ -408,23 +442,17 @@ __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typ
 #pragma unroll
             for (int v = 0; v < N; ++v) s[v] = __builtin_fmaf(A[i][v], s_in[v], H[i][v]);
             if (whole) {
-                if (live) ys.store(V::pack(s), t + wave_run, n, i);
-            } else if (live && t + lane_run + i < end) {
+                ys.store(V::pack(s), t + wave_run, n, i);
+            } else if (t + lane_run + i < end) {
                 ys.store_at(V::pack(s), t + lane_run + i);
             }
         }
     };
     const int64_t blocks_n = end > seg0 ? (end - seg0) / P::kBlock : 0, tail = seg0 + blocks_n * P::kBlock;
-    if (blocks_n > 0) load(blocks[0], seg0);
-    for (int64_t t = seg0; t < tail; t += 2 * P::kBlock) {
-        if (t + P::kBlock < tail) load(blocks[1], t + P::kBlock);
-        __builtin_amdgcn_sched_barrier(0);   // the next block's loads go out before this block's arithmetic
-        scan_block(blocks[0], t, 0, std::true_type{});
-        if (t + P::kBlock >= tail) break;
-        if (t + 2 * P::kBlock < tail) load(blocks[0], t + 2 * P::kBlock);
-        __builtin_amdgcn_sched_barrier(0);
-        scan_block(blocks[1], t + P::kBlock, 1, std::true_type{});
-    }
+    pipelined(blocks_n, [&](auto k, int64_t i) { load(blocks[decltype(k)::value], seg0 + i * P::kBlock); },
+              [&](auto k, int64_t i) {
+                  scan_block(blocks[decltype(k)::value], seg0 + i * P::kBlock, decltype(k)::value, std::true_type{});
+              });
     if (tail < end) {
         Block &w = blocks[0];
         if (tail + wave_run < end) {   // waves behind the end have nothing to load
@@ -433,16 +461,12 @@ __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typ
         }
         scan_block(w, tail, (int)(blocks_n & 1), std::false_type{});
     }
-    if (writes_final && wave == NW - 1 && sub == P::kSub - 1 && live) {
+    if (writes_final && wave == NW - 1 && sub == P::kSub - 1) {
 #pragma unroll
-        for (int v = 0; v < N; ++v) h_final[at.b * D + cw * N + v] = s_end[v];
+        for (int v = 0; v < N; ++v) h_final[at.b * D + (int)cl * N + v] = s_end[v];
     }
-    if (live) {
-        float zero[N];
-#pragma unroll
-        for (int v = 0; v < N; ++v) zero[v] = 0.0f;
-        for (int64_t t = max(seg0, n) + wave * P::kSub + sub; t < seg_end; t += P::kRuns) ys.store_at(V::pack(zero), t);
-    }
+    const float zero[N] = {};
+    for (int64_t t = max(seg0, n) + wave * P::kSub + sub; t < seg_end; t += P::kRuns) ys.store_at(V::pack(zero), t);
 }
 
 // Backward pass of a strip: the scan of c from the last token down, then the gradients of each token from c of
@@ -464,8 +488,7 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int c = lane % LC, sub = lane / LC, words = D / N;
     const int cw = at.strip * LC + c;
-    const bool live = cw < words;
-    const uint32_t cl = (uint32_t)(live ? cw : words - 1);
+    const uint32_t cl = (uint32_t)min(cw, words - 1);   // lanes behind the last channel repeat it, bit for bit
     // tau counts tokens from the sequence's last one; padding is cleared by token index
     const int64_t seg0 = at.seg * sp.seg_len, seg_end = min(seg0 + sp.seg_len, L);
     const int64_t end = min(seg_end, n);
@@ -551,11 +574,9 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
                 }
             }
             if (whole) {
-                if (live) {
-                    dgs.store(V::pack(out_g), tau + wave_run, n, i);
-                    dus.store(V::pack(out_u), tau + wave_run, n, i);
-                }
-            } else if (live && tau + lane_run + i < end) {
+                dgs.store(V::pack(out_g), tau + wave_run, n, i);
+                dus.store(V::pack(out_u), tau + wave_run, n, i);
+            } else if (tau + lane_run + i < end) {
                 dgs.store_at(V::pack(out_g), t);
                 dus.store_at(V::pack(out_u), t);
             }
@@ -565,16 +586,10 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
     int64_t blocks_n = end > seg0 ? (end - seg0) / P::kBlock : 0;
     if (blocks_n > 0 && seg0 + blocks_n * P::kBlock == n) --blocks_n;
     const int64_t tail = seg0 + blocks_n * P::kBlock;
-    if (blocks_n > 0) load(blocks[0], seg0);
-    for (int64_t tau = seg0; tau < tail; tau += 2 * P::kBlock) {
-        if (tau + P::kBlock < tail) load(blocks[1], tau + P::kBlock);
-        __builtin_amdgcn_sched_barrier(0);
-        scan_block(blocks[0], tau, 0, std::true_type{});
-        if (tau + P::kBlock >= tail) break;
-        if (tau + 2 * P::kBlock < tail) load(blocks[0], tau + 2 * P::kBlock);
-        __builtin_amdgcn_sched_barrier(0);
-        scan_block(blocks[1], tau + P::kBlock, 1, std::true_type{});
-    }
+    pipelined(blocks_n, [&](auto k, int64_t i) { load(blocks[decltype(k)::value], seg0 + i * P::kBlock); },
+              [&](auto k, int64_t i) {
+                  scan_block(blocks[decltype(k)::value], seg0 + i * P::kBlock, decltype(k)::value, std::true_type{});
+              });
     if (tail < end) {
         Block &w = blocks[0];
         if (tail + wave_run < end) {
@@ -585,34 +600,48 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
         }
         scan_block(w, tail, (int)(blocks_n & 1), std::false_type{});
     }
-    if (writes_final && dh0 && wave == NW - 1 && sub == P::kSub - 1 && live) {
+    if (writes_final && dh0 && wave == NW - 1 && sub == P::kSub - 1) {
 #pragma unroll
-        for (int v = 0; v < N; ++v) dh0[at.b * D + cw * N + v] = s_end[v];
+        for (int v = 0; v < N; ++v) dh0[at.b * D + (int)cl * N + v] = s_end[v];
     }
-    if (live) {
-        float zero[N];
-#pragma unroll
-        for (int v = 0; v < N; ++v) zero[v] = 0.0f;
-        for (int64_t t = max(seg0, n) + wave * P::kSub + sub; t < seg_end; t += P::kRuns) {
-            dgs.store_at(V::pack(zero), t);
-            dus.store_at(V::pack(zero), t);
-        }
+    const float zero[N] = {};
+    for (int64_t t = max(seg0, n) + wave * P::kSub + sub; t < seg_end; t += P::kRuns) {
+        dgs.store_at(V::pack(zero), t);
+        dus.store_at(V::pack(zero), t);
     }
 }
 
-// One decode token: one thread per (sequence, channel), the state in place.
-template <typename E, GateForm F>
-__global__ __launch_bounds__(256) void gated_step_kernel(float *__restrict__ h, const typename E::store_t *g,
-                                                         const typename E::store_t *u, typename E::store_t *y, int D,
-                                                         int blocks_per_row, int64_t ld_g, int64_t ld_u,
-                                                         int64_t ld_y) {
+// One decode token, the state in place: kVec channels of one sequence per thread, in accesses of up to 16 bytes
+// where all rows start on kVec elements (14 bytes an element of bf16, 8 of them the state).
+template <typename E, GateForm F, int kVec>
+__global__ __launch_bounds__(256) void gated_step_kernel(float *__restrict__ h,
+                                                         const typename E::store_t *__restrict__ g,
+                                                         const typename E::store_t *__restrict__ u,
+                                                         typename E::store_t *__restrict__ y, int D, int blocks_per_row,
+                                                         int64_t ld_g, int64_t ld_u, int64_t ld_y) {
+    using T = typename E::store_t;
+    struct alignas(sizeof(T) * kVec) Values {
+        T v[kVec];
+    };
+    struct alignas(kVec < 4 ? 4 * kVec : 16) States {
+        float v[kVec];
+    };
     const int64_t b = blockIdx.x / blocks_per_row;
-    const int d = (int)(blockIdx.x % blocks_per_row) * 256 + threadIdx.x;
+    const int d = ((int)(blockIdx.x % blocks_per_row) * 256 + threadIdx.x) * kVec;
     if (d >= D) return;
-    const Gate k = gate<F>(E::load(g + b * ld_g + d));
-    const float v = gated_advance(h[b * D + d], k.a, gated_input<F>(k, E::load(u + b * ld_u + d)));
-    h[b * D + d] = v;
-    E::store(y + b * ld_y + d, v);
+    const Values gv = *reinterpret_cast<const Values *>(g + b * ld_g + d);
+    const Values uv = *reinterpret_cast<const Values *>(u + b * ld_u + d);
+    States *hp = reinterpret_cast<States *>(h + b * D + d);
+    States hv = *hp;
+    Values yv;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const Gate k = gate<F>(E::load(&gv.v[i]));
+        hv.v[i] = gated_advance(hv.v[i], k.a, gated_input<F>(k, E::load(&uv.v[i])));
+        E::store(&yv.v[i], hv.v[i]);
+    }
+    *hp = hv;
+    *reinterpret_cast<Values *>(y + b * ld_y + d) = yv;
 }
 
 }  // namespace jscan

@@ -20,8 +20,10 @@ void launch_quantize(const void *x, int8_t *q, float *scale, int64_t M, int64_t 
     const auto *xt = static_cast<const typename E::store_t *>(x);
     const int64_t per = 16 / (int64_t)sizeof(typename E::store_t), chunks = K / per;
     const dim3 grid((unsigned)M);
-    if (!aligned16(x) || ld_x % per != 0 || chunks > 4096)
-        hipLaunchKernelGGL(jscan::quantize_any_rows_kernel<E>, grid, dim3(256), 0, s, xt, q, scale, (int)K, ld_x);
+    if (!aligned16(x) || ld_x % per != 0)
+        hipLaunchKernelGGL((jscan::quantize_any_rows_kernel<E, false>), grid, dim3(1024), 0, s, xt, q, scale, (int)K, ld_x);
+    else if (chunks > 4096)
+        hipLaunchKernelGGL((jscan::quantize_any_rows_kernel<E, true>), grid, dim3(1024), 0, s, xt, q, scale, (int)K, ld_x);
     else if (chunks <= 128)
         hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 1, 2>), grid, dim3(64), 0, s, xt, q, scale, (int)K, ld_x);
     else if (chunks <= 512)

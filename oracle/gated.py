@@ -127,7 +127,7 @@ def quantize_rows(x):
     x = np.asarray(_f64(x), np.float32)
     with np.errstate(invalid="ignore", over="ignore"):
         amax = np.max(np.abs(x), axis=-1)
-        scale = np.maximum(amax / np.float32(127), np.float32(2.0 ** -126)).astype(np.float32)
+        scale = np.maximum(amax * (np.float32(1) / np.float32(127)), np.float32(2.0 ** -126)).astype(np.float32)
         ok = np.isfinite(x).all(axis=-1)
         scale = np.where(ok, scale, np.float32(np.nan))
         q = np.rint(x * (np.float32(1) / scale)[..., None])
