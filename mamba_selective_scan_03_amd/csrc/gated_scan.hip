@@ -45,42 +45,75 @@ struct Plan {
 };
 
 constexpr int kRun = 8;   // tokens a thread takes of a block
-// Work-groups that keep the chip busy: below this a strip is made narrower or the tokens are cut.  1 x 4096 x 8192 bf16
-// scan: 64-lane strips (64 work-groups) 149 us, 16-lane ones (256) 52 us.
-constexpr int64_t kEnough = 160;
 
 // Narrower strips and segments both make more work-groups.  Narrow strips read every byte once but in pieces of 64 or
-// 128 bytes a row; segments read the gate and the input twice (the maps first) in pieces of 256 bytes, with a
-// second launch.  So the widest strip that makes enough work-groups is taken, and the tokens are cut where none does,
-// into about one work-group per CU (1 x 65536 x 1024: 256 work-groups 118 us, 512 121 us; backward 158 and 164 us).
-// The backward pass reads only two of its five or six tensors twice, so on long sequences cutting wins over narrow strips
-// (2 x 4096 x 4096 sigmoid: 96 us against 115 us; forward 60 us against 54 us).  Where even 32 lanes make thousands of
-// work-groups they are shorter and even out better (16 x 4096 x 8192: 32 lanes 580 us, 64 lanes 621 us; 8 x 4096 x
-// 8192, half as many: 309 and 307 us).  Sequences of a few tokens take few waves (256 x 8 x 4096: one wave 10.8 us, four
-// 23 us, eight 42 us; 64 x 32 x 2048: 6.2, 5.4, 8.8 us).
-// channels: per lane.  narrow: whether the lane offsets of narrow strips fit 32 bits.
-Plan plan_for(int64_t batch, int64_t L, int64_t D, int channels, bool backward, bool narrow) {
-    auto groups = [&](int lanes) { return batch * ((D + lanes * channels - 1) / (lanes * channels)); };
+// 128 bytes a row, and a work-group has less in flight; segments read two of the tensors twice (the maps first), with a
+// second launch.  The layout is the one with the least expected time,
+//     not cut   sqrt(memory^2 + chain^2) + 1 us,        cut   max(memory, chain) + 6 us
+// where memory is the bytes at the rates that large scans reach (5.3 TB/s; 6.5 TB/s for what is read twice) and chain is
+// the time along the tokens of one CU's work-groups, taken from single ones (1 x 65536 x 1024: 6.0, 3.8, 3.0 ns a token
+// and tensor for 64, 32, 16 lanes).  What it chooses between, measured (us):
+//     2 x 4096 x 4096 sigmoid   forward   64 lanes 102, 32 lanes 65, 16 lanes 54, 64 lanes in 4 segments 57
+//                               backward  64 lanes 180, 32 lanes 119, 16 lanes 108, 64 lanes in 4 segments 95
+//     24 x 1000 x 500           forward   64 lanes 26.5, 32 lanes 19.6, 16 lanes 23.6
+//     1 x 65536 x 1024          forward   16 lanes 609, 64 lanes in 32 segments 118, in 64 segments 121
+// With thousands of work-groups the shorter ones even out better (16 x 4096 x 8192: 32 lanes 580 us, 64 lanes 621 us; 8 x
+// 4096 x 8192, half as many: 309 and 307 us).  Sequences of a few tokens take few waves (256 x 8 x 4096: one
+// wave 10.8 us, four 23 us, eight 42 us; 64 x 32 x 2048: 6.2, 5.4, 8.8 us; its backward pass 10.1, 11.9, 18.8 us).
+// channels: per lane.  tensors: rows of D elements moved per token.  narrow: whether the lane offsets of narrow strips fit
+// 32 bits.
+constexpr int64_t kLeastSegment = 256;   // tokens
+constexpr int64_t kMostGroups = 768;     // work-groups that cutting makes, at most
+
+Plan plan_for(int64_t batch, int64_t L, int64_t D, int channels, int es, int tensors, bool backward, bool narrow) {
+    auto groups_of = [&](int lanes) { return batch * ((D + lanes * channels - 1) / (lanes * channels)); };
     if (L <= kRun) return {64, 1, 1, L};
-    if (L <= 4 * kRun) return {64, 4, 1, L};
-    if (narrow && groups(32) >= 2048) return {32, 8, 1, L};
-    const int widths[] = {64, 32, 16};
-    for (int lanes : widths) {
-        if (lanes < 64 && (!narrow || (backward && L >= 2048))) break;
-        if (groups(lanes) >= kEnough) return {lanes, 8, 1, L};
+    if (L <= 4 * kRun) return {64, backward && groups_of(64) >= 512 ? 1 : 4, 1, L};
+    if (narrow && groups_of(32) >= 2048) return {32, 8, 1, L};
+    constexpr int kLanes[] = {64, 32, 16};
+    constexpr float kToken[] = {6.0e-3f, 3.8e-3f, 3.0e-3f};
+    const float elements = (float)(batch * L) * (float)D, once = elements * (float)(es * tensors) / 5.3e6f;
+    const float twice = elements * (float)(2 * es) / 6.5e6f;
+    Plan best{64, 8, 1, L};
+    float least = 0.0f;
+    for (int i = 0; i < (narrow ? 3 : 1); ++i) {
+        const int lanes = kLanes[i];
+        if (lanes > 16 && narrow && D <= lanes * channels / 2) continue;   // half the lanes would repeat a channel
+        const int64_t groups = groups_of(lanes);
+        const float token = kToken[i] * (float)tensors;
+        const int64_t block = (int64_t)(64 / lanes) * 8 * kRun;
+        auto consider = [&](int64_t n) {
+            const int64_t seg = n == 1 ? L : ((L + n - 1) / n + block - 1) / block * block, n_seg = (L + seg - 1) / seg;
+            const float chain = (float)((groups * n_seg + 255) / 256) * (float)seg * token;
+            const float both = once + twice;
+            const float us = n_seg == 1 ? __builtin_sqrtf(once * once + chain * chain) + 1.0f
+                                        : (both > chain ? both : chain) + 6.0f;
+            if (least == 0.0f || us < least) {
+                least = us;
+                best = {lanes, 8, n_seg, seg};
+            }
+        };
+        consider(1);
+        if (lanes == 32) continue;
+        for (int64_t want = 256; want <= kMostGroups; want += 256)
+            for (int64_t up = 0; up < 2; ++up) {   // just below and just above whole rounds of the CUs
+                int64_t n = want / groups + up;
+                n = n < L / kLeastSegment ? n : L / kLeastSegment;
+                if (n > 1 && n * groups <= kMostGroups) consider(n);
+            }
     }
-    // cut: segments of at least 256 tokens, whole blocks
-    const int lanes = !narrow || groups(64) * (L / 256) >= 256 ? 64 : 16;
-    const int64_t block = (int64_t)(64 / lanes) * 8 * kRun;
-    int64_t n = (256 + groups(lanes) / 2) / groups(lanes);
-    n = n < L / 256 ? n : L / 256;
-    if (n <= 1) return {lanes, 8, 1, L};
-    const int64_t seg = ((L + n - 1) / n + block - 1) / block * block;
-    return {lanes, 8, (L + seg - 1) / seg, seg};
+    return best;
 }
 
-int64_t plan_workspace(const Plan &p, int64_t batch, int64_t D) {
-    return p.n_seg > 1 ? batch * D * (p.n_seg * 8 + 4) : 0;
+// Enough for any plan: strips of 64 lanes with two channels make the fewest work-groups and so the most segments.
+int64_t most_segments(int64_t batch, int64_t L, int64_t D) {
+    const int64_t n = kMostGroups / (batch * ((D + 127) / 128));
+    return n < L / kLeastSegment ? n : L / kLeastSegment;
+}
+
+int64_t workspace_bytes_for(int64_t batch, int64_t L, int64_t D) {
+    const int64_t n = most_segments(batch, L, D);
+    return n > 1 ? batch * D * (n * 8 + 4) : 0;
 }
 
 jscan::SegSplit split_of(const Plan &p, int64_t batch, int64_t D, void *workspace) {
@@ -174,7 +207,9 @@ template <int N> bool narrow_ok(const Pair (&t)[N], int64_t es) {
 template <typename Args, int N>
 jscan_status launch_args(const Args &a, const Pair (&t)[N], jscan_dtype dtype, jscan_gate_form form, bool backward) {
     const bool two = dtype == JSCAN_BF16 && two_channels(t, a.D);
-    const Plan p = plan_for(a.batch, a.L, a.D, two ? 2 : 1, backward, narrow_ok(t, elem_bytes(dtype)));
+    const int tensors = !backward ? 3 : form == JSCAN_GATE_SIGMOID ? 6 : 5;
+    const Plan p = plan_for(a.batch, a.L, a.D, two ? 2 : 1, (int)elem_bytes(dtype), tensors, backward,
+                            narrow_ok(t, elem_bytes(dtype)));
     auto with_form = [&](auto v) {
         using V = decltype(v);
         if (form == JSCAN_GATE_DECAY) launch_plan<V, GateForm::Decay>(a, p);
@@ -223,13 +258,7 @@ extern "C" {
 int64_t jscan_gated_scan_workspace(int64_t batch, int64_t L, int64_t D) {
     if (!shape_ok(batch, L, D)) return -1;
     if (batch == 0 || D == 0) return 0;
-    int64_t most = 0;
-    for (int channels = 1; channels <= 2; ++channels)
-        for (int k = 0; k < 4; ++k) {
-            const int64_t n = plan_workspace(plan_for(batch, L, D, channels, k & 1, k & 2), batch, D);
-            most = n > most ? n : most;
-        }
-    return most;
+    return workspace_bytes_for(batch, L, D);
 }
 
 jscan_status jscan_gated_scan(const void *g, const void *u, const float *h0, const int32_t *lengths, void *y,

@@ -185,6 +185,32 @@ template <int kN> struct Columns {
     }
 };
 
+// 16 rows of kCols results from LDS (rows kRow bytes apart) to rows m0 .. and columns n0 .. of the output, a P at a
+// time, consecutive lanes to consecutive places.
+template <typename T, typename P, int kCols, int kRow>
+__device__ __forceinline__ void store_rows(T *out, const int8_t *lds, int l, int64_t m0, int64_t n0, int64_t M, int64_t N,
+                                           int64_t ld_out) {
+    constexpr int kPer = (int)(sizeof(P) / sizeof(T)), kPieces = kCols / kPer;
+    // the narrow stores are not unrolled: their many addresses would take the registers that keep two
+    // work-groups on a CU (65536 x 288 x 8192: 264 us against 186 us)
+    constexpr int kUnroll = sizeof(P) == 16 ? (16 * kPieces + 63) / 64 : 1;
+#pragma unroll kUnroll
+    for (int j = 0; j < (16 * kPieces + 63) / 64; ++j) {
+        const int c = l + 64 * j, row = c / kPieces, at = c % kPieces * kPer;
+        if (16 * kPieces % 64 != 0 && c >= 16 * kPieces) break;
+        const int64_t m = m0 + row, n = n0 + at;
+        if (m < M && n < N) {
+            const T *src = reinterpret_cast<const T *>(lds + row * kRow) + at;
+            T *dst = out + m * ld_out + n;
+            if (kPer == 1 || n + kPer <= N) {
+                *reinterpret_cast<P *>(dst) = *reinterpret_cast<const P *>(src);
+            } else {
+                for (int i = 0; i < kPer && n + i < N; ++i) dst[i] = src[i];
+            }
+        }
+    }
+}
+
 // ---- the product --------------------------------------------------------------------------------
 // w is the row operand and q the column operand, so a lane's four sums of a 16 x 16 tile are four columns n of one
 // output row m.  The rows of w that a wave's NT tiles hold are dealt out so that a lane's 4 NT columns are
@@ -223,8 +249,15 @@ __device__ __forceinline__ void block_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// waves per SIMD of the work-groups that LDS lets onto a CU
+constexpr int waves_per_simd(int waves, int lds_bytes) {
+    const int n = 163840 / lds_bytes * waves / 4;
+    return n < 1 ? 1 : n > 8 ? 8 : n;
+}
+
 template <typename E, int BM, int BN, int WR, int WC, int KG, int kBufs>
-__global__ __launch_bounds__(KG * WR * WC * 64) void matmul_i8_tiled_kernel(
+__global__ __launch_bounds__(KG * WR * WC * 64,
+                             waves_per_simd(KG * WR * WC, KG * kBufs * (BM + BN) * 128)) void matmul_i8_tiled_kernel(
     const int8_t *__restrict__ q, const float *__restrict__ sq, const int8_t *__restrict__ w,
     const float *__restrict__ sw, const float *__restrict__ bias, typename E::store_t *__restrict__ out, int64_t M,
     int64_t N, int64_t K, int64_t ld_out, int m_tiles, int n_tiles, int wide) {
@@ -327,9 +360,9 @@ __global__ __launch_bounds__(KG * WR * WC * 64) void matmul_i8_tiled_kernel(
     // Results go out through LDS, 16 rows of a wave at a time, so that a store covers whole rows of the wave's columns
     // (straight from the registers a store touches 64 pieces of 8 bytes: 16384 x 16384 x 256 took 762 us).
     using T = typename E::store_t;
-    constexpr int kCols = 16 * NT, kPerChunk = 16 / (int)sizeof(T), kChunks = kCols / kPerChunk;
+    constexpr int kCols = 16 * NT;
     constexpr int kRow = kCols * (int)sizeof(T) + 16;   // bytes, padded off the banks' period
-    static_assert(kWaves * 16 * kRow <= (int)sizeof(stages_of) && kCols % kPerChunk == 0, "the results fit the stages");
+    static_assert(kWaves * 16 * kRow <= (int)sizeof(stages_of), "the results fit the stages");
     __syncthreads();   // every wave is done with the operands
     if constexpr (KG > 1) {   // the groups' sums to group 0, which goes on alone
         i32x4_t *sums = reinterpret_cast<i32x4_t *>(&stages_of[0][0][0]);
@@ -373,21 +406,9 @@ __global__ __launch_bounds__(KG * WR * WC * 64) void matmul_i8_tiled_kernel(
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-        for (int j = 0; j < (16 * kChunks + 63) / 64; ++j) {
-            const int c = l + 64 * j, row = c / kChunks, at = c % kChunks * kPerChunk;
-            if (16 * kChunks % 64 != 0 && c >= 16 * kChunks) break;
-            const int64_t m = mu + row, n = nw + at;
-            if (m < M && n < N) {
-                const T *src = reinterpret_cast<const T *>(mine + row * kRow) + at;
-                T *dst = out + m * ld_out + n;
-                if (wide && n + kPerChunk <= N) {
-                    *reinterpret_cast<u32x4_t *>(dst) = *reinterpret_cast<const u32x4_t *>(src);
-                } else {
-                    for (int i = 0; i < kPerChunk && n + i < N; ++i) dst[i] = src[i];
-                }
-            }
-        }
+        if (wide == 16) store_rows<T, u32x4_t, kCols, kRow>(out, mine, l, mu, nw, M, N, ld_out);
+        else if (wide == 4) store_rows<T, uint32_t, kCols, kRow>(out, mine, l, mu, nw, M, N, ld_out);
+        else store_rows<T, T, kCols, kRow>(out, mine, l, mu, nw, M, N, ld_out);
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");

@@ -44,17 +44,17 @@ struct Tile {
 constexpr Tile kTiles[] = {
     {16, 16, 8, 3.0f, 0.30f, 0.105f}, {16, 32, 4, 3.0f, 0.26f, 0.14f},  {32, 32, 4, 3.0f, 0.45f, 0.14f},
     {32, 64, 4, 3.0f, 0.60f, 0.20f},  {64, 64, 1, 4.0f, 0.30f, 0.20f},  {128, 128, 1, 5.0f, 0.62f, 0.56f},
-    {256, 192, 1, 8.0f, 1.45f, 1.45f}, {256, 256, 1, 9.0f, 1.60f, 1.60f}};
+    {128, 144, 1, 5.0f, 0.66f, 0.62f}, {256, 256, 1, 9.0f, 1.60f, 1.60f}};
 
 int64_t tiles_of(const Tile &t, int64_t M, int64_t N) { return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn); }
 
 // The tile that is expected to take least: large ones read least per product, small ones fill the chip when
-// rows and columns are few, and the 192 columns leave less of a tile empty for some widths.  The larger of the
+// rows and columns are few, and the 144 columns leave less of a tile empty for some widths.  The larger of the
 // time along one work-group's stages and the time of a CU's share of all stages, on 256 CUs:
 //     1 x 4096 x 8192 (M x N x K): 16 x 16 tiles 5.8 us, 16 x 32 7.9, 64 x 64 22
 //     77 x 4096 x 8192: 32 x 64 12 us, 32 x 32 18, 64 x 64 20, 128 x 128 40
-//     512 x 16384 x 4096: 128 x 128 37 us, 256 x 192 49, 256 x 256 55, 64 x 64 52
-//     65536 x 288 x 8192: 256 x 192 206 us, 128 x 128 231, 256 x 256 237
+//     512 x 16384 x 4096: 128 x 128 37 us, 256 x 256 55, 64 x 64 52
+//     65536 x 288 x 8192: 128 x 144 181 us, 128 x 128 231, 256 x 256 227
 int choose_tile(int64_t M, int64_t N, int64_t K) {
     const int64_t stages = (K + 127) / 128;
     int best = 0;
@@ -82,7 +82,9 @@ struct MatmulArgs {
 template <typename E, int BM, int BN, int WR, int WC, int KG, int kBufs> void launch_tiled(const MatmulArgs &a) {
     using T = typename E::store_t;
     const int m_tiles = (int)((a.M + BM - 1) / BM), n_tiles = (int)((a.N + BN - 1) / BN);
-    const int wide = aligned16(a.out) && a.ld_out * (int64_t)sizeof(T) % 16 == 0;
+    // the widest store that every output row starts on
+    const uint64_t start = reinterpret_cast<uint64_t>(a.out) | (uint64_t)(a.ld_out * (int64_t)sizeof(T));
+    const int wide = start % 16 == 0 ? 16 : start % 4 == 0 ? 4 : 2;
     hipLaunchKernelGGL((jscan::matmul_i8_tiled_kernel<E, BM, BN, WR, WC, KG, kBufs>),
                        dim3((unsigned)((int64_t)m_tiles * n_tiles)), dim3(KG * WR * WC * 64), 0, a.stream, a.q, a.sq,
                        a.w, a.sw, a.bias, static_cast<T *>(a.out), a.M, a.N, a.K, a.ld_out, m_tiles, n_tiles, wide);
@@ -96,8 +98,8 @@ template <typename E> void launch_matmul(const MatmulArgs &a) {
     case 3: launch_tiled<E, 32, 64, 1, 2, 4, 3>(a); break;
     case 4: launch_tiled<E, 64, 64, 2, 2, 1, 3>(a); break;
     case 5: launch_tiled<E, 128, 128, 2, 2, 1, 2>(a); break;
-    case 6: launch_tiled<E, 256, 192, 4, 2, 1, 2>(a); break;
-    default: launch_tiled<E, 256, 256, 2, 4, 1, 2>(a); break;
+    case 6: launch_tiled<E, 128, 144, 4, 1, 1, 2>(a); break;
+    default: launch_tiled<E, 256, 256, 4, 4, 1, 2>(a); break;
     }
 }
 
