@@ -560,18 +560,20 @@ GATE_FORMS = {"decay": 0, "sigmoid": 1}
 # A decode token's kernels take a few microseconds, as much as a handful of Python calls: the checks below
 # build their messages only when they fail, and a launch asks for the raw stream and changes the current
 # device only where it has to.
+_F32, _I8, _I32 = torch.float32, torch.int8, torch.int32
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _launch(fn, dev, *args):
-    """``fn(*args, stream)`` on dev's current stream, with dev current; raises on an error status."""
+def _launch(name, dev, *args):
+    """Library function `name` on args and dev's current stream, with dev current; raises on an error status."""
+    fn = getattr(_lib or library(), name)
     index = dev.index
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch._C._cuda_getDevice():
-        status = fn(*args, stream)
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, stream)
-    if status != 0:
+            status = fn(*args, _raw_stream(index))
+    if status:
         _check(status)
 
 
@@ -586,6 +588,13 @@ def _bad(msg: str):
 def _check_like(name, t, shape, dtype, dev):
     if t.shape != shape or t.dtype != dtype or t.device != dev:
         _bad(f"{name} must have shape {tuple(shape)} and be {dtype} on {dev}, got {tuple(t.shape)}, {t.dtype}, {t.device}")
+
+
+def _matrix(name, t, shape, dtype, dev):
+    """The strides of a matrix of this shape."""
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        _check_like(name, t, shape, dtype, dev)
+    return t.stride()
 
 
 def _check_flat(name, t, shape, dtype, dev):
@@ -620,7 +629,7 @@ def _check_gated(g, form, lengths):
         _bad("g must be bfloat16 or float32")
     if g.dim() != 3:
         _bad("g must be [batch, L, D]")
-    _check_flat("lengths", lengths, g.shape[:1], torch.int32, g.device)
+    _check_flat("lengths", lengths, g.shape[:1], _I32, g.device)
 
 
 def gated_scan_workspace_bytes(batch: int, L: int, D: int) -> int:
@@ -653,17 +662,17 @@ def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, 
     batch, L, D = shape
     ld_g, ld_u = _token_rows("g", g, g, shape), _token_rows("u", u, g, shape)
     state = (batch, D)
-    _check_flat("h0", h0, state, torch.float32, dev)
+    _check_flat("h0", h0, state, _F32, dev)
     if y is None:
         y, ld_y = torch.empty(shape, dtype=g.dtype, device=dev), D
     else:
         ld_y = _token_rows("y", y, g, shape)
     if h_final is None:
-        h_final = torch.empty(state, dtype=torch.float32, device=dev)
+        h_final = torch.empty(state, dtype=_F32, device=dev)
     else:
-        _check_flat("h_final", h_final, state, torch.float32, dev)
+        _check_flat("h_final", h_final, state, _F32, dev)
     workspace, ws_bytes = _gated_workspace(workspace, batch, L, D, dev)
-    _launch(library().jscan_gated_scan, dev, g.data_ptr(), u.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
+    _launch("jscan_gated_scan", dev, g.data_ptr(), u.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
             h_final.data_ptr(), batch, L, D, ld_g, ld_u, ld_y, _addr(workspace), ws_bytes, GATE_FORMS[form],
             _DTYPES[g.dtype])
     return y, h_final
@@ -683,8 +692,8 @@ def gated_scan_backward(g, u, y, dy, h0=None, dh_final=None, lengths=None, form=
     ld_g, ld_y, ld_dy = _token_rows("g", g, g, shape), _token_rows("y", y, g, shape), _token_rows("dy", dy, g, shape)
     ld_u = D if u is None else _token_rows("u", u, g, shape)
     state = (batch, D)
-    _check_flat("h0", h0, state, torch.float32, dev)
-    _check_flat("dh_final", dh_final, state, torch.float32, dev)
+    _check_flat("h0", h0, state, _F32, dev)
+    _check_flat("dh_final", dh_final, state, _F32, dev)
     if dg is None:
         dg, ld_dg = torch.empty(shape, dtype=g.dtype, device=dev), D
     else:
@@ -694,11 +703,11 @@ def gated_scan_backward(g, u, y, dy, h0=None, dh_final=None, lengths=None, form=
     else:
         ld_du = _token_rows("du", du, g, shape)
     if dh0 is None:
-        dh0 = torch.empty(state, dtype=torch.float32, device=dev)
+        dh0 = torch.empty(state, dtype=_F32, device=dev)
     else:
-        _check_flat("dh0", dh0, state, torch.float32, dev)
+        _check_flat("dh0", dh0, state, _F32, dev)
     workspace, ws_bytes = _gated_workspace(workspace, batch, L, D, dev)
-    _launch(library().jscan_gated_scan_backward, dev, g.data_ptr(), _addr(u), y.data_ptr(), dy.data_ptr(), _addr(h0),
+    _launch("jscan_gated_scan_backward", dev, g.data_ptr(), _addr(u), y.data_ptr(), dy.data_ptr(), _addr(h0),
             _addr(dh_final), _addr(lengths), dg.data_ptr(), du.data_ptr(), dh0.data_ptr(), batch, L, D, ld_g, ld_u, ld_y,
             ld_dy, ld_dg, ld_du, _addr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype])
     return dg, du, dh0
@@ -708,25 +717,25 @@ def gated_step(h, g_t, u_t, y_t=None, form="decay"):
     """One decode token of the gated recurrence (``jscan_gated_step``): h ``[batch, D]`` fp32 is updated in
     place; g_t, u_t ``[batch, D]`` may be strided views, e.g. ``g[:, t]``.  Returns y_t ``[batch, D]``: a new
     contiguous tensor, or the given ``y_t``, whose rows may be strided too."""
-    if form not in GATE_FORMS:
+    code = GATE_FORMS.get(form)
+    if code is None:
         _bad(f"form must be one of {tuple(GATE_FORMS)}")
-    if not h.is_cuda or h.dtype != torch.float32 or h.dim() != 2 or not h.is_contiguous():
+    if not h.is_cuda or h.dtype != _F32 or h.dim() != 2 or not h.is_contiguous():
         _bad("h must be a contiguous fp32 [batch, D] CUDA tensor")
     shape, dev, dtype = h.shape, h.device, g_t.dtype
-    batch, D = shape
     if dtype not in _DTYPES:
         _bad("g_t must be bfloat16 or float32")
     if y_t is None:
         y_t = torch.empty(shape, dtype=dtype, device=dev)
-    lds = []
-    for name, t in (("g_t", g_t), ("u_t", u_t), ("y_t", y_t)):
-        _check_like(name, t, shape, dtype, dev)
-        ld, step = t.stride()
-        if step != 1 and D > 1:
-            _bad(f"{name} rows must be contiguous")
-        lds.append(ld if batch > 1 else D)
-    _launch(library().jscan_gated_step, dev, h.data_ptr(), g_t.data_ptr(), u_t.data_ptr(), y_t.data_ptr(), batch, D, *lds,
-            GATE_FORMS[form], _DTYPES[dtype])
+    batch, D = shape
+    (ld_g, one_g), (ld_u, one_u), (ld_y, one_y) = _matrix("g_t", g_t, shape, dtype, dev), \
+        _matrix("u_t", u_t, shape, dtype, dev), _matrix("y_t", y_t, shape, dtype, dev)
+    if D > 1 and not one_g == one_u == one_y == 1:
+        _bad("the rows of g_t, u_t and y_t must be contiguous")
+    if batch <= 1:
+        ld_g = ld_u = ld_y = D
+    _launch("jscan_gated_step", dev, h.data_ptr(), g_t.data_ptr(), u_t.data_ptr(), y_t.data_ptr(), batch, D, ld_g, ld_u, ld_y,
+            code, _DTYPES[dtype])
     return y_t
 
 
@@ -760,14 +769,14 @@ def quantize_rows(x, q=None, scale=None):
     K, lead = shape[-1], shape[:-1]
     ld_x = _row_stride("x", x)
     if q is None:
-        q = torch.empty(shape, dtype=torch.int8, device=dev)
+        q = torch.empty(shape, dtype=_I8, device=dev)
     else:
-        _check_flat("q", q, shape, torch.int8, dev)
+        _check_flat("q", q, shape, _I8, dev)
     if scale is None:
-        scale = torch.empty(lead, dtype=torch.float32, device=dev)
+        scale = torch.empty(lead, dtype=_F32, device=dev)
     else:
-        _check_flat("scale", scale, lead, torch.float32, dev)
-    _launch(library().jscan_quantize_rows, dev, x.data_ptr(), q.data_ptr(), scale.data_ptr(), lead.numel(), K, ld_x,
+        _check_flat("scale", scale, lead, _F32, dev)
+    _launch("jscan_quantize_rows", dev, x.data_ptr(), q.data_ptr(), scale.data_ptr(), lead.numel(), K, ld_x,
             _DTYPES[x.dtype])
     return q, scale
 
@@ -783,10 +792,10 @@ def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
     if w.dim() != 2 or w.shape[1] != K:
         _bad(f"w must be [N, {K}], got {tuple(w.shape)}")
     N = w.shape[0]
-    _check_flat("w", w, (N, K), torch.int8, dev)
-    _check_flat("q_scale", q_scale, lead, torch.float32, dev)
-    _check_flat("w_scale", w_scale, (N,), torch.float32, dev)
-    _check_flat("bias", bias, (N,), torch.float32, dev)
+    _check_flat("w", w, (N, K), _I8, dev)
+    _check_flat("q_scale", q_scale, lead, _F32, dev)
+    _check_flat("w_scale", w_scale, (N,), _F32, dev)
+    _check_flat("bias", bias, (N,), _F32, dev)
     if out is None:
         if out_dtype not in _DTYPES:
             _bad("out_dtype must be bfloat16 or float32")
@@ -796,6 +805,6 @@ def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
             _bad("out must be bfloat16 or float32")
         _check_like("out", out, (*lead, N), out.dtype, dev)
         ld_out = _row_stride("out", out)
-    _launch(library().jscan_matmul_i8, dev, q.data_ptr(), q_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+    _launch("jscan_matmul_i8", dev, q.data_ptr(), q_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
             _addr(bias), out.data_ptr(), lead.numel(), N, K, ld_out, _DTYPES[out.dtype])
     return out
