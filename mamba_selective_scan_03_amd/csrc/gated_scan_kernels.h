@@ -85,8 +85,9 @@ template <typename V, int LC, int NW, int TT> struct Place {
 };
 
 // One tensor's rows as a strip walks them in scan order (kRev: from the last token down).  A row's address is
-// a wave-uniform part and a 32-bit lane part (channel, and the lane's run inside the wave).
-template <typename V, int LC, int TT, bool kRev> struct Stream {
+// a wave-uniform part and a 32-bit lane part (channel, and the lane's run inside the wave).  kNt: whole blocks go by with
+// the non-temporal hint.
+template <typename V, int LC, int TT, bool kRev, bool kNt> struct Stream {
     using word = typename V::word;
     char *base;          // row of token 0 of the sequence, channel 0
     int64_t ld;          // bytes between rows
@@ -109,8 +110,11 @@ template <typename V, int LC, int TT, bool kRev> struct Stream {
     }
     __device__ __forceinline__ void load(word (&w)[TT], int64_t tau, int64_t n, int shift) const {
 #pragma unroll
-        for (int i = 0; i < TT; ++i)
-            w[i] = __builtin_nontemporal_load(reinterpret_cast<const word *>(row(tau, n, i) + shift * ld + lane_off));
+        for (int i = 0; i < TT; ++i) {
+            const word *p = reinterpret_cast<const word *>(row(tau, n, i) + shift * ld + lane_off);
+            if constexpr (kNt) w[i] = __builtin_nontemporal_load(p);
+            else w[i] = *p;
+        }
     }
     // The same near the ends: token by token, tokens outside [lo, hi] taken at the nearer end.
     __device__ __forceinline__ void load_clamped(word (&w)[TT], int64_t lane_tau, int64_t n, int shift, int64_t lo,
@@ -123,7 +127,9 @@ template <typename V, int LC, int TT, bool kRev> struct Stream {
         }
     }
     __device__ __forceinline__ void store(word v, int64_t tau, int64_t n, int i) const {
-        __builtin_nontemporal_store(v, reinterpret_cast<word *>(row(tau, n, i) + lane_off));
+        word *p = reinterpret_cast<word *>(row(tau, n, i) + lane_off);
+        if constexpr (kNt) __builtin_nontemporal_store(v, p);
+        else *p = v;
     }
     __device__ __forceinline__ void store_at(word v, int64_t t) const {
         *reinterpret_cast<word *>(base + t * ld + chan_off) = v;
@@ -313,7 +319,7 @@ __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const 
     if (tau0 + sp.seg_len > n) return;   // never read: no token lies behind a segment that is not whole
     const int64_t per = sp.seg_len / P::kRuns;   // tokens per thread, a multiple of TT
     const uint32_t cl = (uint32_t)(live ? cw : words - 1);
-    Stream<V, LC, TT, kRev> gs(g, at.b, L, sub, cl), xs(x, at.b, L, sub, cl);
+    Stream<V, LC, TT, kRev, false> gs(g, at.b, L, sub, cl), xs(x, at.b, L, sub, cl);
     const int64_t lane_tau = tau0 + (wave * P::kSub + sub) * per;
 
     Map<N> run;
@@ -364,7 +370,7 @@ __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const 
 }
 
 // Forward scan of a strip.
-template <typename V, GateForm F, int LC, int NW, int TT>
+template <typename V, GateForm F, int LC, int NW, int TT, bool kNt>
 __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typename V::store_t> g,
                                                              TokenRows<const typename V::store_t> u, const float *h0,
                                                              const int32_t *__restrict__ lengths,
@@ -383,7 +389,7 @@ __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typ
     const uint32_t cl = (uint32_t)min(cw, words - 1);   // lanes behind the last channel repeat it, bit for bit
     const int64_t seg0 = at.seg * sp.seg_len, seg_end = min(seg0 + sp.seg_len, L);
     const int64_t end = min(seg_end, n);   // tokens [seg0, end) are scanned, [max(seg0, n), seg_end) cleared
-    Stream<V, LC, TT, false> gs(g, at.b, L, sub, cl), us(u, at.b, L, sub, cl), ys(y, at.b, L, sub, cl);
+    Stream<V, LC, TT, false, kNt> gs(g, at.b, L, sub, cl), us(u, at.b, L, sub, cl), ys(y, at.b, L, sub, cl);
 
     // the segment's starting state; the segment with the last token (the first one of an empty sequence) ends with
     // the final state
@@ -471,7 +477,7 @@ __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typ
 
 // Backward pass of a strip: the scan of c from the last token down, then the gradients of each token from c of
 // the token after it and h of the token before it.
-template <typename V, GateForm F, int LC, int NW, int TT>
+template <typename V, GateForm F, int LC, int NW, int TT, bool kNt>
 __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
     TokenRows<const typename V::store_t> g, TokenRows<const typename V::store_t> u,
     TokenRows<const typename V::store_t> y, TokenRows<const typename V::store_t> dy, const float *__restrict__ h0,
@@ -492,7 +498,7 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
     // tau counts tokens from the sequence's last one; padding is cleared by token index
     const int64_t seg0 = at.seg * sp.seg_len, seg_end = min(seg0 + sp.seg_len, L);
     const int64_t end = min(seg_end, n);
-    Stream<V, LC, TT, true> gs(g, at.b, L, sub, cl), us(kSig ? u : g, at.b, L, sub, cl), hs(y, at.b, L, sub, cl),
+    Stream<V, LC, TT, true, kNt> gs(g, at.b, L, sub, cl), us(kSig ? u : g, at.b, L, sub, cl), hs(y, at.b, L, sub, cl),
         ds(dy, at.b, L, sub, cl), dgs(dg, at.b, L, sub, cl), dus(du, at.b, L, sub, cl);
 
     float s_end[N];

@@ -249,6 +249,10 @@ __device__ __forceinline__ void block_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// s_waitcnt operand that leaves n vector-memory operations in flight (gfx9: bits 0-3 and 14-15 of the
+// count; the expcnt and lgkmcnt fields at their maxima do not wait).
+template <int n> constexpr int vmcnt_at_most() { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+
 // waves per SIMD of the work-groups that LDS lets onto a CU
 constexpr int waves_per_simd(int waves, int lds_bytes) {
     const int n = 163840 / lds_bytes * waves / 4;
@@ -329,8 +333,8 @@ __global__ __launch_bounds__(KG * WR * WC * 64,
     for (int64_t round = 0; round < rounds; ++round) {
         const int64_t st = round * KG + kg;
         // this wave's loads of the stage have landed; those of the kBufs - 2 stages behind it may be in flight
-        if (kBufs > 2 && st + (kBufs - 2) * KG < stages) __builtin_amdgcn_s_waitcnt(vmcnt_only<(kBufs - 2) * kPer>());
-        else __builtin_amdgcn_s_waitcnt(vmcnt_only<0>());
+        if (kBufs > 2 && st + (kBufs - 2) * KG < stages) __builtin_amdgcn_s_waitcnt(vmcnt_at_most<(kBufs - 2) * kPer>());
+        else __builtin_amdgcn_s_waitcnt(vmcnt_at_most<0>());
         block_barrier();   // every wave's part is in; every wave is done with the stage before
         const int next = buf == 0 ? kBufs - 1 : buf - 1;   // the buffer of the stage before
         if (st + (kBufs - 1) * KG < stages) dma((st + (kBufs - 1) * KG) * kStage, next);

@@ -27,10 +27,6 @@ __device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// vmcnt for an s_waitcnt that leaves `n` vector-memory operations outstanding (gfx9 encoding:
-// low four bits and bits 14-15; expcnt and lgkmcnt at their maxima, so they do not wait).
-template <int n> constexpr int vmcnt_only() { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
-
 // softplus(z) = log(1 + e^z) = max(z, 0) + log1p(e^-|z|), with t = e^-|z| in (0, 1].
 // log1p(t) is the hardware log2 of 1 + t, except below t = 2^-10, where 1 + t would lose t's
 // low bits and log1p(t) = t (1 - t/2 + ...) is t to within t/2 <= 2^-11 relative, below the

@@ -59,6 +59,10 @@ __device__ __forceinline__ void lds_dma16_nt(const void *src, uint32_t lds) {
 }
 #pragma clang diagnostic pop
 
+// vmcnt for an s_waitcnt that leaves `n` vector-memory operations outstanding (gfx9 encoding:
+// low four bits and bits 14-15; expcnt and lgkmcnt at their maxima, so they do not wait).
+template <int n> constexpr int vmcnt_only() { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+
 // x projection: one work-group = 256 rows (tokens) x all R + 2N output columns.  Its waves form
 // a (256 / 16 kRT) x 2 grid: wave (wr, wc) owns kRT 16-row tiles (rows 16 kRT wr ..) and the
 // half wc of the CT = R / 16 + 2 column tiles (d_low's R / 16 tiles, then one each of B and
