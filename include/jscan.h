@@ -416,8 +416,9 @@ jscan_status jscan_prefill_chunked_noalloc(const void *x, const void *delta, con
  *     JSCAN_GATE_DECAY     h_t = exp(g_t) h_{t-1} + u_t                          (g a log decay)
  *     JSCAN_GATE_SIGMOID   h_t = sigmoid(g_t) h_{t-1} + (1 - sigmoid(g_t)) u_t   (g a gate logit)
  *     y_t = h_t, rounded to nearest even to the dtype
- * g = -inf drops the state before the token (a reset inside a row); gates that make the recurrence
- * unstable (g > 0 in the decay form) are not checked.
+ * g = -inf drops the state before the token (a reset inside a row).  Gates that make the recurrence
+ * unstable (g > 0 in the decay form) are not checked; the decays of any run of tokens have to multiply to
+ * a finite fp32 number.
  *
  * Scan over whole sequences.
  *   g, u, y   batch * L token rows of D values in `dtype`; the row of token t of sequence b starts at
@@ -504,7 +505,8 @@ jscan_status jscan_quantize_rows(const void *x, int8_t *q, float *scale, int64_t
  *   q [M][K], w [N][K]   int8, 16-byte aligned;   q_scale [M], w_scale [N] fp32
  *   bias                 [N] fp32 or NULL
  *   out                  M rows of N values in `dtype`, row stride ld_out >= N elements
- * K a multiple of 16, 16 <= K <= 131056; 0 <= M <= 2^30; 0 <= N <= 2^24 (at most 2^30 tiles of 16 x 16).
+ * K a multiple of 16, 16 <= K <= 131056; 0 <= M <= 2^30; 0 <= N <= 2^24; products
+ * of more results than the tiles' grids count (about 2^38) are JSCAN_ERR_SHAPE.
  */
 jscan_status jscan_matmul_i8(const int8_t *q, const float *q_scale, const int8_t *w,
                              const float *w_scale, const float *bias, void *out, int64_t M, int64_t N,

@@ -129,6 +129,11 @@ template <typename V> TokenRows<typename V::store_t> out_rows(Pair t) {
     return {static_cast<typename V::store_t *>(const_cast<void *>(t.p)), t.ld};
 }
 
+Pair from_row(Pair t, int64_t row, int64_t es) {
+    return {t.p ? static_cast<const char *>(t.p) + row * t.ld * es : nullptr, t.ld};
+}
+template <typename T> T *from(T *p, int64_t i) { return p ? p + i : nullptr; }
+
 struct ScanArgs {
     Pair g, u, y;
     const float *h0;
@@ -137,6 +142,11 @@ struct ScanArgs {
     int64_t batch, L, D;
     void *workspace;
     hipStream_t stream;
+
+    ScanArgs sequences(int64_t b, int64_t n, int64_t es) const {   // the call on sequences b .. b + n - 1
+        return {from_row(g, b * L, es), from_row(u, b * L, es), from_row(y, b * L, es), from(h0, b * D), from(lengths, b),
+                from(h_final, b * D),   n, L, D, workspace, stream};
+    }
 };
 
 struct BackwardArgs {
@@ -147,6 +157,12 @@ struct BackwardArgs {
     int64_t batch, L, D;
     void *workspace;
     hipStream_t stream;
+
+    BackwardArgs sequences(int64_t b, int64_t n, int64_t es) const {
+        return {from_row(g, b * L, es),  from_row(u, b * L, es),  from_row(y, b * L, es), from_row(dy, b * L, es),
+                from_row(dg, b * L, es), from_row(du, b * L, es), from(h0, b * D),        from(dh_final, b * D),
+                from(lengths, b),        from(dh0, b * D),        n, L, D, workspace, stream};
+    }
 };
 
 template <typename V, GateForm F, int LC, int NW, bool kRev>
@@ -225,10 +241,17 @@ jscan_status launch_args(const Args &a, const Pair (&t)[N], jscan_dtype dtype, j
     const int64_t es = elem_bytes(dtype);
     Plan p = plan_for(a.batch, a.L, a.D, two ? 2 : 1, (int)es, tensors, backward, narrow_ok(t, es));
     p.stream = whole_lines(t, es) && a.batch * a.L * a.D * es * tensors > kStreamBytes;
+    // a plan's work-items per sequence; as many sequences a launch as it can count (all but for enormous batches, whose
+    // tokens are not cut)
+    const int64_t channels = two ? 2 : 1, strips = (a.D + p.lanes * channels - 1) / (p.lanes * channels);
+    const int64_t most = kMaxItems / (strips * p.n_seg * p.waves * 64);
     auto with_form = [&](auto v) {
         using V = decltype(v);
-        if (form == JSCAN_GATE_DECAY) launch_plan<V, GateForm::Decay>(a, p);
-        else launch_plan<V, GateForm::Sigmoid>(a, p);
+        for (int64_t b = 0; b < a.batch; b += most) {
+            const Args part = b == 0 && a.batch <= most ? a : a.sequences(b, a.batch - b < most ? a.batch - b : most, es);
+            if (form == JSCAN_GATE_DECAY) launch_plan<V, GateForm::Decay>(part, p);
+            else launch_plan<V, GateForm::Sigmoid>(part, p);
+        }
     };
     if (two) with_form(jscan::Bf16x2{});
     else if (dtype == JSCAN_BF16) with_form(jscan::Bf16x1{});
@@ -245,15 +268,18 @@ jscan_status launch_step(float *h, const void *g, const void *u, void *y, int64_
     constexpr int64_t kVec = 4, kBytes = kVec * (int64_t)sizeof(T);
     const T *gt = static_cast<const T *>(g), *ut = static_cast<const T *>(u);
     T *yt = static_cast<T *>(y);
-    if (D % kVec == 0 && ld_g % kVec == 0 && ld_u % kVec == 0 && ld_y % kVec == 0 && aligned(g, kBytes) &&
-        aligned(u, kBytes) && aligned(y, kBytes) && aligned16(h)) {
-        const int blocks = (int)((D / kVec + 255) / 256);
-        hipLaunchKernelGGL((jscan::gated_step_kernel<E, F, (int)kVec>), dim3((unsigned)(batch * blocks)), dim3(256), 0,
-                           s, h, gt, ut, yt, (int)D, blocks, ld_g, ld_u, ld_y);
-    } else {
-        const int blocks = (int)((D + 255) / 256);
-        hipLaunchKernelGGL((jscan::gated_step_kernel<E, F, 1>), dim3((unsigned)(batch * blocks)), dim3(256), 0, s, h,
-                           gt, ut, yt, (int)D, blocks, ld_g, ld_u, ld_y);
+    const bool wide = D % kVec == 0 && ld_g % kVec == 0 && ld_u % kVec == 0 && ld_y % kVec == 0 && aligned(g, kBytes) &&
+                      aligned(u, kBytes) && aligned(y, kBytes) && aligned16(h);
+    const int64_t per = wide ? 256 * kVec : 256, blocks = (D + per - 1) / per, most = kMaxItems / (blocks * 256);
+    for (int64_t b = 0; b < batch; b += most) {   // as many sequences a launch as it can count
+        const dim3 grid((unsigned)((batch - b < most ? batch - b : most) * blocks));
+        const T *gb = gt + b * ld_g, *ub = ut + b * ld_u;
+        if (wide)
+            hipLaunchKernelGGL((jscan::gated_step_kernel<E, F, (int)kVec>), grid, dim3(256), 0, s, h + b * D, gb, ub,
+                               yt + b * ld_y, (int)D, (int)blocks, ld_g, ld_u, ld_y);
+        else
+            hipLaunchKernelGGL((jscan::gated_step_kernel<E, F, 1>), grid, dim3(256), 0, s, h + b * D, gb, ub,
+                               yt + b * ld_y, (int)D, (int)blocks, ld_g, ld_u, ld_y);
     }
     return launch_status();
 }

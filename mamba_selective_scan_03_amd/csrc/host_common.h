@@ -63,5 +63,8 @@ inline jscan_status launch_status() {
 // Largest grid the launchers accept (work-group counts and row indices are 32-bit ints).
 constexpr int64_t kMaxBlocks = (int64_t)1 << 30;
 
+// Work-items that one dimension of a launch can count.
+constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;
+
 }  // namespace host
 }  // namespace jscan

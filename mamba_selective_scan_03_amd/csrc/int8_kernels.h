@@ -73,10 +73,11 @@ __device__ __forceinline__ uint32_t pack4(const float *v, float r) {
 template <typename E, int kWaves, int kChunks>
 __global__ __launch_bounds__(kWaves * 64) void quantize_rows_kernel(const typename E::store_t *__restrict__ x,
                                                                     int8_t *__restrict__ q, float *__restrict__ scale,
-                                                                    int K, int64_t ld_x) {
+                                                                    int64_t M, int K, int64_t ld_x) {
     using C = quant::Chunk<E>;
     __shared__ float part[kWaves];
-    const int64_t m = blockIdx.x;
+    const int64_t m = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (m >= M) return;
     const int chunks = K / C::n;
     const u32x4_t *row = reinterpret_cast<const u32x4_t *>(x + m * ld_x);
     u32x4_t w[kChunks];
@@ -118,11 +119,12 @@ __global__ __launch_bounds__(kWaves * 64) void quantize_rows_kernel(const typena
 template <typename E, bool kChunked>
 __global__ __launch_bounds__(1024) void quantize_any_rows_kernel(const typename E::store_t *__restrict__ x,
                                                                  int8_t *__restrict__ q, float *__restrict__ scale,
-                                                                 int K, int64_t ld_x) {
+                                                                 int64_t M, int K, int64_t ld_x) {
     using C = quant::Chunk<E>;
     constexpr int n = kChunked ? C::n : 1;
     __shared__ float part[16];
-    const int64_t m = blockIdx.x;
+    const int64_t m = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (m >= M) return;
     const typename E::store_t *row = x + m * ld_x;
     auto load = [&](int k, float (&v)[n]) {
         if constexpr (kChunked) C::unpack(*reinterpret_cast<const u32x4_t *>(row + k), v);

@@ -19,32 +19,35 @@ template <typename E>
 void launch_quantize(const void *x, int8_t *q, float *scale, int64_t M, int64_t K, int64_t ld_x, hipStream_t s) {
     const auto *xt = static_cast<const typename E::store_t *>(x);
     const int64_t per = 16 / (int64_t)sizeof(typename E::store_t), chunks = K / per;
-    const dim3 grid((unsigned)M);
+    // rows over both dimensions: one dimension counts 2^32 work-items
+    const int64_t across = M < (1 << 20) ? M : (1 << 20);
+    const dim3 grid((unsigned)across, (unsigned)((M + across - 1) / across));
     if (!aligned16(x) || ld_x % per != 0)
-        hipLaunchKernelGGL((jscan::quantize_any_rows_kernel<E, false>), grid, dim3(1024), 0, s, xt, q, scale, (int)K, ld_x);
+        hipLaunchKernelGGL((jscan::quantize_any_rows_kernel<E, false>), grid, dim3(1024), 0, s, xt, q, scale, M, (int)K, ld_x);
     else if (chunks > 4096)
-        hipLaunchKernelGGL((jscan::quantize_any_rows_kernel<E, true>), grid, dim3(1024), 0, s, xt, q, scale, (int)K, ld_x);
+        hipLaunchKernelGGL((jscan::quantize_any_rows_kernel<E, true>), grid, dim3(1024), 0, s, xt, q, scale, M, (int)K, ld_x);
     else if (chunks <= 128)
-        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 1, 2>), grid, dim3(64), 0, s, xt, q, scale, (int)K, ld_x);
+        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 1, 2>), grid, dim3(64), 0, s, xt, q, scale, M, (int)K, ld_x);
     else if (chunks <= 512)
-        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 4, 2>), grid, dim3(256), 0, s, xt, q, scale, (int)K, ld_x);
+        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 4, 2>), grid, dim3(256), 0, s, xt, q, scale, M, (int)K, ld_x);
     else if (chunks <= 1024)
-        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 4, 4>), grid, dim3(256), 0, s, xt, q, scale, (int)K, ld_x);
+        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 4, 4>), grid, dim3(256), 0, s, xt, q, scale, M, (int)K, ld_x);
     else
-        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 16, 4>), grid, dim3(1024), 0, s, xt, q, scale, (int)K, ld_x);
+        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 16, 4>), grid, dim3(1024), 0, s, xt, q, scale, M, (int)K, ld_x);
 }
 
 // The tiles of the product and what they take, measured on this chip (us, bf16 output): `fixed` of a call, `round`
 // between two stages of one work-group that is alone on its CU, `stage` of one tile's stage on a CU that has
 // enough of them.
 struct Tile {
-    int bm, bn, groups;
+    int bm, bn, groups, threads;
     float fixed, round, stage;
 };
 constexpr Tile kTiles[] = {
-    {16, 16, 8, 3.0f, 0.30f, 0.105f}, {16, 32, 4, 3.0f, 0.26f, 0.14f},  {32, 32, 4, 3.0f, 0.45f, 0.14f},
-    {32, 64, 4, 3.0f, 0.60f, 0.20f},  {64, 64, 1, 4.0f, 0.30f, 0.20f},  {128, 128, 1, 5.0f, 0.62f, 0.56f},
-    {128, 144, 1, 5.0f, 0.66f, 0.62f}, {256, 256, 1, 9.0f, 1.60f, 1.60f}};
+    {16, 16, 8, 512, 3.0f, 0.30f, 0.105f},  {16, 32, 4, 512, 3.0f, 0.26f, 0.14f},
+    {32, 32, 4, 512, 3.0f, 0.45f, 0.14f},   {32, 64, 4, 512, 3.0f, 0.60f, 0.20f},
+    {64, 64, 1, 256, 4.0f, 0.30f, 0.20f},   {128, 128, 1, 256, 5.0f, 0.62f, 0.56f},
+    {128, 144, 1, 256, 5.0f, 0.66f, 0.62f}, {256, 256, 1, 1024, 9.0f, 1.60f, 1.60f}};
 
 int64_t tiles_of(const Tile &t, int64_t M, int64_t N) { return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn); }
 
@@ -55,16 +58,18 @@ int64_t tiles_of(const Tile &t, int64_t M, int64_t N) { return ((M + t.bm - 1) /
 //     77 x 4096 x 8192: 32 x 64 12 us, 32 x 32 18, 64 x 64 20, 128 x 128 40
 //     512 x 16384 x 4096: 128 x 128 37 us, 256 x 256 55, 64 x 64 52
 //     65536 x 288 x 8192: 128 x 144 181 us, 128 x 128 231, 256 x 256 227
+// Only tiles whose launch one dimension can count (all but for enormous outputs); -1 where there is none.
 int choose_tile(int64_t M, int64_t N, int64_t K) {
     const int64_t stages = (K + 127) / 128;
-    int best = 0;
+    int best = -1;
     float least = 0.0f;
     for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
         const Tile &t = kTiles[i];
+        if (tiles_of(t, M, N) > kMaxItems / t.threads) continue;
         const float along = (float)((stages + t.groups - 1) / t.groups) * t.round;
         const float all = (float)((tiles_of(t, M, N) + 255) / 256) * (float)stages * t.stage;
         const float us = t.fixed + (along > all ? along : all);
-        if (i == 0 || us < least) best = i, least = us;
+        if (best < 0 || us < least) best = i, least = us;
     }
     return best;
 }
@@ -128,9 +133,10 @@ jscan_status jscan_matmul_i8(const int8_t *q, const float *q_scale, const int8_t
                              const float *bias, void *out, int64_t M, int64_t N, int64_t K, int64_t ld_out,
                              jscan_dtype dtype, void *stream) {
     if (dtype != JSCAN_F32 && dtype != JSCAN_BF16) return JSCAN_ERR_DTYPE;
-    if (!dims_ok(M, K) || K == 0 || N < 0 || N > (1 << 24) || ((M + 15) / 16) * ((N + 15) / 16) > kMaxBlocks)
+    if (!dims_ok(M, K) || K == 0 || N < 0 || N > (1 << 24))
         return JSCAN_ERR_SHAPE;
     if (M == 0 || N == 0) return JSCAN_OK;
+    if (choose_tile(M, N, K) < 0) return JSCAN_ERR_SHAPE;
     if (ld_out < N || ld_out > ((int64_t)1 << 58) / M) return JSCAN_ERR_SHAPE;
     if (!q || !q_scale || !w || !w_scale || !out) return JSCAN_ERR_NULL;
     const int64_t es = elem_bytes(dtype);

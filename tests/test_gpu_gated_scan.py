@@ -247,6 +247,26 @@ def test_offsets_beyond_32_bits():
         assert torch.equal(bits(a), bits(b))
 
 
+@pytest.mark.parametrize("what", ["step", "scan"])
+def test_more_sequences_than_one_launch_counts(what):
+    """2^20 sequences of an odd number of channels need more work-items than a launch's 2^32: both ends and the
+    middle against the same sequences alone."""
+    batch, D = 1 << 20, 4099
+    pattern = [t[:, 0] for t in make(1024, 1, D, "bf16", "decay", 61)[:2]]
+    g, u = (t.repeat(batch // 1024, 1) for t in pattern)
+    h = torch.zeros((batch, D), device="cuda")
+    want_h = torch.zeros((1024, D), device="cuda")
+    if what == "step":
+        y = jscan.gated_step(h, g, u)
+        want_y = jscan.gated_step(want_h, *pattern)
+    else:
+        y, h = jscan.gated_scan(g[:, None], u[:, None], h0=h, h_final=h)
+        want_y, want_h = jscan.gated_scan(pattern[0][:, None], pattern[1][:, None], h0=want_h)
+        y, want_y = y[:, 0], want_y[:, 0]
+    for b in range(0, batch, 1024):
+        assert torch.equal(y[b:b + 1024], want_y) and torch.equal(h[b:b + 1024], want_h), b
+
+
 def _layer(g, u, dy, h0, dh, form, ws):
     y, h = jscan.gated_scan(g, u, h0=h0, form=form, workspace=ws)
     return (y, h, *jscan.gated_scan_backward(g, u, y, dy, h0=h0, dh_final=dh, form=form, workspace=ws))

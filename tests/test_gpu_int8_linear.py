@@ -129,6 +129,19 @@ def test_rows_beyond_32_bit_offsets():
     assert not out[100:-300].any()
 
 
+def test_more_rows_than_one_grid_dimension_counts():
+    """2^28 rows of 16 values, two columns: every row against its copy in a small case."""
+    M, K, N = (1 << 28) + 4096, 16, 2
+    x0 = torch.randn(4096, K, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    w, sw = int8(N, K, 5), scales(N, 6)
+    q0, s0 = jscan.quantize_rows(x0)
+    out0 = jscan.matmul_i8(q0, s0, w, sw)
+    q, s = jscan.quantize_rows(x0.repeat(M // 4096, 1))
+    assert (q.view(-1, 4096 * K) == q0.view(1, -1)).all() and (s.view(-1, 4096) == s0).all()
+    out = jscan.matmul_i8(q, s, w, sw)
+    assert (out.view(-1, 4096 * N) == out0.view(1, -1)).all()
+
+
 def test_empty_sizes_write_nothing():
     w, sw = int8(8, 32, 1), scales(8, 1)
     q, s = jscan.quantize_rows(torch.empty(0, 32, dtype=torch.bfloat16, device="cuda"))
