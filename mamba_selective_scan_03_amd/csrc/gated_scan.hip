@@ -47,22 +47,23 @@ struct Plan {
 
 constexpr int kRun = 8;   // tokens a thread takes of a block
 
-// Narrower strips and segments both make more work-groups.  Narrow strips read every byte once but in pieces of 64 or
-// 128 bytes a row, and a work-group has less in flight; segments read two of the tensors twice (the maps first), with a
-// second launch.  The layout is the one with the least expected time,
+// Narrower strips and segments both make more work-groups.  Narrow strips read every byte once but in
+// pieces of 64 or 128 bytes a row, and a work-group has less in flight; segments read two of the tensors
+// twice (the maps first), with a second launch.  The layout is the one with the least expected time,
 //     not cut   sqrt(memory^2 + chain^2) + 1 us,        cut   max(memory, chain) + 6 us
-// where memory is the bytes at the rates that large scans reach (5.3 TB/s; 6.5 TB/s for what is read twice) and chain is
-// the time along the tokens of one CU's work-groups, taken from single ones (1 x 65536 x 1024: 6.0, 3.8, 3.0 ns a token
-// and tensor for 64, 32, 16 lanes).  What it chooses between, measured (us):
+// where memory is the bytes at the rates that large scans reach (5.3 TB/s; 6.5 TB/s for what is read twice)
+// and chain is the time along the tokens of one CU's work-groups, taken from single ones (1 x 65536 x 1024:
+// 6.0, 3.8, 3.0 ns a token and tensor for 64, 32, 16 lanes).  What it chooses between, measured (us):
 //     2 x 4096 x 4096 sigmoid   forward   64 lanes 102, 32 lanes 65, 16 lanes 54, 64 lanes in 4 segments 57
 //                               backward  64 lanes 180, 32 lanes 119, 16 lanes 108, 64 lanes in 4 segments 95
 //     24 x 1000 x 500           forward   64 lanes 26.5, 32 lanes 19.6, 16 lanes 23.6
 //     1 x 65536 x 1024          forward   16 lanes 609, 64 lanes in 32 segments 118, in 64 segments 121
-// With thousands of work-groups the shorter ones even out better (16 x 4096 x 8192: 32 lanes 580 us, 64 lanes 621 us; 8 x
-// 4096 x 8192, half as many: 309 and 307 us).  Sequences of a few tokens take few waves (256 x 8 x 4096: one
-// wave 10.8 us, four 23 us, eight 42 us; 64 x 32 x 2048: 6.2, 5.4, 8.8 us; its backward pass 10.1, 11.9, 18.8 us).
-// channels: per lane.  tensors: rows of D elements moved per token.  narrow: whether the lane offsets of narrow strips fit
-// 32 bits.
+// With thousands of work-groups the shorter ones even out better (16 x 4096 x 8192: 32 lanes 580 us, 64
+// lanes 621 us; 8 x 4096 x 8192, half as many: 309 and 307 us).  Sequences of a few tokens take few waves
+// (256 x 8 x 4096: one wave 10.8 us, four 23 us, eight 42 us; 64 x 32 x 2048: 6.2, 5.4, 8.8 us; its
+// backward pass 10.1, 11.9, 18.8 us).
+// channels: per lane.  tensors: rows of D elements moved per token.  narrow: whether the lane offsets of
+// narrow strips fit 32 bits.
 constexpr int64_t kLeastSegment = 256;   // tokens
 constexpr int64_t kMostGroups = 768;     // work-groups that cutting makes, at most
 
@@ -144,8 +145,8 @@ struct ScanArgs {
     hipStream_t stream;
 
     ScanArgs sequences(int64_t b, int64_t n, int64_t es) const {   // the call on sequences b .. b + n - 1
-        return {from_row(g, b * L, es), from_row(u, b * L, es), from_row(y, b * L, es), from(h0, b * D), from(lengths, b),
-                from(h_final, b * D),   n, L, D, workspace, stream};
+        return {from_row(g, b * L, es), from_row(u, b * L, es), from_row(y, b * L, es), from(h0, b * D),
+                from(lengths, b),       from(h_final, b * D),   n, L, D, workspace, stream};
     }
 };
 
@@ -228,10 +229,11 @@ template <int N> bool whole_lines(const Pair (&t)[N], int64_t es) {
     return true;
 }
 
-// More than the last-level cache holds (256 MB) goes by with the non-temporal hint where rows are whole lines
-// (16 x 4096 x 8192: 583 us against 620 us without, backward 1198 and 1265 us; 1 x 65536 x 1024: 120 and 132, 160 and 192 us).
-// Rows that share lines want them kept for the neighbouring strip (3 x 6225 x 3864: 123 us with, 115 us without, backward
-// 283 and 248 us), and less data may be in the cache already (2 x 4096 x 4096 repeated: 55 us with, 38 us without).
+// More than the last-level cache holds (256 MB) goes by with the non-temporal hint where rows are whole
+// lines (16 x 4096 x 8192: 583 us against 620 us without, backward 1198 and 1265 us; 1 x 65536 x 1024: 120
+// and 132, 160 and 192 us). Rows that share lines want them kept for the neighbouring strip (3 x 6225 x
+// 3864: 123 us with, 115 us without, backward 283 and 248 us), and less data may be in the cache already (2
+// x 4096 x 4096 repeated: 55 us with, 38 us without).
 constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 
 template <typename Args, int N>
@@ -241,8 +243,8 @@ jscan_status launch_args(const Args &a, const Pair (&t)[N], jscan_dtype dtype, j
     const int64_t es = elem_bytes(dtype);
     Plan p = plan_for(a.batch, a.L, a.D, two ? 2 : 1, (int)es, tensors, backward, narrow_ok(t, es));
     p.stream = whole_lines(t, es) && a.batch * a.L * a.D * es * tensors > kStreamBytes;
-    // a plan's work-items per sequence; as many sequences a launch as it can count (all but for enormous batches, whose
-    // tokens are not cut)
+    // a plan's work-items per sequence; as many sequences a launch as it can count (all but for
+    // enormous batches, whose tokens are not cut)
     const int64_t channels = two ? 2 : 1, strips = (a.D + p.lanes * channels - 1) / (p.lanes * channels);
     const int64_t most = kMaxItems / (strips * p.n_seg * p.waves * 64);
     auto with_form = [&](auto v) {

@@ -16,6 +16,13 @@
 //      of the runs before its own (through lane shuffles first for the runs inside a wave);
 //   3. the states are s_i = A_i s_in + H_i, independent of each other.
 // Every order is fixed, so results repeat bit for bit.
+//
+// A run of eight tokens keeps two blocks of words and the maps of one in registers; sixteen tokens took the
+// registers of the prefetch, four made twice the barriers.  Keeping (A_i, H_i) instead of walking the run a
+// second time costs a multiply per element and makes the second pass independent.  Eight waves: sixteen ran
+// the same where strips are many and lose registers to the backward pass (8 x 4096 x 8192 decay: scan 302
+// us with sixteen, 307 us with eight; backward 515 and 513 us).  The gate is evaluated once; the maps are
+// not rounded.
 #pragma once
 
 #include <type_traits>
@@ -84,9 +91,9 @@ template <typename V, int LC, int NW, int TT> struct Place {
     static constexpr int kChannels = LC * V::n;  // channels per strip
 };
 
-// One tensor's rows as a strip walks them in scan order (kRev: from the last token down).  A row's address is
-// a wave-uniform part and a 32-bit lane part (channel, and the lane's run inside the wave).  kNt: whole blocks go by with
-// the non-temporal hint.
+// One tensor's rows as a strip walks them in scan order (kRev: from the last token down).  A row's address
+// is a wave-uniform part and a 32-bit lane part (channel, and the lane's run inside the wave).  kNt: whole
+// blocks go by with the non-temporal hint.
 template <typename V, int LC, int TT, bool kRev, bool kNt> struct Stream {
     using word = typename V::word;
     char *base;          // row of token 0 of the sequence, channel 0
@@ -96,8 +103,8 @@ template <typename V, int LC, int TT, bool kRev, bool kNt> struct Stream {
 
     template <typename T>
     __device__ __forceinline__ Stream(TokenRows<T> r, int64_t b, int64_t L, int sub, uint32_t channel_word) {
-        base = reinterpret_cast<char *>(const_cast<typename V::store_t *>(r.p)) + b * L * r.ld * (int64_t)sizeof(typename V::store_t);
         ld = r.ld * (int64_t)sizeof(typename V::store_t);
+        base = reinterpret_cast<char *>(const_cast<typename V::store_t *>(r.p)) + b * L * ld;
         chan_off = channel_word * (uint32_t)sizeof(word);
         const int runs_down = kRev ? 64 / LC - 1 - sub : sub;
         lane_off = chan_off + (uint32_t)(runs_down * TT) * (uint32_t)ld;
@@ -156,7 +163,8 @@ template <typename V, int LC, int NW> struct Join {
     float2 maps[2][NW][LC * N];
     float carry[2][LC * N];
 
-    __device__ __forceinline__ void operator()(Map<N> run, float (&s_in)[N], float (&s_out)[N], int wave, int lane, int parity) {
+    __device__ __forceinline__ void operator()(Map<N> run, float (&s_in)[N], float (&s_out)[N], int wave, int lane,
+                                               int parity) {
         const int c = lane % LC, sub = lane / LC;
         Map<N> before;   // the runs of this wave before this one
 #pragma unroll
@@ -207,10 +215,10 @@ template <typename V, int LC, int NW> struct Join {
     }
 };
 
-// Runs `count` blocks with one block of loads in flight: load(k, i) starts the loads of block i into buffer k,
-// scan(k, i) works on it.  Every path to a scan has the same operations behind the loads that it waits for (the other
-// buffer's loads and the stores of one block), so that the wait the compiler places there leaves all of them in
-// flight; a load under a condition would make it wait for everything.
+// Runs `count` blocks with one block of loads in flight: load(k, i) starts the loads of block i into buffer
+// k, scan(k, i) works on it.  Every path to a scan has the same operations behind the loads that it waits
+// for (the other buffer's loads and the stores of one block), so that the wait the compiler places there
+// leaves all of them in flight; a load under a condition would make it wait for everything.
 template <typename Load, typename Scan>
 __device__ __forceinline__ void pipelined(int64_t count, Load load, Scan scan) {
     using B0 = IntConst<0>;
@@ -293,8 +301,9 @@ __device__ __forceinline__ void scan_terms(typename V::word gw, typename V::word
 
 }  // namespace strip
 
-// The maps of all segments but the last of a cut sequence, which must be whole.  Each thread takes one long run of the
-// segment, so nothing is joined until its end.
+// The maps of all segments but the last of a cut sequence, which must be whole.  Each thread takes one long
+// run of the segment, so nothing is joined until its end.  Memory bounds it: 1 x 65536 x 1024 bf16 in 44
+// us, 6.0 TB/s.
 template <typename V, GateForm F, int LC, int NW, int TT, bool kRev>
 __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const typename V::store_t> g,
                                                                 TokenRows<const typename V::store_t> x,
@@ -369,7 +378,9 @@ __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const 
     }
 }
 
-// Forward scan of a strip.
+// Forward scan of a strip.  Memory bounds it: 16 x 4096 x 8192 bf16 sigmoid in 587 us, 5.5 TB/s, with the
+// traffic of the algorithm (2.15 GB read, 1.07 GB written); 1 x 65536 x 1024 in 32 segments in 73 us behind
+// their maps, 5.5 TB/s.
 template <typename V, GateForm F, int LC, int NW, int TT, bool kNt>
 __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typename V::store_t> g,
                                                              TokenRows<const typename V::store_t> u, const float *h0,
@@ -408,7 +419,8 @@ __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typ
     }
     if (at.seg > 0 && seg0 < end) {
         float unused[N];
-        join(share_before<V, LC, NW>(sp, at.b, at.seg, D, (int)cl * N, wave * P::kSub + sub), unused, s_end, wave, lane, 1);
+        join(share_before<V, LC, NW>(sp, at.b, at.seg, D, (int)cl * N, wave * P::kSub + sub), unused, s_end, wave,
+             lane, 1);
     }
 
     const int64_t wave_run = (int64_t)wave * P::kSub * TT, lane_run = wave_run + sub * TT;
@@ -475,8 +487,9 @@ __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typ
     for (int64_t t = max(seg0, n) + wave * P::kSub + sub; t < seg_end; t += P::kRuns) ys.store_at(V::pack(zero), t);
 }
 
-// Backward pass of a strip: the scan of c from the last token down, then the gradients of each token from c of
-// the token after it and h of the token before it.
+// Backward pass of a strip: the scan of c from the last token down, then the gradients of each token from c
+// of the token after it and h of the token before it, read from y.  Memory bounds it: 8 x 4096 x 8192 bf16
+// decay in 521 us, 5.2 TB/s; 16 x 4096 x 8192 sigmoid (six tensors) in 1156 us, 5.6 TB/s.
 template <typename V, GateForm F, int LC, int NW, int TT, bool kNt>
 __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
     TokenRows<const typename V::store_t> g, TokenRows<const typename V::store_t> u,
@@ -516,7 +529,8 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
     }
     if (at.seg > 0 && seg0 < end) {
         float unused[N];
-        join(share_before<V, LC, NW>(sp, at.b, at.seg, D, (int)cl * N, wave * P::kSub + sub), unused, s_end, wave, lane, 1);
+        join(share_before<V, LC, NW>(sp, at.b, at.seg, D, (int)cl * N, wave * P::kSub + sub), unused, s_end, wave,
+             lane, 1);
     }
 
     const int64_t wave_run = (int64_t)wave * P::kSub * TT, lane_run = wave_run + sub * TT;
@@ -617,8 +631,9 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
     }
 }
 
-// One decode token, the state in place: kVec channels of one sequence per thread, in accesses of up to 16 bytes
-// where all rows start on kVec elements (14 bytes an element of bf16, 8 of them the state).
+// One decode token, the state in place: kVec channels of one sequence per thread, in accesses of up to 16
+// bytes where all rows start on kVec elements (14 bytes an element of bf16, 8 of them the state).  256 x
+// 8192 bf16 in 4.8 us, 6.1 TB/s; one sequence is a launch's latency, 2.1 us.
 template <typename E, GateForm F, int kVec>
 __global__ __launch_bounds__(256) void gated_step_kernel(float *__restrict__ h,
                                                          const typename E::store_t *__restrict__ g,

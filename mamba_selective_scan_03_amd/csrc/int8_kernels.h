@@ -21,8 +21,8 @@ __device__ __forceinline__ i32x4_t mfma_i8(i32x4_t a, i32x4_t b, i32x4_t c) {
 }
 
 namespace quant {
-// The scale of a row whose largest magnitude is amax, 1 / 127 rounded to fp32 first.  The lower bound keeps 1 / s finite; a row of
-// zeros takes it and quantises to zeros.
+// The scale of a row whose largest magnitude is amax, 1 / 127 rounded to fp32 first.  The lower bound keeps
+// 1 / s finite; a row of zeros takes it and quantises to zeros.
 __device__ __forceinline__ float row_scale(float amax) { return fmaxf(amax * (1.0f / 127.0f), 0x1.0p-126f); }
 
 // Largest magnitude over a work-group of `kWaves` waves; +inf where any value is a NaN or an infinity
@@ -116,13 +116,13 @@ __global__ __launch_bounds__(kWaves * 64) void quantize_rows_kernel(const typena
 
 // Any other row, read twice (the second time from the caches): in chunks of 16 bytes where rows start on them
 // (kChunked), else element by element.
-template <typename E, bool kChunked>
-__global__ __launch_bounds__(1024) void quantize_any_rows_kernel(const typename E::store_t *__restrict__ x,
+template <typename E, int kWaves, bool kChunked>
+__global__ __launch_bounds__(kWaves * 64) void quantize_any_rows_kernel(const typename E::store_t *__restrict__ x,
                                                                  int8_t *__restrict__ q, float *__restrict__ scale,
                                                                  int64_t M, int K, int64_t ld_x) {
     using C = quant::Chunk<E>;
     constexpr int n = kChunked ? C::n : 1;
-    __shared__ float part[16];
+    __shared__ float part[kWaves];
     const int64_t m = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (m >= M) return;
     const typename E::store_t *row = x + m * ld_x;
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(1024) void quantize_any_rows_kernel(const typename 
         else v[0] = E::load(row + k);
     };
     float amax = 0.0f, poison = 0.0f;
-    for (int k = threadIdx.x * n; k < K; k += 1024 * n) {
+    for (int k = threadIdx.x * n; k < K; k += kWaves * 64 * n) {
         float v[n];
         load(k, v);
 #pragma unroll
@@ -140,10 +140,10 @@ __global__ __launch_bounds__(1024) void quantize_any_rows_kernel(const typename 
             poison = __builtin_fmaf(v[i], 0.0f, poison);
         }
     }
-    amax = quant::group_amax<16>(amax, poison, part);
+    amax = quant::group_amax<kWaves>(amax, poison, part);
     const bool finite = amax < __builtin_inff();
     const float s = finite ? quant::row_scale(amax) : __builtin_nanf(""), r = 1.0f / s;
-    for (int k = threadIdx.x * n; k < K; k += 1024 * n) {
+    for (int k = threadIdx.x * n; k < K; k += kWaves * 64 * n) {
         float v[n];
         load(k, v);
         if constexpr (kChunked) {
@@ -219,11 +219,14 @@ __device__ __forceinline__ void store_rows(T *out, const int8_t *lds, int l, int
 // consecutive: result row r of tile t is column (r / 4) * 4 NT + 4 t + r % 4.
 template <int NT> __device__ __forceinline__ int w_row(int t, int r) { return (r >> 2) * 4 * NT + 4 * t + (r & 3); }
 
-// A BM x BN tile per work-group, K in stages of 128 bytes.  WR x WC waves make the tile; with KG > 1 as many
-// groups of waves take every KG-th stage each and add their sums through LDS at the end, which shortens the
-// chain of stages where tiles are too few to fill the chip.  A stage's rows of q and w go from
-// memory straight into LDS, one stage ahead of the products.  A row's eight 16-byte chunks are permuted by
-// (row / 2) % 8, so that the 16 rows of one operand read fall on distinct banks.
+// A BM x BN tile per work-group, K in stages of 128 bytes.  WR x WC waves make the tile; with KG > 1 as
+// many groups of waves take every KG-th stage each and add their sums through LDS at the end, which
+// shortens the chain of stages where tiles are too few to fill the chip. 16384 x 16384 x 4096 with 256 x
+// 256 tiles in 0.94 ms, 2.3 POP/s: the power limit holds the clock at about 1.6 GHz, and the matrix cores
+// are busy for 60% of it.  1 x 16384 x 4096 in 12.8 us, w at 5.2 TB/s.  77 x 4096 x 8192 in 12.6 us: the
+// latency of the stages.  A stage's rows of q and w go from memory straight into LDS, one stage ahead of
+// the products.  A row's eight 16-byte chunks are permuted by (row / 2) % 8, so that the 16 rows of one
+// operand read fall on distinct banks.
 namespace tiled {
 constexpr int kStage = 128;
 constexpr int kGroup = 8;   // tile rows that are walked together, column by column, so that tiles in
@@ -363,8 +366,9 @@ __global__ __launch_bounds__(KG * WR * WC * 64,
         }
     }
 
-    // Results go out through LDS, 16 rows of a wave at a time, so that a store covers whole rows of the wave's columns
-    // (straight from the registers a store touches 64 pieces of 8 bytes: 16384 x 16384 x 256 took 762 us).
+    // Results go out through LDS, 16 rows of a wave at a time, so that a store covers whole rows of the
+    // wave's columns (straight from the registers a store touches 64 pieces of 8 bytes: 16384 x 16384 x
+    // 256 took 762 us).
     using T = typename E::store_t;
     constexpr int kCols = 16 * NT;
     constexpr int kRow = kCols * (int)sizeof(T) + 16;   // bytes, padded off the banks' period

@@ -22,18 +22,17 @@ void launch_quantize(const void *x, int8_t *q, float *scale, int64_t M, int64_t 
     // rows over both dimensions: one dimension counts 2^32 work-items
     const int64_t across = M < (1 << 20) ? M : (1 << 20);
     const dim3 grid((unsigned)across, (unsigned)((M + across - 1) / across));
-    if (!aligned16(x) || ld_x % per != 0)
-        hipLaunchKernelGGL((jscan::quantize_any_rows_kernel<E, false>), grid, dim3(1024), 0, s, xt, q, scale, M, (int)K, ld_x);
-    else if (chunks > 4096)
-        hipLaunchKernelGGL((jscan::quantize_any_rows_kernel<E, true>), grid, dim3(1024), 0, s, xt, q, scale, M, (int)K, ld_x);
-    else if (chunks <= 128)
-        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 1, 2>), grid, dim3(64), 0, s, xt, q, scale, M, (int)K, ld_x);
-    else if (chunks <= 512)
-        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 4, 2>), grid, dim3(256), 0, s, xt, q, scale, M, (int)K, ld_x);
-    else if (chunks <= 1024)
-        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 4, 4>), grid, dim3(256), 0, s, xt, q, scale, M, (int)K, ld_x);
-    else
-        hipLaunchKernelGGL((jscan::quantize_rows_kernel<E, 16, 4>), grid, dim3(1024), 0, s, xt, q, scale, M, (int)K, ld_x);
+    auto launch = [&](auto kernel, int threads) {
+        hipLaunchKernelGGL(kernel, grid, dim3((unsigned)threads), 0, s, xt, q, scale, M, (int)K, ld_x);
+    };
+    const bool on16 = aligned16(x) && ld_x % per == 0;
+    if (!on16 && K <= 8192) launch(jscan::quantize_any_rows_kernel<E, 4, false>, 256);
+    else if (!on16) launch(jscan::quantize_any_rows_kernel<E, 16, false>, 1024);
+    else if (chunks > 4096) launch(jscan::quantize_any_rows_kernel<E, 16, true>, 1024);
+    else if (chunks <= 128) launch(jscan::quantize_rows_kernel<E, 1, 2>, 64);
+    else if (chunks <= 512) launch(jscan::quantize_rows_kernel<E, 4, 2>, 256);
+    else if (chunks <= 1024) launch(jscan::quantize_rows_kernel<E, 4, 4>, 256);
+    else launch(jscan::quantize_rows_kernel<E, 16, 4>, 1024);
 }
 
 // The tiles of the product and what they take, measured on this chip (us, bf16 output): `fixed` of a call, `round`
