@@ -84,6 +84,35 @@ def test_long_sequences_match_the_oracle(dtype, batch, L, D, form, memory):
 
 
 @pytest.mark.parametrize("form", ["decay", "sigmoid"])
+@pytest.mark.parametrize("dtype,repeats,L,D", [("bf16", 260, 400, 256), ("f32", 260, 200, 256), ("bf16", 50, 1000, 512),
+                                               ("f32", 50, 500, 512), ("bf16", 90, 333, 250), ("bf16", 40, 130, 514)])
+def test_many_sequences_match_the_oracle(dtype, repeats, L, D, form):
+    """Batches that fill the chip with uncut strips, the larger ones beyond the last-level cache: two sequences
+    against the oracle, repeated; every repetition has the same bits."""
+    g, u, dy, h0, dh = make(2, L, D, dtype, form, 9 * L + D)
+    many = [t.repeat(repeats, *[1] * (t.dim() - 1)) for t in (g, u, dy, h0, dh)]
+    y, h = jscan.gated_scan(many[0], many[1], h0=many[3], form=form)
+    grads = jscan.gated_scan_backward(many[0], many[1], y, many[2], h0=many[3], dh_final=many[4], form=form)
+    for t in (y, h, *grads):
+        b = bits(t).view(repeats, -1)
+        assert (b == b[:1]).all()
+    y, h = y[:2].contiguous(), h[:2]
+    dg, du, dh0 = (t[:2] for t in grads)
+    E, _ = O.scan_error(g, u, h0, None, form)
+    want, want_h = O.scan(g, u, h0, None, form)
+    assert_within(y, want, E, y.dtype, "y")
+    assert_within(h, want_h, E[:, -1], torch.float32, "h_final")
+    w, e = O.backward(g, u, y, dy, h0, dh, None, form), O.backward_error(g, u, y, dy, h0, dh, None, form)
+    for got, a, b, t in zip((dg, du, dh0), w, e, (dg.dtype, du.dtype, torch.float32)):
+        assert_within(got, a, b, t, "gradient")
+
+
+def test_long_sequence_beyond_the_cache():
+    """Segments of a sequence of more than 256 MB."""
+    check(*make(1, 23001, 1024, "f32", "sigmoid", 77), "sigmoid")
+
+
+@pytest.mark.parametrize("form", ["decay", "sigmoid"])
 @pytest.mark.parametrize("dtype,batch,L,D,lengths", [
     ("f32", 4, 20, 40, [0, 1, 20, 7]), ("bf16", 3, 513, 66, [512, 0, 513]), ("bf16", 2, 9000, 64, [8191, 4500]),
     ("f32", 3, 3000, 24, [2999, 1, 0]), ("bf16", 2, 300, 31, [-5, 1000]), ("bf16", 70, 33, 128, None),

@@ -94,6 +94,17 @@ def test_product_matches_integer_sums(M, N, K, dtype, bias):
     check_product(out, q, sq, w, sw, b)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [   # the larger tiles, each with rows, columns and K that end inside one
+    (1000, 4100, 144), (700, 2300, 272), (2500, 2600, 1552), (2049, 5000, 272), (6000, 6001, 96), (1000, 4100, 1040),
+    (3900, 4090, 2064), (4096, 4090, 1040), (8200, 8301, 144),
+])
+def test_large_products_match_integer_sums(M, N, K, dtype):
+    q, w, sq, sw = int8(M, K, M + K), int8(N, K, N + K + 1, -128), scales(M, 1), scales(N, 2)
+    b = torch.randn(N, generator=torch.Generator().manual_seed(N)).cuda()
+    check_product(jscan.matmul_i8(q, sq, w, sw, bias=b, out_dtype=DT[dtype]), q, sq, w, sw, b)
+
+
 def test_largest_sums_do_not_wrap():
     """K at its limit with every product at 127 * 128 or 128 * 128: the int32 sums stay below 2^31."""
     K = 131056
