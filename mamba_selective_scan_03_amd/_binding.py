@@ -646,8 +646,8 @@ def _gated_workspace(workspace, batch, L, D, dev):
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is None:
         return None, 0
-    if workspace.device != dev:
-        _bad(f"workspace must be on {dev}")
+    if workspace.device != dev or not workspace.is_contiguous():
+        _bad(f"workspace must be contiguous and on {dev}")
     return workspace, workspace.numel() * workspace.element_size()
 
 

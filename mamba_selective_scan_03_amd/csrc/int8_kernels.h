@@ -246,8 +246,8 @@ __device__ __forceinline__ void lds_dma16_at(const void *base, uint32_t off, uin
 }
 #pragma clang diagnostic pop
 
-// A work-group barrier that leaves loads into LDS in flight (__syncthreads() waits for all of them); earlier LDS
-// reads have returned, since the products that used them were issued.
+// A work-group barrier that leaves loads into LDS in flight (__syncthreads() waits for all of them); its release
+// fence waits for the wave's earlier LDS reads.
 __device__ __forceinline__ void block_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_s_barrier();

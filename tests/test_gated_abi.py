@@ -143,6 +143,21 @@ def test_binding_refuses_before_the_library():
                         torch.zeros(4))
 
 
+def test_workspaces_that_are_not_memory_of_their_size_are_refused():
+    from mamba_selective_scan_03_amd._binding import _gated_workspace
+
+    need = jscan.gated_scan_workspace_bytes(1, 65536, 64)
+    assert need > 0
+    dev = torch.device("cpu")
+    ws = torch.empty(need, dtype=torch.uint8)
+    assert _gated_workspace(ws, 1, 65536, 64, dev) == (ws, need)
+    assert _gated_workspace(torch.empty(3, dtype=torch.float64), 1, 65536, 64, dev)[1] == 24   # the library refuses it
+    for bad in (torch.empty(1, dtype=torch.uint8).expand(need), torch.empty(2 * need, dtype=torch.uint8)[::2],
+                torch.empty(need, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError, match="workspace"):
+            _gated_workspace(bad, 1, 65536, 64, dev)
+
+
 def test_token_rows_of_views():
     from mamba_selective_scan_03_amd._binding import _token_rows
 

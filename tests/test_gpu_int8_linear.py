@@ -161,6 +161,49 @@ def test_empty_sizes_write_nothing():
     assert jscan.matmul_i8(int8(3, 32, 1), scales(3, 1), w[:0], sw[:0]).shape == (3, 0)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 640, 512), (37, 300, 4112), (600, 1500, 640), (2100, 4100, 272)])
+def test_captured_and_replayed(M, N, K):
+    """Quantiser and product recorded into a graph; every replay on new contents gives the eager calls' bits."""
+    r = torch.Generator().manual_seed(M)
+    w, sw, b = int8(N, K, 3), scales(N, 4), scales(N, 5)
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        jscan.matmul_i8(*jscan.quantize_rows(x), w, sw, bias=b)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q, s = jscan.quantize_rows(x)
+        out = jscan.matmul_i8(q, s, w, sw, bias=b)
+    for k in range(4):
+        x.copy_(torch.randn(M, K, generator=r).to(torch.bfloat16).cuda() * 2.0 ** k)
+        graph.replay()
+        torch.cuda.synchronize()
+        q1, s1 = jscan.quantize_rows(x)
+        assert torch.equal(q, q1) and torch.equal(s, s1)
+        assert torch.equal(out, jscan.matmul_i8(q1, s1, w, sw, bias=b))
+
+
+def test_calls_on_two_streams_at_once():
+    """Layers of different sizes side by side on two streams give what they give alone."""
+    layers = []
+    for M, N, K in ((3000, 2100, 272), (40, 4000, 4096)):
+        x = torch.randn(M, K, generator=torch.Generator().manual_seed(N)).to(torch.bfloat16).cuda()
+        layers.append((x, int8(N, K, N), scales(N, K)))
+    alone = [jscan.matmul_i8(*jscan.quantize_rows(x), w, sw) for x, w, sw in layers]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    got = [[], []]
+    for _ in range(6):
+        for i, (x, w, sw) in enumerate(layers):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(jscan.matmul_i8(*jscan.quantize_rows(x), w, sw))
+    torch.cuda.synchronize()
+    for a, outs in zip(alone, got):
+        assert all(torch.equal(a, o) for o in outs)
+
+
 def test_binding_refusals_on_the_gpu():
     q, w, sq, sw = int8(4, 32, 5), int8(6, 32, 6), scales(4, 1), scales(6, 2)
     for kw in (dict(q=q.float()), dict(w=w[:, :16]), dict(w=w.t()), dict(q_scale=sq[:3]), dict(w_scale=sw.double()),
