@@ -35,39 +35,49 @@ void launch_quantize(const void *x, int8_t *q, float *scale, int64_t M, int64_t 
     else launch(jscan::quantize_rows_kernel<E, 16, 4>, 1024);
 }
 
-// The tiles of the product and what they take, measured on this chip (us, bf16 output): `fixed` of a call, `round`
-// between two stages of one work-group that is alone on its CU, `stage` of one tile's stage on a CU that has
-// enough of them.
+// The tiles of the product and what they take on this chip (us, bf16 output; fitted to 714 products of 1 to 16384
+// rows and columns and 64 to 16384 deep): `start` of a work-group, `round` from one of its stages to the
+// next, `stage` of a CU's work for one stage of one tile, with `per_cu` work-groups side by side on a CU.
 struct Tile {
-    int bm, bn, groups, threads;
-    float fixed, round, stage;
+    int bm, bn, groups, threads, per_cu;
+    float start, round, stage;
 };
 constexpr Tile kTiles[] = {
-    {16, 16, 8, 512, 3.0f, 0.30f, 0.105f},  {16, 32, 4, 512, 3.0f, 0.26f, 0.14f},
-    {32, 32, 4, 512, 3.0f, 0.45f, 0.14f},   {32, 64, 4, 512, 3.0f, 0.60f, 0.20f},
-    {64, 64, 1, 256, 4.0f, 0.30f, 0.20f},   {128, 128, 1, 256, 5.0f, 0.62f, 0.56f},
-    {128, 144, 1, 256, 5.0f, 0.66f, 0.62f}, {256, 256, 1, 1024, 9.0f, 1.60f, 1.60f}};
+    {16, 16, 8, 512, 1, 0.95f, 0.40f, 0.057f},   {16, 32, 4, 512, 2, 1.1f, 0.19f, 0.083f},
+    {32, 32, 4, 512, 1, 1.2f, 0.50f, 0.12f},     {64, 32, 4, 512, 1, 1.75f, 0.48f, 0.177f},
+    {64, 64, 2, 512, 1, 1.65f, 0.53f, 0.26f},    {64, 64, 1, 256, 3, 1.45f, 0.285f, 0.265f},
+    {64, 128, 1, 256, 2, 2.35f, 0.39f, 0.424f},  {128, 128, 1, 512, 2, 2.5f, 0.72f, 0.61f},
+    {128, 144, 1, 256, 2, 5.2f, 0.60f, 0.70f},   {256, 256, 1, 1024, 1, 6.7f, 1.41f, 1.41f}};
+constexpr float kLaunch = 2.0f;
 
 int64_t tiles_of(const Tile &t, int64_t M, int64_t N) { return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn); }
 
 // The tile that is expected to take least: large ones read least per product, small ones fill the chip when
-// rows and columns are few, and the 144 columns leave less of a tile empty for some widths.  The larger of the
-// time along one work-group's stages and the time of a CU's share of all stages, on 256 CUs:
-//     1 x 4096 x 8192 (M x N x K): 16 x 16 tiles 5.8 us, 16 x 32 7.9, 64 x 64 22
-//     77 x 4096 x 8192: 32 x 64 12 us, 32 x 32 18, 64 x 64 20, 128 x 128 40
-//     512 x 16384 x 4096: 128 x 128 37 us, 256 x 256 55, 64 x 64 52
-//     65536 x 288 x 8192: 128 x 144 181 us, 128 x 128 231, 256 x 256 227
-// Only tiles whose launch one dimension can count (all but for enormous outputs); -1 where there is none.
+// rows and columns are few, K dealt out to groups of waves shortens the chain of stages, and the 144 columns leave
+// less of a tile empty for some widths.  A CU runs its share of the tiles per_cu at a time; each turn
+// costs a start, and all of them the larger of the time along the stages and the time of the CU's work.
+// Measured with w read from memory (M x N x K):
+//     1 x 4096 x 8192: 16 x 16 tiles 8.9 us, 16 x 32 10.0, 64 x 64 25
+//     77 x 4096 x 8192: 64 x 32 13.7 us, 32 x 32 20, 64 x 64 25 (in two groups 18.5)
+//     256 x 4096 x 8192: 64 x 64 in two groups 20.9 us, in one 26, 64 x 32 28
+//     512 x 4096 x 8192: 64 x 128 32 us, 64 x 64 35 (in two groups 38), 128 x 128 55
+//     512 x 16384 x 4096: 128 x 128 41 us, 256 x 256 54, 64 x 128 57
+//     2048 x 8192 x 4096: 256 x 256 58 us, 128 x 128 73
+//     65536 x 288 x 8192: 128 x 144 183 us, 128 x 128 228, 256 x 256 219
+// Over products of random sizes the choice is 1 to 2% slower than the best of these and six other tiles.  Only tiles
+// whose launch one dimension can count (all but for enormous outputs); -1 where there is none.
 int choose_tile(int64_t M, int64_t N, int64_t K) {
     const int64_t stages = (K + 127) / 128;
     int best = -1;
     float least = 0.0f;
     for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
         const Tile &t = kTiles[i];
-        if (tiles_of(t, M, N) > kMaxItems / t.threads) continue;
-        const float along = (float)((stages + t.groups - 1) / t.groups) * t.round;
-        const float all = (float)((tiles_of(t, M, N) + 255) / 256) * (float)stages * t.stage;
-        const float us = t.fixed + (along > all ? along : all);
+        const int64_t tiles = tiles_of(t, M, N);
+        if (tiles > kMaxItems / t.threads) continue;
+        const float share = (float)((tiles + 255) / 256), turns = (float)(((tiles + 255) / 256 + t.per_cu - 1) / t.per_cu);
+        const float along = turns * (float)((stages + t.groups - 1) / t.groups) * t.round;
+        const float work = share * (float)stages * t.stage;
+        const float us = kLaunch + turns * t.start + (along > work ? along : work);
         if (best < 0 || us < least) best = i, least = us;
     }
     return best;
@@ -99,10 +109,12 @@ template <typename E> void launch_matmul(const MatmulArgs &a) {
     case 0: launch_tiled<E, 16, 16, 1, 1, 8, 3>(a); break;
     case 1: launch_tiled<E, 16, 32, 1, 2, 4, 3>(a); break;
     case 2: launch_tiled<E, 32, 32, 2, 1, 4, 4>(a); break;
-    case 3: launch_tiled<E, 32, 64, 1, 2, 4, 3>(a); break;
-    case 4: launch_tiled<E, 64, 64, 2, 2, 1, 3>(a); break;
-    case 5: launch_tiled<E, 128, 128, 2, 2, 1, 2>(a); break;
-    case 6: launch_tiled<E, 128, 144, 4, 1, 1, 2>(a); break;
+    case 3: launch_tiled<E, 64, 32, 2, 1, 4, 3>(a); break;
+    case 4: launch_tiled<E, 64, 64, 2, 2, 2, 3>(a); break;
+    case 5: launch_tiled<E, 64, 64, 2, 2, 1, 3>(a); break;
+    case 6: launch_tiled<E, 64, 128, 2, 2, 1, 3>(a); break;
+    case 7: launch_tiled<E, 128, 128, 2, 4, 1, 2>(a); break;
+    case 8: launch_tiled<E, 128, 144, 4, 1, 1, 2>(a); break;
     default: launch_tiled<E, 256, 256, 4, 4, 1, 2>(a); break;
     }
 }

@@ -97,7 +97,8 @@ def test_product_matches_integer_sums(M, N, K, dtype, bias):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("M,N,K", [   # the larger tiles, each with rows, columns and K that end inside one
     (1000, 4100, 144), (700, 2300, 272), (2500, 2600, 1552), (2049, 5000, 272), (6000, 6001, 96), (1000, 4100, 1040),
-    (3900, 4090, 2064), (4096, 4090, 1040), (8200, 8301, 144),
+    (3900, 4090, 2064), (4096, 4090, 1040), (8200, 8301, 144), (190, 2050, 8208), (90, 3900, 2064), (100, 4097, 4112),
+    (256, 2100, 4112), (777, 2111, 2064), (500, 4100, 1040),
 ])
 def test_large_products_match_integer_sums(M, N, K, dtype):
     q, w, sq, sw = int8(M, K, M + K), int8(N, K, N + K + 1, -128), scales(M, 1), scales(N, 2)
