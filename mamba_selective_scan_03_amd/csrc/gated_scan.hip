@@ -50,7 +50,7 @@ constexpr int kRun = 8;   // tokens a thread takes of a block
 // Narrower strips and segments both make more work-groups.  Narrow strips read every byte once but in
 // pieces of 64 or 128 bytes a row, and a work-group has less in flight; segments read two of the tensors
 // twice (the maps first), with a second launch.  The layout is the one with the least expected time,
-//     not cut   sqrt(memory^2 + chain^2) + 1 us,        cut   max(memory, chain) + 6 us
+//     sqrt(memory^2 + chain^2), and 7 us more when cut,
 // where memory is the bytes at the rates that large scans reach (5.3 TB/s; 6.5 TB/s for what is read twice)
 // and chain is the time along the tokens of one CU's work-groups, taken from single ones (1 x 65536 x 1024:
 // 6.0, 3.8, 3.0 ns a token and tensor for 64, 32, 16 lanes).  What it chooses between, measured (us):
@@ -58,20 +58,27 @@ constexpr int kRun = 8;   // tokens a thread takes of a block
 //                               backward  64 lanes 180, 32 lanes 119, 16 lanes 108, 64 lanes in 4 segments 95
 //     24 x 1000 x 500           forward   64 lanes 26.5, 32 lanes 19.6, 16 lanes 23.6
 //     1 x 65536 x 1024          forward   16 lanes 609, 64 lanes in 32 segments 118, in 64 segments 121
-// With thousands of work-groups the shorter ones even out better (16 x 4096 x 8192: 32 lanes 580 us, 64
-// lanes 621 us; 8 x 4096 x 8192, half as many: 309 and 307 us).  Sequences of a few tokens take few waves
-// (256 x 8 x 4096: one wave 10.8 us, four 23 us, eight 42 us; 64 x 32 x 2048: 6.2, 5.4, 8.8 us; its
-// backward pass 10.1, 11.9, 18.8 us).
+//     39 x 13148 x 184 sigmoid  backward  16 lanes 287, 64 lanes in 2 segments 537, in 3 segments 423
+// Over 590 scans and backward passes of random sizes its choice is 1.5% slower than the best.
+// Where work-groups are many already, what counts is how little of a block lies behind a short sequence's end
+// (one wave takes 8 tokens a block, four 32, eight 64, narrow strips of 32 lanes 128), and for long ones
+// how evenly they end (16 x 4096 x 8192: 32 lanes 580 us, 64 lanes 621 us):
+//     36 x 36 x 8832 bf16       forward   one wave 13.1, 32 lanes 45;      backward  21 and 75
+//     60 x 60 x 9504 sigmoid    forward   four waves 34, 32 lanes 94
+//     108 x 157 x 7161          forward   four waves 154, 32 lanes 230;    backward  274 and 494
+//     596 x 130 x 1152          forward   eight waves 89, 32 lanes 174
+// and sequences of a few tokens take few waves everywhere (256 x 8 x 4096: one wave 10.8 us, four 23 us).
 // channels: per lane.  tensors: rows of D elements moved per token.  narrow: whether the lane offsets of
 // narrow strips fit 32 bits.
 constexpr int64_t kLeastSegment = 256;   // tokens
 constexpr int64_t kMostGroups = 768;     // work-groups that cutting makes, at most
 
-Plan plan_for(int64_t batch, int64_t L, int64_t D, int channels, int es, int tensors, bool backward, bool narrow) {
+Plan plan_for(int64_t batch, int64_t L, int64_t D, int channels, int es, int tensors, bool narrow) {
     auto groups_of = [&](int lanes) { return batch * ((D + lanes * channels - 1) / (lanes * channels)); };
-    if (L <= kRun) return {64, 1, 1, L};
-    if (L <= 4 * kRun) return {64, backward && groups_of(64) >= 512 ? 1 : 4, 1, L};
-    if (narrow && groups_of(32) >= 2048) return {32, 8, 1, L};
+    const int64_t wide = groups_of(64);
+    if (L <= kRun || (L <= 8 * kRun && wide >= 768)) return {64, 1, 1, L};
+    if (L <= 4 * kRun || (L <= 32 * kRun && wide >= 256)) return {64, 4, 1, L};
+    if (narrow && groups_of(32) >= 2048) return {L < 1024 ? 64 : 32, 8, 1, L};
     constexpr int kLanes[] = {64, 32, 16};
     constexpr float kToken[] = {6.0e-3f, 3.8e-3f, 3.0e-3f};
     const float elements = (float)(batch * L) * (float)D, once = elements * (float)(es * tensors) / 5.3e6f;
@@ -87,9 +94,8 @@ Plan plan_for(int64_t batch, int64_t L, int64_t D, int channels, int es, int ten
         auto consider = [&](int64_t n) {
             const int64_t seg = n == 1 ? L : ((L + n - 1) / n + block - 1) / block * block, n_seg = (L + seg - 1) / seg;
             const float chain = (float)((groups * n_seg + 255) / 256) * (float)seg * token;
-            const float both = once + twice;
-            const float us = n_seg == 1 ? __builtin_sqrtf(once * once + chain * chain) + 1.0f
-                                        : (both > chain ? both : chain) + 6.0f;
+            const float memory = n_seg == 1 ? once : once + twice;
+            const float us = __builtin_sqrtf(memory * memory + chain * chain) + (n_seg == 1 ? 0.0f : 7.0f);
             if (least == 0.0f || us < least) {
                 least = us;
                 best = {lanes, 8, n_seg, seg};
@@ -97,8 +103,8 @@ Plan plan_for(int64_t batch, int64_t L, int64_t D, int channels, int es, int ten
         };
         consider(1);
         if (lanes == 32) continue;
-        for (int64_t want = 256; want <= kMostGroups; want += 256)
-            for (int64_t up = 0; up < 2; ++up) {   // just below and just above whole rounds of the CUs
+        for (int64_t want = 128; want <= kMostGroups; want += 128)
+            for (int64_t up = 0; up < 2; ++up) {   // just below and just above whole and half rounds of the CUs
                 int64_t n = want / groups + up;
                 n = n < L / kLeastSegment ? n : L / kLeastSegment;
                 if (n > 1 && n * groups <= kMostGroups) consider(n);
@@ -241,7 +247,7 @@ jscan_status launch_args(const Args &a, const Pair (&t)[N], jscan_dtype dtype, j
     const bool two = dtype == JSCAN_BF16 && two_channels(t, a.D);
     const int tensors = !backward ? 3 : form == JSCAN_GATE_SIGMOID ? 6 : 5;
     const int64_t es = elem_bytes(dtype);
-    Plan p = plan_for(a.batch, a.L, a.D, two ? 2 : 1, (int)es, tensors, backward, narrow_ok(t, es));
+    Plan p = plan_for(a.batch, a.L, a.D, two ? 2 : 1, (int)es, tensors, narrow_ok(t, es));
     p.stream = whole_lines(t, es) && a.batch * a.L * a.D * es * tensors > kStreamBytes;
     // a plan's work-items per sequence; as many sequences a launch as it can count (all but for
     // enormous batches, whose tokens are not cut)

@@ -85,7 +85,9 @@ def test_long_sequences_match_the_oracle(dtype, batch, L, D, form, memory):
 
 @pytest.mark.parametrize("form", ["decay", "sigmoid"])
 @pytest.mark.parametrize("dtype,repeats,L,D", [("bf16", 260, 400, 256), ("f32", 260, 200, 256), ("bf16", 50, 1000, 512),
-                                               ("f32", 50, 500, 512), ("bf16", 90, 333, 250), ("bf16", 40, 130, 514)])
+                                               ("f32", 50, 500, 512), ("bf16", 90, 333, 250), ("bf16", 40, 130, 514),
+                                               ("bf16", 260, 1030, 256), ("f32", 260, 1030, 256), ("bf16", 260, 61, 256),
+                                               ("f32", 130, 37, 250), ("bf16", 130, 251, 250)])
 def test_many_sequences_match_the_oracle(dtype, repeats, L, D, form):
     """Batches that fill the chip with uncut strips, the larger ones beyond the last-level cache: two sequences
     against the oracle, repeated; every repetition has the same bits."""
