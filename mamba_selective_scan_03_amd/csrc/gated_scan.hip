@@ -63,10 +63,10 @@ constexpr int kRun = 8;   // tokens a thread takes of a block
 // Where work-groups are many already, what counts is how little of a block lies behind a short sequence's end
 // (one wave takes 8 tokens a block, four 32, eight 64, narrow strips of 32 lanes 128), and for long ones
 // how evenly they end (16 x 4096 x 8192: 32 lanes 580 us, 64 lanes 621 us):
-//     36 x 36 x 8832 bf16       forward   one wave 13.1, 32 lanes 45;      backward  21 and 75
-//     60 x 60 x 9504 sigmoid    forward   four waves 34, 32 lanes 94
-//     108 x 157 x 7161          forward   four waves 154, 32 lanes 230;    backward  274 and 494
-//     596 x 130 x 1152          forward   eight waves 89, 32 lanes 174
+//     36 x 36 x 8832            forward   one wave 13, four 16, eight 20, 32 lanes 45;       backward  21, 26, 48, 75
+//     497 x 123 x 2016 sigmoid  forward   one wave 157, four 141, eight 143, 32 lanes 235;   backward  310, 284, 318, 395
+//     108 x 157 x 7161          forward   one wave 167, four 154, eight 168, 32 lanes 230;   backward  289, 274, 336, 494
+//     72 x 379 x 3810 fp32 sig. forward   one wave 284, four 264, eight 251, 32 lanes 257;   backward  659, 560, 506, 546
 // and sequences of a few tokens take few waves everywhere (256 x 8 x 4096: one wave 10.8 us, four 23 us).
 // channels: per lane.  tensors: rows of D elements moved per token.  narrow: whether the lane offsets of
 // narrow strips fit 32 bits.
