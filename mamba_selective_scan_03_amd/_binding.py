@@ -600,16 +600,16 @@ def _matrix(name, t, shape, dtype, dev):
 
 def _check_flat(name, t, shape, dtype, dev):
     """t is None or a contiguous tensor of this shape and dtype on dev."""
-    if t is not None:
+    if t is not None and (t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous()):
         _check_like(name, t, shape, dtype, dev)
-        if not t.is_contiguous():
-            _bad(f"{name} must be contiguous")
+        _bad(f"{name} must be contiguous")
 
 
 def _token_rows(name, t, like, shape):
     """The token stride in elements of a [batch, L, D] tensor whose rows are contiguous and evenly
     spaced (contiguous, or a slice of a wider last dimension)."""
-    _check_like(name, t, shape, like.dtype, like.device)
+    if t is not like and (t.shape != shape or t.dtype != like.dtype or t.device != like.device):
+        _check_like(name, t, shape, like.dtype, like.device)
     batch, L, D = shape
     s_b, s_t, s_d = t.stride()
     if s_d != 1 and D > 1:
@@ -727,10 +727,12 @@ def gated_step(h, g_t, u_t, y_t=None, form="decay"):
     if dtype not in _DTYPES:
         _bad("g_t must be bfloat16 or float32")
     batch, D = shape
+    ld_g, one_g = _matrix("g_t", g_t, shape, dtype, dev)
+    ld_u, one_u = _matrix("u_t", u_t, shape, dtype, dev)
     if y_t is None:
-        y_t = torch.empty(batch, D, dtype=dtype, device=dev)
-    (ld_g, one_g), (ld_u, one_u), (ld_y, one_y) = _matrix("g_t", g_t, shape, dtype, dev), \
-        _matrix("u_t", u_t, shape, dtype, dev), _matrix("y_t", y_t, shape, dtype, dev)
+        y_t, ld_y, one_y = torch.empty(batch, D, dtype=dtype, device=dev), D, 1
+    else:
+        ld_y, one_y = _matrix("y_t", y_t, shape, dtype, dev)
     if D > 1 and not one_g == one_u == one_y == 1:
         _bad("the rows of g_t, u_t and y_t must be contiguous")
     if batch <= 1:
