@@ -657,7 +657,9 @@ def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, 
     fp32; rows may be slices of a wider projection): ``h_t = a h_{t-1} + u_t`` with ``a = exp(g_t)``
     (form "decay"), or ``h_t = a h_{t-1} + (1 - a) u_t`` with ``a = sigmoid(g_t)`` (form "sigmoid").  h0
     ``[batch, D]`` fp32; ``lengths`` int32 ``[batch]`` for padded sequences (y is zero in the padding).
-    Returns ``(y [batch, L, D] in g's dtype, h_final [batch, D] fp32)``; ``h_final`` may be ``h0``."""
+    Returns ``(y [batch, L, D] in g's dtype, h_final [batch, D] fp32)``; ``h_final`` may be ``h0``.  Decays above
+    one (g > 0 in the decay form) have to multiply to a finite fp32 number over any run of tokens: runs are
+    composed before they meet their starting state."""
     _check_gated(g, form, lengths)
     shape, dev = g.shape, g.device
     batch, L, D = shape
