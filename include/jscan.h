@@ -455,7 +455,10 @@ int64_t jscan_gated_scan_workspace(int64_t batch, int64_t L, int64_t D);
  *     G_t = dy_t + c_{t+1}   (dh_final in place of c after the last token),   dh0 = c_1
  *     JSCAN_GATE_DECAY     du_t = G_t               dg_t = c_t h_{t-1}
  *     JSCAN_GATE_SIGMOID   du_t = (1 - a_t) G_t     dg_t = c_t (1 - a_t) (h_{t-1} - u_t)
- * G and c are fp32; h_{t-1} is read from y, so for bf16 it carries y's one rounding (at most 2^-8 relative).
+ * G and c are fp32; h_{t-1} is read from y, so for bf16 dg carries y's one rounding: an error of at most
+ * 2^-8 |c_t h_{t-1}| in the decay form and 2^-8 |c_t (1 - a_t) h_{t-1}| in the sigmoid form, where
+ * h_{t-1} - u_t may cancel, so that it has no bound relative to dg (10% and more where states and
+ * inputs are close).  jscan_gated_scan_backward_saved, below, has h in fp32.
  *   g, u, y, dy   token rows as above; u may be NULL (and is not read) in the decay form; y is the
  *                 scan's output
  *   h0            the scan's, NULL for zeros;   dh_final [batch][D] fp32, NULL for zeros
@@ -472,6 +475,35 @@ jscan_status jscan_gated_scan_backward(const void *g, const void *u, const void 
                                        int64_t ld_u, int64_t ld_y, int64_t ld_dy, int64_t ld_dg,
                                        int64_t ld_du, void *workspace, int64_t workspace_bytes,
                                        jscan_gate_form form, jscan_dtype dtype, void *stream);
+
+/*
+ * Training in bf16 with fp32 states.  jscan_gated_scan_save is jscan_gated_scan that also keeps the fp32 state
+ * before every eighth token; jscan_gated_scan_backward_saved is jscan_gated_scan_backward that walks up from
+ * them, so that no h is rounded to bf16 (y and h0 are not needed; u is, in both forms).
+ *   states    [batch][ceil(L / 8)][D] fp32, jscan_gated_scan_states(batch, L, D) bytes, 16-byte aligned: row r
+ *             of a sequence is its state before token 8 r.  Rows behind a sequence's last token are
+ *             neither written nor read
+ * JSCAN_BF16 only (JSCAN_ERR_DTYPE otherwise): with JSCAN_F32 y itself holds the states.  With L == 0,
+ * states may be NULL.  Everything else as for the calls without it; y, h_final, du and dh0 agree with
+ * theirs to the fp32 rounding of the composition.
+ */
+jscan_status jscan_gated_scan_save(const void *g, const void *u, const float *h0,
+                                   const int32_t *lengths, void *y, float *h_final, float *states,
+                                   int64_t batch, int64_t L, int64_t D, int64_t ld_g, int64_t ld_u,
+                                   int64_t ld_y, void *workspace, int64_t workspace_bytes,
+                                   jscan_gate_form form, jscan_dtype dtype, void *stream);
+
+/* Bytes of states for this shape, or -1 if the shape is invalid.  Host-only. */
+int64_t jscan_gated_scan_states(int64_t batch, int64_t L, int64_t D);
+
+jscan_status jscan_gated_scan_backward_saved(const void *g, const void *u, const float *states,
+                                             const void *dy, const float *dh_final,
+                                             const int32_t *lengths, void *dg, void *du, float *dh0,
+                                             int64_t batch, int64_t L, int64_t D, int64_t ld_g,
+                                             int64_t ld_u, int64_t ld_dy, int64_t ld_dg,
+                                             int64_t ld_du, void *workspace,
+                                             int64_t workspace_bytes, jscan_gate_form form,
+                                             jscan_dtype dtype, void *stream);
 
 /*
  * One decode token of the gated recurrence for a batch: h [batch][D] fp32 in place; g_t, u_t and y_t

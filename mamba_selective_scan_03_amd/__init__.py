@@ -22,6 +22,7 @@ There is no CPU fallback: without the built library every call raises.
     y_t = step_mimo_trapezoid(h, x_prev, B_prev, x_t, delta_t, lam_t, A, B_t, C_t)
     y, h_final = gated_scan(g, u, form="decay")            # gated recurrence: one state per channel
     dg, du, dh0 = gated_scan_backward(g, u, y, dy)         # its gradients
+    states = gated_scan_states(g)                          # given to both: fp32 states behind bf16 gradients
     y_t = gated_step(h, g_t, u_t)                          # its decode token, h in place
     q, q_scale = quantize_rows(x)                          # activations to int8, a scale per token
     out = matmul_i8(q, q_scale, w, w_scale)                # int8 projection, a scale per output channel
@@ -34,6 +35,7 @@ from ._binding import (  # noqa: F401
     chunked_workspace_bytes,
     gated_scan,
     gated_scan_backward,
+    gated_scan_states,
     gated_scan_workspace_bytes,
     gated_step,
     library,

@@ -67,6 +67,11 @@ def library():
     lib.jscan_gated_scan.argtypes = [vp, vp, fp, vp, vp, fp, i64, i64, i64, i64, i64, i64, vp, i64, i32, i32, vp]
     lib.jscan_gated_scan_backward.argtypes = [vp, vp, vp, vp, fp, fp, vp, vp, vp, fp, i64, i64, i64, i64, i64, i64, i64,
                                               i64, i64, vp, i64, i32, i32, vp]
+    lib.jscan_gated_scan_save.argtypes = [vp, vp, fp, vp, vp, fp, fp, i64, i64, i64, i64, i64, i64, vp, i64, i32, i32, vp]
+    lib.jscan_gated_scan_backward_saved.argtypes = [vp, vp, fp, vp, fp, vp, vp, vp, fp, i64, i64, i64, i64, i64, i64, i64,
+                                                    i64, vp, i64, i32, i32, vp]
+    lib.jscan_gated_scan_states.argtypes = [i64, i64, i64]
+    lib.jscan_gated_scan_states.restype = i64
     lib.jscan_gated_step.argtypes = [fp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i32, vp]
     lib.jscan_gated_scan_workspace.argtypes = [i64, i64, i64]
     lib.jscan_gated_scan_workspace.restype = i64
@@ -77,7 +82,8 @@ def library():
               lib.jscan_prefill_scalar_a, lib.jscan_step_scalar_a, lib.jscan_prefill_complex, lib.jscan_step_complex,
               lib.jscan_prefill_trapezoid, lib.jscan_step_trapezoid, lib.jscan_prefill_mimo, lib.jscan_step_mimo,
               lib.jscan_prefill_mimo_trapezoid, lib.jscan_step_mimo_trapezoid, lib.jscan_gated_scan,
-              lib.jscan_gated_scan_backward, lib.jscan_gated_step, lib.jscan_quantize_rows, lib.jscan_matmul_i8):
+              lib.jscan_gated_scan_backward, lib.jscan_gated_scan_save, lib.jscan_gated_scan_backward_saved,
+              lib.jscan_gated_step, lib.jscan_quantize_rows, lib.jscan_matmul_i8):
         f.restype = i32
     lib.jscan_status_string.argtypes = [i32]
     lib.jscan_status_string.restype = ctypes.c_char_p
@@ -652,12 +658,29 @@ def _gated_workspace(workspace, batch, L, D, dev):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, workspace=None):
+def gated_scan_states(g):
+    """A new tensor for the states that :func:`gated_scan` of g ``[batch, L, D]`` bf16 keeps for its backward pass:
+    ``[batch, ceil(L / 8), D]`` fp32, the state before every eighth token.  None for fp32, where y holds them."""
+    if g.dtype not in _DTYPES or g.dim() != 3:
+        _bad("g must be a bfloat16 or float32 [batch, L, D]")
+    batch, L, D = g.shape
+    return torch.empty(batch, (L + 7) // 8, D, dtype=_F32, device=g.device) if g.dtype != _F32 else None
+
+
+def _check_states(states, g):
+    if g.dtype == _F32:
+        _bad("states are for bfloat16 tensors: with float32, y holds them")
+    batch, L, D = g.shape
+    _check_flat("states", states, (batch, (L + 7) // 8, D), _F32, g.device)
+
+
+def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, workspace=None, states=None):
     """Gated recurrence over whole sequences (``jscan_gated_scan``).  g, u ``[batch, L, D]`` (bf16 or
     fp32; rows may be slices of a wider projection): ``h_t = a h_{t-1} + u_t`` with ``a = exp(g_t)``
     (form "decay"), or ``h_t = a h_{t-1} + (1 - a) u_t`` with ``a = sigmoid(g_t)`` (form "sigmoid").  h0
     ``[batch, D]`` fp32; ``lengths`` int32 ``[batch]`` for padded sequences (y is zero in the padding).
-    Returns ``(y [batch, L, D] in g's dtype, h_final [batch, D] fp32)``; ``h_final`` may be ``h0``.  Decays above
+    Returns ``(y [batch, L, D] in g's dtype, h_final [batch, D] fp32)``; ``h_final`` may be ``h0``.  For training
+    in bf16, ``states`` from :func:`gated_scan_states` keeps fp32 states for the backward pass.  Decays above
     one (g > 0 in the decay form) have to multiply to a finite fp32 number over any run of tokens: runs are
     composed before they meet their starting state."""
     _check_gated(g, form, lengths)
@@ -675,27 +698,41 @@ def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, 
     else:
         _check_flat("h_final", h_final, state, _F32, dev)
     workspace, ws_bytes = _gated_workspace(workspace, batch, L, D, dev)
-    _launch("jscan_gated_scan", dev, g.data_ptr(), u.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
-            h_final.data_ptr(), batch, L, D, ld_g, ld_u, ld_y, _addr(workspace), ws_bytes, GATE_FORMS[form],
-            _DTYPES[g.dtype])
+    name, kept = "jscan_gated_scan", ()
+    if states is not None:
+        _check_states(states, g)
+        name, kept = "jscan_gated_scan_save", (states.data_ptr(),)
+    _launch(name, dev, g.data_ptr(), u.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(), h_final.data_ptr(), *kept,
+            batch, L, D, ld_g, ld_u, ld_y, _addr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype])
     return y, h_final
 
 
 def gated_scan_backward(g, u, y, dy, h0=None, dh_final=None, lengths=None, form="decay", dg=None, du=None, dh0=None,
-                        workspace=None):
+                        workspace=None, states=None):
     """Gradients of :func:`gated_scan` (``jscan_gated_scan_backward``): g, u, h0, lengths and form as given
     to it, y as it returned, dy ``[batch, L, D]`` and optionally dh_final ``[batch, D]`` fp32 the gradients of
     its results.  The decay form does not read u (it may be None).  Returns ``(dg, du, dh0)``; dg and du
-    may be given as the halves of one wider gradient."""
+    may be given as the halves of one wider gradient.
+
+    The state before each token is read from y.  In bf16 that is its rounded value, and dg is off by up to
+    ``2**-8 * |c * h|`` (sigmoid: ``2**-8 * |c * (1 - a) * h|``, which may be a large part of it where states and
+    inputs are close).  With the ``states`` that the scan kept, h is in fp32 throughout; u is then needed
+    in both forms, and y and h0 are not read (they may be None)."""
     _check_gated(g, form, lengths)
     shape, dev = g.shape, g.device
     batch, L, D = shape
-    if u is None and form != "decay":
-        _bad("u is needed by the sigmoid form")
-    ld_g, ld_y, ld_dy = _token_rows("g", g, g, shape), _token_rows("y", y, g, shape), _token_rows("dy", dy, g, shape)
+    if u is None and (form != "decay" or states is not None):
+        _bad("u is needed by the sigmoid form and with states")
+    ld_g, ld_dy = _token_rows("g", g, g, shape), _token_rows("dy", dy, g, shape)
     ld_u = D if u is None else _token_rows("u", u, g, shape)
     state = (batch, D)
-    _check_flat("h0", h0, state, _F32, dev)
+    if states is None:
+        if y is None:
+            _bad("y is needed without states")
+        ld_y = _token_rows("y", y, g, shape)
+        _check_flat("h0", h0, state, _F32, dev)
+    else:
+        _check_states(states, g)
     _check_flat("dh_final", dh_final, state, _F32, dev)
     if dg is None:
         dg, ld_dg = torch.empty(batch, L, D, dtype=g.dtype, device=dev), D
@@ -710,9 +747,14 @@ def gated_scan_backward(g, u, y, dy, h0=None, dh_final=None, lengths=None, form=
     else:
         _check_flat("dh0", dh0, state, _F32, dev)
     workspace, ws_bytes = _gated_workspace(workspace, batch, L, D, dev)
-    _launch("jscan_gated_scan_backward", dev, g.data_ptr(), _addr(u), y.data_ptr(), dy.data_ptr(), _addr(h0),
-            _addr(dh_final), _addr(lengths), dg.data_ptr(), du.data_ptr(), dh0.data_ptr(), batch, L, D, ld_g, ld_u, ld_y,
-            ld_dy, ld_dg, ld_du, _addr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype])
+    grads = (_addr(dh_final), _addr(lengths), dg.data_ptr(), du.data_ptr(), dh0.data_ptr(), batch, L, D)
+    tail = (ld_dy, ld_dg, ld_du, _addr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype])
+    if states is None:
+        _launch("jscan_gated_scan_backward", dev, g.data_ptr(), _addr(u), y.data_ptr(), dy.data_ptr(), _addr(h0), *grads,
+                ld_g, ld_u, ld_y, *tail)
+    else:
+        _launch("jscan_gated_scan_backward_saved", dev, g.data_ptr(), u.data_ptr(), states.data_ptr(), dy.data_ptr(),
+                *grads, ld_g, ld_u, *tail)
     return dg, du, dh0
 
 

@@ -45,7 +45,9 @@ struct Plan {
     bool stream = false;   // with the non-temporal hint
 };
 
-constexpr int kRun = 8;   // tokens a thread takes of a block
+constexpr int kRun = 8;   // tokens a thread takes of a block, and between two saved states
+
+int64_t state_rows(int64_t L) { return (L + kRun - 1) / kRun; }
 
 // Narrower strips and segments both make more work-groups.  Narrow strips read every byte once but in
 // pieces of 64 or 128 bytes a row, and a work-group has less in flight; segments read two of the tensors
@@ -145,20 +147,21 @@ struct ScanArgs {
     Pair g, u, y;
     const float *h0;
     const int32_t *lengths;
-    float *h_final;
+    float *h_final, *states;   // states: NULL unless saved
     int64_t batch, L, D;
     void *workspace;
     hipStream_t stream;
 
     ScanArgs sequences(int64_t b, int64_t n, int64_t es) const {   // the call on sequences b .. b + n - 1
         return {from_row(g, b * L, es), from_row(u, b * L, es), from_row(y, b * L, es), from(h0, b * D),
-                from(lengths, b),       from(h_final, b * D),   n, L, D, workspace, stream};
+                from(lengths, b),       from(h_final, b * D),   from(states, b * state_rows(L) * D),
+                n, L, D, workspace, stream};
     }
 };
 
 struct BackwardArgs {
     Pair g, u, y, dy, dg, du;
-    const float *h0, *dh_final;
+    const float *h0, *states, *dh_final;   // states in place of y and h0 when saved
     const int32_t *lengths;
     float *dh0;
     int64_t batch, L, D;
@@ -167,51 +170,52 @@ struct BackwardArgs {
 
     BackwardArgs sequences(int64_t b, int64_t n, int64_t es) const {
         return {from_row(g, b * L, es),  from_row(u, b * L, es),  from_row(y, b * L, es), from_row(dy, b * L, es),
-                from_row(dg, b * L, es), from_row(du, b * L, es), from(h0, b * D),        from(dh_final, b * D),
-                from(lengths, b),        from(dh0, b * D),        n, L, D, workspace, stream};
+                from_row(dg, b * L, es), from_row(du, b * L, es), from(h0, b * D),
+                from(states, b * state_rows(L) * D), from(dh_final, b * D), from(lengths, b), from(dh0, b * D),
+                n, L, D, workspace, stream};
     }
 };
 
-template <typename V, GateForm F, int LC, int NW, bool kRev>
+template <typename V, GateForm F, int LC, int NW, bool kRev, bool kSaved>
 void launch_summary(Pair g, Pair x, const float *s0, const int32_t *lengths, const jscan::SegSplit &sp, int64_t batch,
                     int64_t L, int64_t D, hipStream_t stream) {
     const int strips = (int)((D + LC * V::n - 1) / (LC * V::n));
-    hipLaunchKernelGGL((jscan::gated_summary_kernel<V, F, LC, NW, kRun, kRev>),
+    hipLaunchKernelGGL((jscan::gated_summary_kernel<V, F, LC, NW, kRun, kRev, kRev && kSaved>),
                        dim3((unsigned)(batch * strips * (sp.n_seg - 1))), dim3(NW * 64), 0, stream, in_rows<V>(g),
                        in_rows<V>(x), s0, lengths, sp, L, (int)D, strips);
 }
 
-template <typename V, GateForm F, int LC, int NW, bool kNt> void launch_as(const ScanArgs &a, const Plan &p) {
+template <typename V, GateForm F, int LC, int NW, bool kNt, bool kSaved> void launch_as(const ScanArgs &a, const Plan &p) {
     const int strips = (int)((a.D + LC * V::n - 1) / (LC * V::n));
     const jscan::SegSplit sp = split_of(p, a.batch, a.D, a.workspace);
     if constexpr (NW == 8 && LC != 32) {
         if (p.n_seg > 1)
-            launch_summary<V, F, LC, NW, false>(a.g, a.u, a.h0, a.lengths, sp, a.batch, a.L, a.D, a.stream);
+            launch_summary<V, F, LC, NW, false, kSaved>(a.g, a.u, a.h0, a.lengths, sp, a.batch, a.L, a.D, a.stream);
     }
-    hipLaunchKernelGGL((jscan::gated_scan_kernel<V, F, LC, NW, kRun, kNt>), dim3((unsigned)(a.batch * strips * p.n_seg)),
-                       dim3(NW * 64), 0, a.stream, in_rows<V>(a.g), in_rows<V>(a.u), a.h0, a.lengths,
-                       out_rows<V>(a.y), a.h_final, sp, a.L, (int)a.D, strips);
+    hipLaunchKernelGGL((jscan::gated_scan_kernel<V, F, LC, NW, kRun, kNt, kSaved>),
+                       dim3((unsigned)(a.batch * strips * p.n_seg)), dim3(NW * 64), 0, a.stream, in_rows<V>(a.g),
+                       in_rows<V>(a.u), a.h0, a.lengths, out_rows<V>(a.y), a.h_final, a.states, sp, a.L, (int)a.D, strips);
 }
 
-template <typename V, GateForm F, int LC, int NW, bool kNt> void launch_as(const BackwardArgs &a, const Plan &p) {
+template <typename V, GateForm F, int LC, int NW, bool kNt, bool kSaved> void launch_as(const BackwardArgs &a, const Plan &p) {
     const int strips = (int)((a.D + LC * V::n - 1) / (LC * V::n));
     const jscan::SegSplit sp = split_of(p, a.batch, a.D, a.workspace);
     if constexpr (NW == 8 && LC != 32) {
         if (p.n_seg > 1)
-            launch_summary<V, F, LC, NW, true>(a.g, a.dy, a.dh_final, a.lengths, sp, a.batch, a.L, a.D, a.stream);
+            launch_summary<V, F, LC, NW, true, kSaved>(a.g, a.dy, a.dh_final, a.lengths, sp, a.batch, a.L, a.D, a.stream);
     }
-    hipLaunchKernelGGL((jscan::gated_backward_kernel<V, F, LC, NW, kRun, kNt>), dim3((unsigned)(a.batch * strips * p.n_seg)),
-                       dim3(NW * 64), 0, a.stream, in_rows<V>(a.g), in_rows<V>(a.u), in_rows<V>(a.y), in_rows<V>(a.dy),
-                       a.h0, a.dh_final, a.lengths, out_rows<V>(a.dg), out_rows<V>(a.du), a.dh0, sp, a.L, (int)a.D,
-                       strips);
+    hipLaunchKernelGGL((jscan::gated_backward_kernel<V, F, LC, NW, kRun, kNt, kSaved>),
+                       dim3((unsigned)(a.batch * strips * p.n_seg)), dim3(NW * 64), 0, a.stream, in_rows<V>(a.g),
+                       in_rows<V>(a.u), in_rows<V>(a.y), in_rows<V>(a.dy), a.h0, a.states, a.dh_final, a.lengths,
+                       out_rows<V>(a.dg), out_rows<V>(a.du), a.dh0, sp, a.L, (int)a.D, strips);
 }
 
-template <typename V, GateForm F, typename Args> void launch_plan(const Args &a, const Plan &p) {
-    if (p.waves == 1) launch_as<V, F, 64, 1, false>(a, p);
-    else if (p.waves == 4) launch_as<V, F, 64, 4, false>(a, p);
-    else if (p.lanes == 64) p.stream ? launch_as<V, F, 64, 8, true>(a, p) : launch_as<V, F, 64, 8, false>(a, p);
-    else if (p.lanes == 32) p.stream ? launch_as<V, F, 32, 8, true>(a, p) : launch_as<V, F, 32, 8, false>(a, p);
-    else launch_as<V, F, 16, 8, false>(a, p);
+template <typename V, GateForm F, bool kS, typename Args> void launch_plan(const Args &a, const Plan &p) {
+    if (p.waves == 1) launch_as<V, F, 64, 1, false, kS>(a, p);
+    else if (p.waves == 4) launch_as<V, F, 64, 4, false, kS>(a, p);
+    else if (p.lanes == 64) p.stream ? launch_as<V, F, 64, 8, true, kS>(a, p) : launch_as<V, F, 64, 8, false, kS>(a, p);
+    else if (p.lanes == 32) p.stream ? launch_as<V, F, 32, 8, true, kS>(a, p) : launch_as<V, F, 32, 8, false, kS>(a, p);
+    else launch_as<V, F, 16, 8, false, kS>(a, p);
 }
 
 // Whether every row of a call's tensors starts on 4 bytes and holds an even number of bf16 values.
@@ -242,10 +246,11 @@ template <int N> bool whole_lines(const Pair (&t)[N], int64_t es) {
 // x 4096 x 4096 repeated: 55 us with, 38 us without).
 constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 
-template <typename Args, int N>
+// kSaved: with saved states (bf16 only).
+template <bool kSaved, typename Args, int N>
 jscan_status launch_args(const Args &a, const Pair (&t)[N], jscan_dtype dtype, jscan_gate_form form, bool backward) {
     const bool two = dtype == JSCAN_BF16 && two_channels(t, a.D);
-    const int tensors = !backward ? 3 : form == JSCAN_GATE_SIGMOID ? 6 : 5;
+    const int tensors = !backward ? 3 : form == JSCAN_GATE_SIGMOID && !kSaved ? 6 : 5;
     const int64_t es = elem_bytes(dtype);
     Plan p = plan_for(a.batch, a.L, a.D, two ? 2 : 1, (int)es, tensors, narrow_ok(t, es));
     p.stream = whole_lines(t, es) && a.batch * a.L * a.D * es * tensors > kStreamBytes;
@@ -257,14 +262,80 @@ jscan_status launch_args(const Args &a, const Pair (&t)[N], jscan_dtype dtype, j
         using V = decltype(v);
         for (int64_t b = 0; b < a.batch; b += most) {
             const Args part = b == 0 && a.batch <= most ? a : a.sequences(b, a.batch - b < most ? a.batch - b : most, es);
-            if (form == JSCAN_GATE_DECAY) launch_plan<V, GateForm::Decay>(part, p);
-            else launch_plan<V, GateForm::Sigmoid>(part, p);
+            if (form == JSCAN_GATE_DECAY) launch_plan<V, GateForm::Decay, kSaved>(part, p);
+            else launch_plan<V, GateForm::Sigmoid, kSaved>(part, p);
         }
     };
     if (two) with_form(jscan::Bf16x2{});
-    else if (dtype == JSCAN_BF16) with_form(jscan::Bf16x1{});
-    else with_form(jscan::F32x1{});
+    else if (kSaved || dtype == JSCAN_BF16) with_form(jscan::Bf16x1{});
+    else if constexpr (!kSaved) with_form(jscan::F32x1{});
     return launch_status();
+}
+
+// The checks of a scan and its launch.  states: where they are saved, of which a call without tokens has none.
+template <bool kSaved>
+jscan_status scan(const ScanArgs &a, int64_t workspace_bytes, jscan_gate_form form, jscan_dtype dtype) {
+    if (!form_ok(form)) return JSCAN_ERR_FORM;
+    if (dtype != JSCAN_BF16 && (kSaved || dtype != JSCAN_F32)) return JSCAN_ERR_DTYPE;
+    if (!shape_ok(a.batch, a.L, a.D)) return JSCAN_ERR_SHAPE;
+    if (a.batch == 0 || a.D == 0) return JSCAN_OK;
+    const int64_t tokens = a.batch * a.L, es = elem_bytes(dtype), state = a.batch * a.D * 4;
+    const Pair t[] = {a.g, a.u, a.y};
+    if (a.L > 0) {
+        for (const Pair &p : t)
+            if (!ld_ok(p.ld, tokens, a.D)) return JSCAN_ERR_SHAPE;
+        if (!a.g.p || !a.u.p || !a.y.p || (kSaved && !a.states)) return JSCAN_ERR_NULL;
+    }
+    if (!a.h_final) return JSCAN_ERR_NULL;
+    const int64_t need = workspace_bytes_for(a.batch, a.L, a.D);
+    if (need > 0 && !a.workspace) return JSCAN_ERR_NULL;
+    if (need > 0 && workspace_bytes < need) return JSCAN_ERR_WORKSPACE;
+    for (const Pair &p : t)
+        if (!aligned(p.p, es)) return JSCAN_ERR_ALIGN;
+    if (!aligned(a.h0, 4) || !aligned(a.h_final, 4) || !aligned(a.lengths, 4) || !aligned16(a.states) ||
+        (need > 0 && !aligned16(a.workspace)))
+        return JSCAN_ERR_ALIGN;
+    const Rows out[] = {rows_of(a.y, tokens, a.D, es), flat(a.h_final, state), flat(a.workspace, need),
+                        flat(a.states, state * state_rows(a.L))};
+    const Rows in[] = {rows_of(a.g, tokens, a.D, es), rows_of(a.u, tokens, a.D, es),
+                       flat(a.h0 == a.h_final ? nullptr : a.h0, state), flat(a.lengths, a.batch * 4)};
+    if (any_overlap(out, in)) return JSCAN_ERR_ALIAS;
+    return launch_args<kSaved>(a, t, dtype, form, false);
+}
+
+// The same for a backward pass.
+template <bool kSaved>
+jscan_status backward(BackwardArgs a, int64_t workspace_bytes, jscan_gate_form form, jscan_dtype dtype) {
+    if (!form_ok(form)) return JSCAN_ERR_FORM;
+    if (dtype != JSCAN_BF16 && (kSaved || dtype != JSCAN_F32)) return JSCAN_ERR_DTYPE;
+    if (!shape_ok(a.batch, a.L, a.D)) return JSCAN_ERR_SHAPE;
+    if (a.batch == 0 || a.D == 0) return JSCAN_OK;
+    const int64_t tokens = a.batch * a.L, es = elem_bytes(dtype), state = a.batch * a.D * 4;
+    const bool reads_u = kSaved || form == JSCAN_GATE_SIGMOID;   // from y, the decay form does not
+    if (!reads_u) a.u = {nullptr, a.D};
+    const Pair t[] = {a.g, a.u, a.y, a.dy, a.dg, a.du};
+    if (a.L > 0) {
+        for (const Pair &p : t)
+            if (!ld_ok(p.ld, tokens, a.D)) return JSCAN_ERR_SHAPE;
+        if (!a.g.p || !(kSaved ? (const void *)a.states : a.y.p) || !a.dy.p || !a.dg.p || !a.du.p || (reads_u && !a.u.p))
+            return JSCAN_ERR_NULL;
+    }
+    const int64_t need = workspace_bytes_for(a.batch, a.L, a.D);
+    if (need > 0 && !a.workspace) return JSCAN_ERR_NULL;
+    if (need > 0 && workspace_bytes < need) return JSCAN_ERR_WORKSPACE;
+    for (const Pair &p : t)
+        if (!aligned(p.p, es)) return JSCAN_ERR_ALIGN;
+    if (!aligned(a.h0, 4) || !aligned(a.dh_final, 4) || !aligned(a.dh0, 4) || !aligned(a.lengths, 4) ||
+        !aligned16(a.states) || (need > 0 && !aligned16(a.workspace)))
+        return JSCAN_ERR_ALIGN;
+    const Rows out[] = {rows_of(a.dg, tokens, a.D, es), rows_of(a.du, tokens, a.D, es), flat(a.dh0, state),
+                        flat(a.workspace, need)};
+    const Rows in[] = {rows_of(a.g, tokens, a.D, es),  rows_of(a.u, tokens, a.D, es),
+                       rows_of(a.y, tokens, a.D, es),  rows_of(a.dy, tokens, a.D, es),
+                       flat(a.h0, state),              flat(a.dh_final == a.dh0 ? nullptr : a.dh_final, state),
+                       flat(a.lengths, a.batch * 4),   flat(a.states, state * state_rows(a.L))};
+    if (any_overlap(out, in)) return JSCAN_ERR_ALIAS;
+    return launch_args<kSaved>(a, t, dtype, form, true);
 }
 
 // Four channels a thread where D, the strides and the addresses allow it (256 x 8192 bf16 4.8 us, 6.1 TB/s), or one
@@ -314,26 +385,22 @@ jscan_status jscan_gated_scan(const void *g, const void *u, const float *h0, con
                               float *h_final, int64_t batch, int64_t L, int64_t D, int64_t ld_g, int64_t ld_u,
                               int64_t ld_y, void *workspace, int64_t workspace_bytes, jscan_gate_form form,
                               jscan_dtype dtype, void *stream) {
-    if (!form_ok(form)) return JSCAN_ERR_FORM;
-    if (dtype != JSCAN_F32 && dtype != JSCAN_BF16) return JSCAN_ERR_DTYPE;
-    if (!shape_ok(batch, L, D)) return JSCAN_ERR_SHAPE;
-    if (batch == 0 || D == 0) return JSCAN_OK;
-    const int64_t tokens = batch * L, es = elem_bytes(dtype), state = batch * D * 4;
-    if (L > 0 && !(ld_ok(ld_g, tokens, D) && ld_ok(ld_u, tokens, D) && ld_ok(ld_y, tokens, D))) return JSCAN_ERR_SHAPE;
-    if (!h_final || (L > 0 && (!g || !u || !y))) return JSCAN_ERR_NULL;
-    const int64_t need = jscan_gated_scan_workspace(batch, L, D);
-    if (need > 0 && !workspace) return JSCAN_ERR_NULL;
-    if (need > 0 && workspace_bytes < need) return JSCAN_ERR_WORKSPACE;
-    if (!aligned(g, es) || !aligned(u, es) || !aligned(y, es) || !aligned(h0, 4) || !aligned(h_final, 4) ||
-        !aligned(lengths, 4) || (need > 0 && !aligned16(workspace)))
-        return JSCAN_ERR_ALIGN;
-    const Rows out[] = {rows_of({y, ld_y}, tokens, D, es), flat(h_final, state), flat(workspace, need)};
-    const Rows in[] = {rows_of({g, ld_g}, tokens, D, es), rows_of({u, ld_u}, tokens, D, es),
-                       flat(h0 == h_final ? nullptr : h0, state), flat(lengths, batch * 4)};
-    if (any_overlap(out, in)) return JSCAN_ERR_ALIAS;
-    const Pair t[] = {{g, ld_g}, {u, ld_u}, {y, ld_y}};
-    const ScanArgs a{t[0], t[1], t[2], h0, lengths, h_final, batch, L, D, workspace, static_cast<hipStream_t>(stream)};
-    return launch_args(a, t, dtype, form, false);
+    return scan<false>({{g, ld_g}, {u, ld_u}, {y, ld_y}, h0, lengths, h_final, nullptr, batch, L, D, workspace,
+                        static_cast<hipStream_t>(stream)}, workspace_bytes, form, dtype);
+}
+
+int64_t jscan_gated_scan_states(int64_t batch, int64_t L, int64_t D) {
+    if (!shape_ok(batch, L, D)) return -1;
+    const int64_t rows = batch * state_rows(L);
+    return D > 0 && rows > ((int64_t)1 << 58) / D ? -1 : rows * D * 4;
+}
+
+jscan_status jscan_gated_scan_save(const void *g, const void *u, const float *h0, const int32_t *lengths, void *y,
+                                   float *h_final, float *states, int64_t batch, int64_t L, int64_t D, int64_t ld_g,
+                                   int64_t ld_u, int64_t ld_y, void *workspace, int64_t workspace_bytes,
+                                   jscan_gate_form form, jscan_dtype dtype, void *stream) {
+    return scan<true>({{g, ld_g}, {u, ld_u}, {y, ld_y}, h0, lengths, h_final, states, batch, L, D, workspace,
+                       static_cast<hipStream_t>(stream)}, workspace_bytes, form, dtype);
 }
 
 jscan_status jscan_gated_scan_backward(const void *g, const void *u, const void *y, const void *dy, const float *h0,
@@ -342,38 +409,20 @@ jscan_status jscan_gated_scan_backward(const void *g, const void *u, const void 
                                        int64_t ld_dy, int64_t ld_dg, int64_t ld_du, void *workspace,
                                        int64_t workspace_bytes, jscan_gate_form form, jscan_dtype dtype,
                                        void *stream) {
-    if (!form_ok(form)) return JSCAN_ERR_FORM;
-    if (dtype != JSCAN_F32 && dtype != JSCAN_BF16) return JSCAN_ERR_DTYPE;
-    if (!shape_ok(batch, L, D)) return JSCAN_ERR_SHAPE;
-    if (batch == 0 || D == 0) return JSCAN_OK;
-    const int64_t tokens = batch * L, es = elem_bytes(dtype), state = batch * D * 4;
-    const bool sig = form == JSCAN_GATE_SIGMOID;   // the decay form does not read u
-    if (L > 0) {
-        const int64_t lds[] = {ld_g, ld_y, ld_dy, ld_dg, ld_du, sig ? ld_u : D};
-        for (int64_t ld : lds)
-            if (!ld_ok(ld, tokens, D)) return JSCAN_ERR_SHAPE;
-        if (!g || !y || !dy || !dg || !du || (sig && !u)) return JSCAN_ERR_NULL;
-    }
-    const int64_t need = jscan_gated_scan_workspace(batch, L, D);
-    if (need > 0 && !workspace) return JSCAN_ERR_NULL;
-    if (need > 0 && workspace_bytes < need) return JSCAN_ERR_WORKSPACE;
-    const void *elems[] = {g, sig ? u : nullptr, y, dy, dg, du};
-    for (const void *p : elems)
-        if (!aligned(p, es)) return JSCAN_ERR_ALIGN;
-    if (!aligned(h0, 4) || !aligned(dh_final, 4) || !aligned(dh0, 4) || !aligned(lengths, 4) ||
-        (need > 0 && !aligned16(workspace)))
-        return JSCAN_ERR_ALIGN;
-    const Rows out[] = {rows_of({dg, ld_dg}, tokens, D, es), rows_of({du, ld_du}, tokens, D, es), flat(dh0, state),
-                        flat(workspace, need)};
-    const Rows in[] = {rows_of({g, ld_g}, tokens, D, es),   rows_of({sig ? u : nullptr, ld_u}, tokens, D, es),
-                       rows_of({y, ld_y}, tokens, D, es),   rows_of({dy, ld_dy}, tokens, D, es),
-                       flat(h0, state),                     flat(dh_final == dh0 ? nullptr : dh_final, state),
-                       flat(lengths, batch * 4)};
-    if (any_overlap(out, in)) return JSCAN_ERR_ALIAS;
-    const Pair t[] = {{g, ld_g}, {sig ? u : nullptr, ld_u}, {y, ld_y}, {dy, ld_dy}, {dg, ld_dg}, {du, ld_du}};
-    const BackwardArgs a{t[0], t[1], t[2], t[3], t[4], t[5], h0, dh_final, lengths, dh0, batch, L, D, workspace,
-                         static_cast<hipStream_t>(stream)};
-    return launch_args(a, t, dtype, form, true);
+    return backward<false>({{g, ld_g}, {u, ld_u}, {y, ld_y}, {dy, ld_dy}, {dg, ld_dg}, {du, ld_du}, h0, nullptr, dh_final,
+                            lengths, dh0, batch, L, D, workspace, static_cast<hipStream_t>(stream)},
+                           workspace_bytes, form, dtype);
+}
+
+jscan_status jscan_gated_scan_backward_saved(const void *g, const void *u, const float *states, const void *dy,
+                                             const float *dh_final, const int32_t *lengths, void *dg, void *du,
+                                             float *dh0, int64_t batch, int64_t L, int64_t D, int64_t ld_g,
+                                             int64_t ld_u, int64_t ld_dy, int64_t ld_dg, int64_t ld_du,
+                                             void *workspace, int64_t workspace_bytes, jscan_gate_form form,
+                                             jscan_dtype dtype, void *stream) {
+    return backward<true>({{g, ld_g}, {u, ld_u}, {nullptr, D}, {dy, ld_dy}, {dg, ld_dg}, {du, ld_du}, nullptr, states,
+                           dh_final, lengths, dh0, batch, L, D, workspace, static_cast<hipStream_t>(stream)},
+                          workspace_bytes, form, dtype);
 }
 
 jscan_status jscan_gated_step(float *h, const void *g_t, const void *u_t, void *y_t, int64_t batch, int64_t D,

@@ -44,11 +44,14 @@ __device__ __forceinline__ int64_t tokens_of(const int32_t *lengths, int64_t b, 
     return n < 0 ? 0 : (n > L ? L : n);
 }
 
-// What a lane loads and stores at a time: n channels in one word.  The two-channel bf16 word needs rows
-// that start on 4 bytes and an even D; the one-channel word takes the rest.
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+// What a lane loads and stores at a time: n channels in one word (their fp32 states in one state_word).  The
+// two-channel bf16 word needs rows that start on 4 bytes and an even D; the one-channel word takes the rest.
 struct Bf16x2 {
     using store_t = uint16_t;
     using word = uint32_t;
+    using state_word = f32x2_t;
     static constexpr int n = 2;
     static __device__ __forceinline__ void unpack(word w, float (&f)[2]) {
         f[0] = bf16_lo(w);
@@ -59,6 +62,7 @@ struct Bf16x2 {
 struct Bf16x1 {
     using store_t = uint16_t;
     using word = uint16_t;
+    using state_word = float;
     static constexpr int n = 1;
     static __device__ __forceinline__ void unpack(word w, float (&f)[1]) { f[0] = bf16_bits_to_f32(w); }
     static __device__ __forceinline__ word pack(const float (&f)[1]) { return f32_to_bf16_bits(f[0]); }
@@ -66,6 +70,7 @@ struct Bf16x1 {
 struct F32x1 {
     using store_t = float;
     using word = float;
+    using state_word = float;
     static constexpr int n = 1;
     static __device__ __forceinline__ void unpack(word w, float (&f)[1]) { f[0] = w; }
     static __device__ __forceinline__ word pack(const float (&f)[1]) { return f[0]; }
@@ -140,6 +145,48 @@ template <typename V, int LC, int TT, bool kRev, bool kNt> struct Stream {
     }
     __device__ __forceinline__ void store_at(word v, int64_t t) const {
         *reinterpret_cast<word *>(base + t * ld + chan_off) = v;
+    }
+};
+
+// The saved fp32 states [batch][rows][D]: row r of a sequence is the state before its token r TT, where one thread's
+// run starts in the forward scan.  A row's address is a wave-uniform part and a 32-bit lane part, as in Stream.
+template <typename V, int LC, int TT, bool kRev, bool kNt> struct Starts {
+    using word = typename V::state_word;
+    char *base;          // row 0 of the sequence, channel 0
+    int64_t ld;          // bytes between rows
+    uint32_t lane_off, chan_off;
+
+    __device__ __forceinline__ Starts(float *p, int64_t b, int64_t L, int D, int sub, uint32_t channel_word) {
+        ld = (int64_t)D * 4;
+        base = reinterpret_cast<char *>(p) + b * ((L + TT - 1) / TT) * ld;
+        chan_off = channel_word * (uint32_t)sizeof(word);
+        lane_off = chan_off + (uint32_t)(kRev ? 64 / LC - 1 - sub : sub) * (uint32_t)ld;
+    }
+    // Row of the wave's run with the lowest token (the wave's runs start at scan position tau, whose last token,
+    // of `top`, is a run's end where kRev).
+    __device__ __forceinline__ word *row(int64_t tau, int64_t top) const {
+        const int64_t r = kRev ? (top - tau) / TT - 64 / LC : tau / TT;
+        return reinterpret_cast<word *>(base + r * ld + lane_off);
+    }
+    __device__ __forceinline__ void load(float (&s)[V::n], int64_t tau, int64_t top) const {
+        const word *p = row(tau, top);
+        unpack(kNt ? __builtin_nontemporal_load(p) : *p, s);
+    }
+    // The state before the run that holds scan position lane_tau first; runs behind the scan's end take row 0.
+    __device__ __forceinline__ void load_clamped(float (&s)[V::n], int64_t lane_tau, int64_t top) const {
+        const int64_t r = (top - lane_tau) / TT - 1;
+        unpack(*reinterpret_cast<const word *>(base + (r < 0 ? 0 : r) * ld + chan_off), s);
+    }
+    __device__ __forceinline__ void store(const float (&s)[V::n], int64_t tau) const {
+        word w;
+        if constexpr (V::n == 1) w = s[0];
+        else w = word{s[0], s[1]};
+        if constexpr (kNt) __builtin_nontemporal_store(w, row(tau, 0));
+        else *row(tau, 0) = w;
+    }
+    static __device__ __forceinline__ void unpack(word w, float (&s)[V::n]) {
+        if constexpr (V::n == 1) s[0] = w;
+        else s[0] = w.x, s[1] = w.y;
     }
 };
 
@@ -303,8 +350,8 @@ __device__ __forceinline__ void scan_terms(typename V::word gw, typename V::word
 
 // The maps of all segments but the last of a cut sequence, which must be whole.  Each thread takes one long
 // run of the segment, so nothing is joined until its end.  Memory bounds it: 1 x 65536 x 1024 bf16 in 44
-// us, 6.0 TB/s.
-template <typename V, GateForm F, int LC, int NW, int TT, bool kRev>
+// us, 6.0 TB/s.  kWholeRuns: the scan starts at a whole run of TT tokens (see gated_backward_kernel).
+template <typename V, GateForm F, int LC, int NW, int TT, bool kRev, bool kWholeRuns>
 __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const typename V::store_t> g,
                                                                 TokenRows<const typename V::store_t> x,
                                                                 const float *s0, const int32_t *__restrict__ lengths,
@@ -324,8 +371,8 @@ __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const 
 #pragma unroll
         for (int v = 0; v < N; ++v) sp.start[at.b * D + cw * N + v] = s0 ? s0[at.b * D + cw * N + v] : 0.0f;
     }
-    const int64_t tau0 = at.seg * sp.seg_len;
-    if (tau0 + sp.seg_len > n) return;   // never read: no token lies behind a segment that is not whole
+    const int64_t tau0 = at.seg * sp.seg_len, top = kWholeRuns ? (n + TT - 1) / TT * TT : n;
+    if (tau0 + sp.seg_len > top) return;   // never read: no token lies behind a segment that is not whole
     const int64_t per = sp.seg_len / P::kRuns;   // tokens per thread, a multiple of TT
     const uint32_t cl = (uint32_t)(live ? cw : words - 1);
     Stream<V, LC, TT, kRev, false> gs(g, at.b, L, sub, cl), xs(x, at.b, L, sub, cl);
@@ -335,14 +382,19 @@ __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const 
 #pragma unroll
     for (int v = 0; v < N; ++v) run.A[v] = 1.0f, run.H[v] = 0.0f;
     // rows of a lane: runs lie `per` tokens apart here
-    const int64_t step = kRev ? -1 : 1, t0 = kRev ? n - 1 - lane_tau : lane_tau;
+    const int64_t step = kRev ? -1 : 1, t0 = kRev ? top - 1 - lane_tau : lane_tau;
+    // the first of this run's tokens that exists (kWholeRuns: up to TT - 1 of the first run do not)
+    const int first = kWholeRuns && lane_tau == 0 ? (int)(top - n) : 0;
     const char *gp = gs.base + t0 * gs.ld + gs.chan_off, *xp = xs.base + t0 * xs.ld + xs.chan_off;
     word gw[TT], xw[TT], gn[TT], xn[TT];
     auto load = [&](word(&gd)[TT], word(&xd)[TT], int64_t i0) {
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
-            gd[i] = *reinterpret_cast<const word *>(gp + (i0 + i) * step * gs.ld);
-            xd[i] = *reinterpret_cast<const word *>(xp + (i0 + i) * step * xs.ld);
+            int64_t r = i0 + i;
+            if constexpr (kWholeRuns)
+                if (i0 == 0) r = max(i, first);
+            gd[i] = *reinterpret_cast<const word *>(gp + r * step * gs.ld);
+            xd[i] = *reinterpret_cast<const word *>(xp + r * step * xs.ld);
         }
     };
     load(gw, xw, 0);
@@ -353,10 +405,12 @@ __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const 
             Gate k[N];
             float in[N];
             scan_terms<V, F, kRev>(gw[i], xw[i], k, in);
+            const bool on = !kWholeRuns || i0 + i >= first;
 #pragma unroll
             for (int v = 0; v < N; ++v) {
-                run.H[v] = __builtin_fmaf(k[v].a, run.H[v], in[v]);
-                run.A[v] *= k[v].a;
+                const float a = on ? k[v].a : 1.0f, x = on ? in[v] : 0.0f;
+                run.H[v] = __builtin_fmaf(a, run.H[v], x);
+                run.A[v] *= a;
             }
         }
 #pragma unroll
@@ -381,12 +435,14 @@ __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const 
 // Forward scan of a strip.  Memory bounds it: 16 x 4096 x 8192 bf16 sigmoid in 587 us, 5.5 TB/s, with the
 // traffic of the algorithm (2.15 GB read, 1.07 GB written); 1 x 65536 x 1024 in 32 segments in 73 us behind
 // their maps, 5.5 TB/s.
-template <typename V, GateForm F, int LC, int NW, int TT, bool kNt>
-__global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typename V::store_t> g,
-                                                             TokenRows<const typename V::store_t> u, const float *h0,
-                                                             const int32_t *__restrict__ lengths,
-                                                             TokenRows<typename V::store_t> y, float *h_final,
-                                                             SegSplit sp, int64_t L, int D, int strips) {
+// kSave: the state before each thread's run is kept for the backward pass, 0.5 bytes an element beside 6 (8 x 4096 x
+// 8192 336 us, without 308); four waves a SIMD are asked for, which the kernels of 64 lanes have without it (else
+// 140 VGPRs, one work-group a CU).
+template <typename V, GateForm F, int LC, int NW, int TT, bool kNt, bool kSave>
+__global__ __launch_bounds__(NW * 64, kSave && LC == 64 ? 4 : 1) void gated_scan_kernel(
+    TokenRows<const typename V::store_t> g, TokenRows<const typename V::store_t> u, const float *h0,
+    const int32_t *__restrict__ lengths, TokenRows<typename V::store_t> y, float *h_final, float *states, SegSplit sp,
+    int64_t L, int D, int strips) {
     using namespace strip;
     using P = Place<V, LC, NW, TT>;
     using word = typename V::word;
@@ -401,6 +457,7 @@ __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typ
     const int64_t seg0 = at.seg * sp.seg_len, seg_end = min(seg0 + sp.seg_len, L);
     const int64_t end = min(seg_end, n);   // tokens [seg0, end) are scanned, [max(seg0, n), seg_end) cleared
     Stream<V, LC, TT, false, kNt> gs(g, at.b, L, sub, cl), us(u, at.b, L, sub, cl), ys(y, at.b, L, sub, cl);
+    const Starts<V, LC, TT, false, kNt> starts(states, at.b, L, D, sub, cl);
 
     // the segment's starting state; the segment with the last token (the first one of an empty sequence) ends with
     // the final state
@@ -454,6 +511,8 @@ __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typ
         }
         float s_in[N];
         join(run, s_in, s_end, wave, lane, parity);
+        if constexpr (kSave)
+            if (whole || t + lane_run < end) starts.store(s_in, t + wave_run);
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
             float s[N];
@@ -488,19 +547,25 @@ __global__ __launch_bounds__(NW * 64) void gated_scan_kernel(TokenRows<const typ
 }
 
 // Backward pass of a strip: the scan of c from the last token down, then the gradients of each token from c
-// of the token after it and h of the token before it, read from y.  Memory bounds it: 8 x 4096 x 8192 bf16
+// of the token after it and h of the token before it.  Memory bounds it: 8 x 4096 x 8192 bf16
 // decay in 521 us, 5.2 TB/s; 16 x 4096 x 8192 sigmoid (six tensors) in 1156 us, 5.6 TB/s.
-template <typename V, GateForm F, int LC, int NW, int TT, bool kNt>
+// Without kSaved h is read from y, which holds it in the tensors' type.  With it (y and h0 are not read) a
+// thread walks its run up from the saved fp32 state, so h is in fp32 throughout; for that its runs
+// have to be those of the forward scan, so scan positions count from the end of the last of them, `top`:
+// up to TT - 1 positions before the last token hold none and pass c on.
+// States against y: 8 x 4096 x 8192 decay 530 and 522 us, sigmoid 549 and 629 us (five tensors in place of six).
+template <typename V, GateForm F, int LC, int NW, int TT, bool kNt, bool kSaved>
 __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
     TokenRows<const typename V::store_t> g, TokenRows<const typename V::store_t> u,
     TokenRows<const typename V::store_t> y, TokenRows<const typename V::store_t> dy, const float *__restrict__ h0,
-    const float *dh_final, const int32_t *__restrict__ lengths, TokenRows<typename V::store_t> dg,
-    TokenRows<typename V::store_t> du, float *dh0, SegSplit sp, int64_t L, int D, int strips) {
+    const float *__restrict__ states, const float *dh_final, const int32_t *__restrict__ lengths,
+    TokenRows<typename V::store_t> dg, TokenRows<typename V::store_t> du, float *dh0, SegSplit sp, int64_t L, int D,
+    int strips) {
     using namespace strip;
     using P = Place<V, LC, NW, TT>;
     using word = typename V::word;
     constexpr int N = V::n;
-    constexpr bool kSig = F == GateForm::Sigmoid;
+    constexpr bool kSig = F == GateForm::Sigmoid, kReadsU = kSig || kSaved;
     __shared__ Join<V, LC, NW> join;
     const Where at = where(strips, sp.n_seg);
     const int64_t n = tokens_of(lengths, at.b, L);
@@ -508,23 +573,27 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
     const int c = lane % LC, sub = lane / LC, words = D / N;
     const int cw = at.strip * LC + c;
     const uint32_t cl = (uint32_t)min(cw, words - 1);   // lanes behind the last channel repeat it, bit for bit
-    // tau counts tokens from the sequence's last one; padding is cleared by token index
+    // tau counts tokens from the sequence's last one (its last run's end); padding is cleared by token index
+    const int64_t top = kSaved ? (n + TT - 1) / TT * TT : n, none = top - n;
     const int64_t seg0 = at.seg * sp.seg_len, seg_end = min(seg0 + sp.seg_len, L);
-    const int64_t end = min(seg_end, n);
-    Stream<V, LC, TT, true, kNt> gs(g, at.b, L, sub, cl), us(kSig ? u : g, at.b, L, sub, cl), hs(y, at.b, L, sub, cl),
-        ds(dy, at.b, L, sub, cl), dgs(dg, at.b, L, sub, cl), dus(du, at.b, L, sub, cl);
+    const int64_t end = sp.n_seg > 1 ? min(seg0 + sp.seg_len, top) : top;
+    Stream<V, LC, TT, true, kNt> gs(g, at.b, L, sub, cl), us(kReadsU ? u : g, at.b, L, sub, cl),
+        hs(kSaved ? g : y, at.b, L, sub, cl), ds(dy, at.b, L, sub, cl), dgs(dg, at.b, L, sub, cl), dus(du, at.b, L, sub, cl);
+    const Starts<V, LC, TT, true, kNt> starts(const_cast<float *>(states), at.b, L, D, sub, cl);
 
     float s_end[N];
 #pragma unroll
     for (int v = 0; v < N; ++v) s_end[v] = 0.0f;
-    const bool writes_final = seg0 < n ? seg_end >= n : (n == 0 && at.seg == 0);
+    const bool writes_final = seg0 < n ? end == top : (n == 0 && at.seg == 0);
+    // a first block with positions that hold no token goes by itself, before the whole ones
+    const bool head = kSaved && none > 0 && at.seg == 0 && end >= P::kBlock;
     const float *begin = sp.n_seg > 1 ? sp.start : dh_final;
     if (wave == NW - 1 || threadIdx.x < LC) {
 #pragma unroll
         for (int v = 0; v < N; ++v) s_end[v] = begin ? begin[at.b * D + (int)cl * N + v] : 0.0f;
         if (threadIdx.x < LC) {
 #pragma unroll
-            for (int v = 0; v < N; ++v) join.carry[at.seg > 0][c * N + v] = s_end[v];
+            for (int v = 0; v < N; ++v) join.carry[at.seg > 0 || head][c * N + v] = s_end[v];
         }
     }
     if (at.seg > 0 && seg0 < end) {
@@ -535,26 +604,42 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
 
     const int64_t wave_run = (int64_t)wave * P::kSub * TT, lane_run = wave_run + sub * TT;
     struct Block {
-        word g[TT], d[TT], h[TT], u[kSig ? TT : 1];
+        word g[TT], d[TT], h[kSaved ? 1 : TT], u[kReadsU ? TT : 1];
+        float start[N];
     } blocks[2];
     auto load = [&](Block &w, int64_t tau) {   // the whole block at tau
-        gs.load(w.g, tau + wave_run, n, 0);
-        ds.load(w.d, tau + wave_run, n, 0);
-        hs.load(w.h, tau + wave_run, n, -1);
-        if constexpr (kSig) us.load(w.u, tau + wave_run, n, 0);
+        gs.load(w.g, tau + wave_run, top, 0);
+        ds.load(w.d, tau + wave_run, top, 0);
+        if constexpr (kSaved) starts.load(w.start, tau + wave_run, top);
+        else hs.load(w.h, tau + wave_run, n, -1);
+        if constexpr (kReadsU) us.load(w.u, tau + wave_run, top, 0);
+    };
+    auto load_part = [&](Block &w, int64_t tau) {   // a block with positions that hold no token, or with token 0
+        if (tau + wave_run < end) {
+            gs.load_clamped(w.g, tau + lane_run, top, 0, 0, n - 1);
+            ds.load_clamped(w.d, tau + lane_run, top, 0, 0, n - 1);
+            if constexpr (kSaved) starts.load_clamped(w.start, tau + lane_run, top);
+            else hs.load_clamped(w.h, tau + lane_run, n, -1, 0, n - 1);
+            if constexpr (kReadsU) us.load_clamped(w.u, tau + lane_run, top, 0, 0, n - 1);
+        }
     };
     auto scan_block = [&](const Block &w, int64_t tau, int parity, auto is_whole) {
         constexpr bool whole = decltype(is_whole)::value;
         float A[TT][N], H[TT][N], b[TT][N];
+        float of_c[TT][N];   // kSaved: dg = of_c c
         Map<N> run;
 #pragma unroll
         for (int v = 0; v < N; ++v) run.A[v] = 1.0f, run.H[v] = 0.0f;
+        auto is_on = [&](int i) {   // whether position i of this thread's run holds a token of the segment
+            const int64_t at_tau = tau + lane_run + i;
+            return whole || (at_tau < end && (!kSaved || at_tau >= none));
+        };
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
             Gate k[N];
             float in[N];
             scan_terms<V, F, true>(w.g[i], w.d[i], k, in);
-            const bool on = whole || tau + lane_run + i < end;
+            const bool on = is_on(i);
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 const float a = on ? k[v].a : 1.0f, x = on ? in[v] : 0.0f;
@@ -565,6 +650,23 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
                 if constexpr (kSig) b[i][v] = k[v].b;
             }
         }
+        if constexpr (kSaved) {   // up the run from its saved state
+            float h[N];
+#pragma unroll
+            for (int v = 0; v < N; ++v) h[v] = w.start[v];
+#pragma unroll
+            for (int i = TT - 1; i >= 0; --i) {
+                Gate k[N];
+                float in[N], uu[N];
+                scan_terms<V, F, false>(w.g[i], w.u[i], k, in);
+                V::unpack(w.u[i], uu);
+#pragma unroll
+                for (int v = 0; v < N; ++v) {
+                    of_c[i][v] = kSig ? k[v].b * (h[v] - uu[v]) : h[v];
+                    h[v] = gated_advance(h[v], k[v].a, in[v]);
+                }
+            }
+        }
         float s_in[N];
         join(run, s_in, s_end, wave, lane, parity);
         float after[N];   // c of the token after this one
@@ -573,52 +675,52 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
             float h[N], d[N], uu[N], out_g[N], out_u[N];
-            V::unpack(w.h[i], h);
             V::unpack(w.d[i], d);
-            if constexpr (kSig) V::unpack(w.u[i], uu);
-            const int64_t t = n - 1 - (tau + lane_run + i);
-            if (!whole && t == 0) {
+            const int64_t t = top - 1 - (tau + lane_run + i);
+            if constexpr (!kSaved) {
+                V::unpack(w.h[i], h);
+                if constexpr (kSig) V::unpack(w.u[i], uu);
+                if (!whole && t == 0) {
 #pragma unroll
-                for (int v = 0; v < N; ++v) h[v] = h0 ? h0[at.b * D + (int)cl * N + v] : 0.0f;
+                    for (int v = 0; v < N; ++v) h[v] = h0 ? h0[at.b * D + (int)cl * N + v] : 0.0f;
+                }
             }
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 const float cc = __builtin_fmaf(A[i][v], s_in[v], H[i][v]), G = d[v] + after[v];
                 after[v] = cc;
-                if constexpr (kSig) {
-                    out_g[v] = cc * b[i][v] * (h[v] - uu[v]);
-                    out_u[v] = b[i][v] * G;
-                } else {
-                    out_g[v] = cc * h[v];
-                    out_u[v] = G;
-                }
+                out_u[v] = kSig ? b[i][v] * G : G;
+                if constexpr (kSaved) out_g[v] = cc * of_c[i][v];
+                else if constexpr (kSig) out_g[v] = cc * b[i][v] * (h[v] - uu[v]);
+                else out_g[v] = cc * h[v];
             }
             if (whole) {
-                dgs.store(V::pack(out_g), tau + wave_run, n, i);
-                dus.store(V::pack(out_u), tau + wave_run, n, i);
-            } else if (tau + lane_run + i < end) {
+                dgs.store(V::pack(out_g), tau + wave_run, top, i);
+                dus.store(V::pack(out_u), tau + wave_run, top, i);
+            } else if (is_on(i)) {
                 dgs.store_at(V::pack(out_g), t);
                 dus.store_at(V::pack(out_u), t);
             }
         }
     };
-    // A block is whole when all its tokens, and the one before each, exist.
-    int64_t blocks_n = end > seg0 ? (end - seg0) / P::kBlock : 0;
-    if (blocks_n > 0 && seg0 + blocks_n * P::kBlock == n) --blocks_n;
-    const int64_t tail = seg0 + blocks_n * P::kBlock;
-    pipelined(blocks_n, [&](auto k, int64_t i) { load(blocks[decltype(k)::value], seg0 + i * P::kBlock); },
+    // A block is whole when all its tokens (from y: and the one before each) exist.
+    const int64_t begin0 = seg0 + (head ? P::kBlock : 0);
+    int64_t blocks_n = end > begin0 ? (end - begin0) / P::kBlock : 0;
+    if (!kSaved && blocks_n > 0 && begin0 + blocks_n * P::kBlock == n) --blocks_n;
+    const int64_t tail = begin0 + blocks_n * P::kBlock;
+    if constexpr (kSaved) {
+        if (head) {
+            load_part(blocks[0], seg0);
+            scan_block(blocks[0], seg0, 1, std::false_type{});
+        }
+    }
+    pipelined(blocks_n, [&](auto k, int64_t i) { load(blocks[decltype(k)::value], begin0 + i * P::kBlock); },
               [&](auto k, int64_t i) {
-                  scan_block(blocks[decltype(k)::value], seg0 + i * P::kBlock, decltype(k)::value, std::true_type{});
+                  scan_block(blocks[decltype(k)::value], begin0 + i * P::kBlock, decltype(k)::value, std::true_type{});
               });
     if (tail < end) {
-        Block &w = blocks[0];
-        if (tail + wave_run < end) {
-            gs.load_clamped(w.g, tail + lane_run, n, 0, 0, n - 1);
-            ds.load_clamped(w.d, tail + lane_run, n, 0, 0, n - 1);
-            hs.load_clamped(w.h, tail + lane_run, n, -1, 0, n - 1);
-            if constexpr (kSig) us.load_clamped(w.u, tail + lane_run, n, 0, 0, n - 1);
-        }
-        scan_block(w, tail, (int)(blocks_n & 1), std::false_type{});
+        load_part(blocks[0], tail);
+        scan_block(blocks[0], tail, (int)(blocks_n & 1), std::false_type{});
     }
     if (writes_final && dh0 && wave == NW - 1 && sub == P::kSub - 1) {
 #pragma unroll

@@ -93,10 +93,12 @@ def scan_error(g, u, h0=None, lengths=None, form="decay"):
     return E, M
 
 
-def backward_error(g, u, y, dy, h0=None, dh_final=None, lengths=None, form="decay"):
+def backward_error(g, u, y, dy, h0=None, dh_final=None, lengths=None, form="decay", h_error=None):
     """Bounds of |dg - exact|, |du - exact|, |dh0 - exact| for gradients formed in fp32 from the given y,
     before the rounding of the outputs: c is a scan from the last token to the first with gates a
-    and inputs a dy, so scan_error's argument holds for it."""
+    and inputs a dy, so scan_error's argument holds for it.  h_error: bounds of |h_t - y_t| where the gradients are
+    formed from states h in place of y (the scan's fp32 states against its exact ones); it enters dg once,
+    by c b, whose own error changes it by less than 2^-10 of it."""
     a, b = gates(g, form)
     y, dy, u = _f64(y), _f64(dy), None if u is None else _f64(u)
     batch, L, D = y.shape
@@ -119,6 +121,8 @@ def backward_error(g, u, y, dy, h0=None, dh_final=None, lengths=None, form="deca
             span = before + np.abs(u[on, t])
             Eu[on, t] = b[on, t] * EG + (e[on, t] + r) * b[on, t] * G
             Eg[on, t] = b[on, t] * span * (E[on] + (e[on, t] + 4 * r) * M[on])
+        if h_error is not None and t:
+            Eg[on, t] += (1 + 2.0 ** -10) * M[on] * b[on, t] * h_error[on, t - 1]
     return Eg, Eu, E
 
 
