@@ -219,7 +219,9 @@ def _own(s):
     if c["kind"] == "step":
         y = jscan.gated_step(s["h0"], s["g"][:, 0], s["u"][:, 0], form=c["form"])
         return dict(y=y, h=s["h0"])
-    y, h = jscan.gated_scan(s["g"], s["u"], h0=s["h0"], lengths=s["lengths"], form=c["form"])
+    # a training step in bf16 keeps fp32 states for its gradients (in fp32, y holds them)
+    states = jscan.gated_scan_states(s["g"]) if c["kind"] == "train" else None
+    y, h = jscan.gated_scan(s["g"], s["u"], h0=s["h0"], lengths=s["lengths"], form=c["form"], states=states)
     if c["kind"] == "scan":
         return dict(y=y, h=h)
     dproj = dg = du = None
@@ -227,7 +229,7 @@ def _own(s):
         dproj = torch.empty_like(s["proj"])
         dg, du = dproj[..., :c["D"]], dproj[..., c["D"]:]
     dg, du, dh0 = jscan.gated_scan_backward(s["g"], s["u"], y, s["dy"], h0=s["h0"], dh_final=s["dh"],
-                                            lengths=s["lengths"], form=c["form"], dg=dg, du=du)
+                                            lengths=s["lengths"], form=c["form"], dg=dg, du=du, states=states)
     if dproj is not None:
         return dict(y=y, h=h, dproj=dproj, dh0=dh0)
     return dict(y=y, h=h, dg=dg, du=du, dh0=dh0)
