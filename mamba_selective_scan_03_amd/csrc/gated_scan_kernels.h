@@ -611,7 +611,7 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
         gs.load(w.g, tau + wave_run, top, 0);
         ds.load(w.d, tau + wave_run, top, 0);
         if constexpr (kSaved) starts.load(w.start, tau + wave_run, top);
-        else hs.load(w.h, tau + wave_run, n, -1);
+        else hs.load(w.h, tau + wave_run, top, -1);
         if constexpr (kReadsU) us.load(w.u, tau + wave_run, top, 0);
     };
     auto load_part = [&](Block &w, int64_t tau) {   // a block with positions that hold no token, or with token 0
@@ -619,7 +619,7 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
             gs.load_clamped(w.g, tau + lane_run, top, 0, 0, n - 1);
             ds.load_clamped(w.d, tau + lane_run, top, 0, 0, n - 1);
             if constexpr (kSaved) starts.load_clamped(w.start, tau + lane_run, top);
-            else hs.load_clamped(w.h, tau + lane_run, n, -1, 0, n - 1);
+            else hs.load_clamped(w.h, tau + lane_run, top, -1, 0, n - 1);
             if constexpr (kReadsU) us.load_clamped(w.u, tau + lane_run, top, 0, 0, n - 1);
         }
     };
