@@ -568,7 +568,9 @@ GATE_FORMS = {"decay": 0, "sigmoid": 1}
 # device only where it has to.  New tensors take their sizes one by one (a torch.Size costs torch.empty 0.8 us
 # more of its 2.1).
 _F32, _I8, _I32 = torch.float32, torch.int8, torch.int32
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# Its private accessors where torch has them; the public ones build a Stream object and check the device's state.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _launch(name, dev, *args):
