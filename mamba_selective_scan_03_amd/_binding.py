@@ -594,6 +594,13 @@ def _bad(msg: str):
     raise ValueError(msg)
 
 
+def _refuse_grad():
+    """For calls on tensors that require gradients, which autograd would lose without a word where it records."""
+    if torch.is_grad_enabled():
+        _bad("autograd does not record this call: make it under torch.no_grad(), on detached tensors, or inside a "
+             "torch.autograd.Function whose backward gives its gradients (gated_scan_backward for gated_scan)")
+
+
 def _check_like(name, t, shape, dtype, dev):
     if t.shape != shape or t.dtype != dtype or t.device != dev:
         _bad(f"{name} must have shape {tuple(shape)} and be {dtype} on {dev}, got {tuple(t.shape)}, {t.dtype}, {t.device}")
@@ -677,7 +684,8 @@ def _check_states(states, g):
 
 
 def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, workspace=None, states=None):
-    """Gated recurrence over whole sequences (``jscan_gated_scan``).  g, u ``[batch, L, D]`` (bf16 or
+    """Gated recurrence over whole sequences (``jscan_gated_scan``), not recorded by autograd (its gradients are
+    :func:`gated_scan_backward`'s; tensors that require them are refused outside of ``torch.no_grad()``).  g, u ``[batch, L, D]`` (bf16 or
     fp32; rows may be slices of a wider projection): ``h_t = a h_{t-1} + u_t`` with ``a = exp(g_t)``
     (form "decay"), or ``h_t = a h_{t-1} + (1 - a) u_t`` with ``a = sigmoid(g_t)`` (form "sigmoid").  h0
     ``[batch, D]`` fp32; ``lengths`` int32 ``[batch]`` for padded sequences (y is zero in the padding).
@@ -685,6 +693,8 @@ def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, 
     in bf16, ``states`` from :func:`gated_scan_states` keeps fp32 states for the backward pass.  Decays above
     one (g > 0 in the decay form) have to multiply to a finite fp32 number over any run of tokens: runs are
     composed before they meet their starting state."""
+    if g.requires_grad or u.requires_grad or (h0 is not None and h0.requires_grad):
+        _refuse_grad()
     _check_gated(g, form, lengths)
     shape, dev = g.shape, g.device
     batch, L, D = shape
@@ -700,12 +710,15 @@ def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, 
     else:
         _check_flat("h_final", h_final, state, _F32, dev)
     workspace, ws_bytes = _gated_workspace(workspace, batch, L, D, dev)
-    name, kept = "jscan_gated_scan", ()
-    if states is not None:
+    if states is None:
+        _launch("jscan_gated_scan", dev, g.data_ptr(), u.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
+                h_final.data_ptr(), batch, L, D, ld_g, ld_u, ld_y, _addr(workspace), ws_bytes, GATE_FORMS[form],
+                _DTYPES[g.dtype])
+    else:
         _check_states(states, g)
-        name, kept = "jscan_gated_scan_save", (states.data_ptr(),)
-    _launch(name, dev, g.data_ptr(), u.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(), h_final.data_ptr(), *kept,
-            batch, L, D, ld_g, ld_u, ld_y, _addr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype])
+        _launch("jscan_gated_scan_save", dev, g.data_ptr(), u.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
+                h_final.data_ptr(), states.data_ptr(), batch, L, D, ld_g, ld_u, ld_y, _addr(workspace), ws_bytes,
+                GATE_FORMS[form], _DTYPES[g.dtype])
     return y, h_final
 
 
@@ -720,6 +733,8 @@ def gated_scan_backward(g, u, y, dy, h0=None, dh_final=None, lengths=None, form=
     ``2**-8 * |c * h|`` (sigmoid: ``2**-8 * |c * (1 - a) * h|``, which may be a large part of it where states and
     inputs are close).  With the ``states`` that the scan kept, h is in fp32 throughout; u is then needed
     in both forms, and y and h0 are not read (they may be None)."""
+    if g.requires_grad or dy.requires_grad or any(t is not None and t.requires_grad for t in (u, y, h0, dh_final)):
+        _refuse_grad()
     _check_gated(g, form, lengths)
     shape, dev = g.shape, g.device
     batch, L, D = shape
@@ -749,14 +764,14 @@ def gated_scan_backward(g, u, y, dy, h0=None, dh_final=None, lengths=None, form=
     else:
         _check_flat("dh0", dh0, state, _F32, dev)
     workspace, ws_bytes = _gated_workspace(workspace, batch, L, D, dev)
-    grads = (_addr(dh_final), _addr(lengths), dg.data_ptr(), du.data_ptr(), dh0.data_ptr(), batch, L, D)
-    tail = (ld_dy, ld_dg, ld_du, _addr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype])
     if states is None:
-        _launch("jscan_gated_scan_backward", dev, g.data_ptr(), _addr(u), y.data_ptr(), dy.data_ptr(), _addr(h0), *grads,
-                ld_g, ld_u, ld_y, *tail)
+        _launch("jscan_gated_scan_backward", dev, g.data_ptr(), _addr(u), y.data_ptr(), dy.data_ptr(), _addr(h0),
+                _addr(dh_final), _addr(lengths), dg.data_ptr(), du.data_ptr(), dh0.data_ptr(), batch, L, D, ld_g, ld_u,
+                ld_y, ld_dy, ld_dg, ld_du, _addr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype])
     else:
         _launch("jscan_gated_scan_backward_saved", dev, g.data_ptr(), u.data_ptr(), states.data_ptr(), dy.data_ptr(),
-                *grads, ld_g, ld_u, *tail)
+                _addr(dh_final), _addr(lengths), dg.data_ptr(), du.data_ptr(), dh0.data_ptr(), batch, L, D, ld_g, ld_u,
+                ld_dy, ld_dg, ld_du, _addr(workspace), ws_bytes, GATE_FORMS[form], _DTYPES[g.dtype])
     return dg, du, dh0
 
 
@@ -764,6 +779,8 @@ def gated_step(h, g_t, u_t, y_t=None, form="decay"):
     """One decode token of the gated recurrence (``jscan_gated_step``): h ``[batch, D]`` fp32 is updated in
     place; g_t, u_t ``[batch, D]`` may be strided views, e.g. ``g[:, t]``.  Returns y_t ``[batch, D]``: a new
     contiguous tensor, or the given ``y_t``, whose rows may be strided too."""
+    if h.requires_grad or g_t.requires_grad or u_t.requires_grad:
+        _refuse_grad()
     code = GATE_FORMS.get(form)
     if code is None:
         _bad(f"form must be one of {tuple(GATE_FORMS)}")
@@ -810,6 +827,8 @@ def quantize_rows(x, q=None, scale=None):
     """Rows of x ``[..., K]`` (bf16 or fp32, K a multiple of 16; a slice of a wider tensor too) to int8, each
     with a scale of its own (``jscan_quantize_rows``).  Returns ``(q [..., K] int8, scale [...] fp32)``: the
     first input of :func:`matmul_i8`."""
+    if x.requires_grad:
+        _refuse_grad()
     if not x.is_cuda or x.dtype not in _DTYPES:
         _bad("x must be a bfloat16 or float32 CUDA tensor")
     if x.dim() < 1:
@@ -835,6 +854,8 @@ def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
     ``[...]`` (a token each) and ``[N]`` (an output channel each) and an optional fp32 bias ``[N]``
     (``jscan_matmul_i8``).  Returns out ``[..., N]`` in out_dtype; a given ``out`` may be a slice of a wider
     tensor."""
+    if q_scale.requires_grad or w_scale.requires_grad or (bias is not None and bias.requires_grad):
+        _refuse_grad()
     if not q.is_cuda or q.dtype != torch.int8 or q.dim() < 1 or not q.is_contiguous():
         _bad("q must be a contiguous int8 CUDA tensor")
     dev, K, lead = q.device, q.shape[-1], q.shape[:-1]
