@@ -416,7 +416,11 @@ jscan_status jscan_prefill_chunked_noalloc(const void *x, const void *delta, con
  *     JSCAN_GATE_DECAY     h_t = exp(g_t) h_{t-1} + u_t                          (g a log decay)
  *     JSCAN_GATE_SIGMOID   h_t = sigmoid(g_t) h_{t-1} + (1 - sigmoid(g_t)) u_t   (g a gate logit)
  *     y_t = h_t, rounded to nearest even to the dtype
- * g = -inf drops the state before the token (a reset inside a row).  Gates that make the recurrence
+ * g = -inf makes the decay 0, which drops a finite state before the token (a reset inside a row).  It is a
+ * product like any other: 0 times an infinity or a NaN is NaN, so a reset does not clear those (nor
+ * do decays whose product underflows to 0).  They stay in their channel to the end of their sequence,
+ * in the backward pass (from dy) to its start, and reach no other channel or sequence.  Documents that
+ * must not reach each other in that case are sequences of their own.  Gates that make the recurrence
  * unstable (g > 0 in the decay form) are not checked; the decays of any run of tokens have to multiply to
  * a finite fp32 number.
  *

@@ -25,8 +25,8 @@ struct Gate {
 // exp(g) is the hardware base-2 exponential of g log2(e).  The sigmoid is formed from
 // t = exp(-|g|) in (0, 1], so that both a and 1 - a keep their relative precision at either
 // end and no infinity arises from a finite gate: the larger of the two is 1 / (1 + t), the
-// smaller t / (1 + t).  g = -inf gives a = 0 in both forms (the state is dropped), +inf in the
-// sigmoid form a = 1, b = 0; a NaN stays one.
+// smaller t / (1 + t).  g = -inf gives a = 0 in both forms (a finite state is dropped; an infinite one becomes
+// NaN), +inf in the sigmoid form a = 1, b = 0; a NaN stays one.
 template <GateForm F> __device__ __forceinline__ Gate gate(float g) {
     if constexpr (F == GateForm::Decay) {
         return Gate{__builtin_amdgcn_exp2f(g * kLog2e), 1.0f};
