@@ -61,10 +61,15 @@ int64_t state_rows(int64_t L) { return (L + kRun - 1) / kRun; }
 //     24 x 1000 x 500           forward   64 lanes 26.5, 32 lanes 19.6, 16 lanes 23.6
 //     1 x 65536 x 1024          forward   16 lanes 609, 64 lanes in 32 segments 118, in 64 segments 121
 //     39 x 13148 x 184 sigmoid  backward  16 lanes 287, 64 lanes in 2 segments 537, in 3 segments 423
-// Over 590 scans and backward passes of random sizes its choice is 1.5% slower than the best.
-// Where work-groups are many already, what counts is how little of a block lies behind a short sequence's end
-// (one wave takes 8 tokens a block, four 32, eight 64, narrow strips of 32 lanes 128), and for long ones
-// how evenly they end (16 x 4096 x 8192: 32 lanes 580 us, 64 lanes 621 us):
+// Over 630 scans and backward passes of random sizes its choice is 1.4% slower than the best layout tried, which itself
+// may be well off the passes' bytes (profiles/sweep_gated_scan_layouts.txt has every time).
+// Where strips of 64 lanes are more than the chip holds at a time (512, two work-groups a CU), what counts is how
+// little of a block lies behind a short sequence's end (one wave takes 8 tokens a block, four 32, eight 64,
+// narrow strips of 32 lanes 128), and for long ones how evenly the turns end (us for 64 and 32 lanes: 75 x 1500
+// x 1000 sigmoid 170 and 159, backward 330 and 314; 38 x 1500 x 2048 decay 146 and 128, 247 and 225; 16 x 4096 x
+// 8192 621 and 580; at 512 strips, 32 x 1500 x 2048 sigmoid 117 and 119, 229 and 235; at 600 tokens, 75 x 600 x 1000
+// 55 and 62). From 257 tokens on, over 280 passes of 300 to 4096 tokens and 300 to 3000 strips this choice is 1.6%
+// slower than the better of the two:
 //     36 x 36 x 8832            forward   one wave 13, four 16, eight 20, 32 lanes 45;       backward  21, 26, 48, 75
 //     497 x 123 x 2016 sigmoid  forward   one wave 157, four 141, eight 143, 32 lanes 235;   backward  310, 284, 318, 395
 //     108 x 157 x 7161          forward   one wave 167, four 154, eight 168, 32 lanes 230;   backward  289, 274, 336, 494
@@ -74,13 +79,14 @@ int64_t state_rows(int64_t L) { return (L + kRun - 1) / kRun; }
 // narrow strips fit 32 bits.
 constexpr int64_t kLeastSegment = 256;   // tokens
 constexpr int64_t kMostGroups = 768;     // work-groups that cutting makes, at most
+constexpr int64_t kWideAtOnce = 512;     // work-groups of 64 lanes that run at a time
 
 Plan plan_for(int64_t batch, int64_t L, int64_t D, int channels, int es, int tensors, bool narrow) {
     auto groups_of = [&](int lanes) { return batch * ((D + lanes * channels - 1) / (lanes * channels)); };
     const int64_t wide = groups_of(64);
     if (L <= kRun || (L <= 8 * kRun && wide >= 768)) return {64, 1, 1, L};
     if (L <= 4 * kRun || (L <= 32 * kRun && wide >= 256)) return {64, 4, 1, L};
-    if (narrow && groups_of(32) >= 2048) return {L < 1024 ? 64 : 32, 8, 1, L};
+    if (narrow && wide > kWideAtOnce) return {L < 1024 ? 64 : 32, 8, 1, L};
     constexpr int kLanes[] = {64, 32, 16};
     constexpr float kToken[] = {6.0e-3f, 3.8e-3f, 3.0e-3f};
     const float elements = (float)(batch * L) * (float)D, once = elements * (float)(es * tensors) / 5.3e6f;
