@@ -93,7 +93,6 @@ template <typename V, int LC, int NW, int TT> struct Place {
     static constexpr int kSub = 64 / LC;         // runs per wave
     static constexpr int kRuns = kSub * NW;      // runs per work-group
     static constexpr int kBlock = kRuns * TT;    // tokens per block
-    static constexpr int kChannels = LC * V::n;  // channels per strip
 };
 
 // One tensor's rows as a strip walks them in scan order (kRev: from the last token down).  A row's address
@@ -409,7 +408,7 @@ __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const 
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 const float a = on ? k[v].a : 1.0f, x = on ? in[v] : 0.0f;
-                run.H[v] = __builtin_fmaf(a, run.H[v], x);
+                run.H[v] = gated_advance(run.H[v], a, x);
                 run.A[v] *= a;
             }
         }
@@ -503,7 +502,7 @@ __global__ __launch_bounds__(NW * 64, kSave && LC == 64 ? 4 : 1) void gated_scan
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 const float a = on ? k[v].a : 1.0f, x = on ? in[v] : 0.0f;
-                run.H[v] = __builtin_fmaf(a, run.H[v], x);
+                run.H[v] = gated_advance(run.H[v], a, x);
                 run.A[v] *= a;
                 A[i][v] = run.A[v];
                 H[i][v] = run.H[v];
@@ -643,7 +642,7 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 const float a = on ? k[v].a : 1.0f, x = on ? in[v] : 0.0f;
-                run.H[v] = __builtin_fmaf(a, run.H[v], x);
+                run.H[v] = gated_advance(run.H[v], a, x);
                 run.A[v] *= a;
                 A[i][v] = run.A[v];
                 H[i][v] = run.H[v];

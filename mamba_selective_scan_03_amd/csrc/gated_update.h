@@ -3,7 +3,8 @@
 // One fp32 state per channel (no expansion over d_state), its gate g an input like u:
 //     decay form     a = exp(g)       h <- a h + u
 //     sigmoid form   a = sigmoid(g)   h <- a h + b u,   b = 1 - a = sigmoid(-g)
-// Every kernel of the recurrence takes a and b from gate() and advances with gated_advance().
+// Every kernel of the recurrence takes a and b from gate() and walks along tokens, be it with a state or with a run's
+// map, by gated_advance().
 //
 // Backward.  With G_t = dL/dh_t and c_t = a_t G_t, the gradient that token t hands to token t-1,
 //     G_t = dy_t + c_{t+1},   c_t = a_t G_t       (a reverse scan of the same affine kind)

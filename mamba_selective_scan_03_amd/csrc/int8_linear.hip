@@ -35,8 +35,8 @@ void launch_quantize(const void *x, int8_t *q, float *scale, int64_t M, int64_t 
     else launch(jscan::quantize_rows_kernel<E, 16, 4>, 1024);
 }
 
-// The tiles of the product and what they take on this chip (us, bf16 output; fitted to 714 products of 1 to 16384
-// rows and columns and 64 to 16384 deep): `start` of a work-group, `round` from one of its stages to the
+// The tiles of the product and what they take on this chip (us, bf16 output; fitted to 710 products of random sizes
+// up to 16384, times in profiles/sweep_int8_tiles.txt): `start` of a work-group, `round` from one of its stages to the
 // next, `stage` of a CU's work for one stage of one tile, with `per_cu` work-groups side by side on a CU.
 struct Tile {
     int bm, bn, groups, threads, per_cu;
