@@ -389,22 +389,17 @@ __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const 
     auto load = [&](word(&gd)[TT], word(&xd)[TT], int64_t i0) {
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
-            int64_t r = i0 + i;
-            if constexpr (kWholeRuns)
-                if (i0 == 0) r = max(i, first);
-            gd[i] = *reinterpret_cast<const word *>(gp + r * step * gs.ld);
-            xd[i] = *reinterpret_cast<const word *>(xp + r * step * xs.ld);
+            gd[i] = *reinterpret_cast<const word *>(gp + (i0 + i) * step * gs.ld);
+            xd[i] = *reinterpret_cast<const word *>(xp + (i0 + i) * step * xs.ld);
         }
     };
-    load(gw, xw, 0);
-    for (int64_t i0 = 0; i0 < per; i0 += TT) {
-        load(gn, xn, i0 + TT < per ? i0 + TT : i0);
+    auto walk = [&](const word(&gd)[TT], const word(&xd)[TT], auto is_first) {
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
             Gate k[N];
             float in[N];
-            scan_terms<V, F, kRev>(gw[i], xw[i], k, in);
-            const bool on = !kWholeRuns || i0 + i >= first;
+            scan_terms<V, F, kRev>(gd[i], xd[i], k, in);
+            const bool on = !decltype(is_first)::value || i >= first;
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 const float a = on ? k[v].a : 1.0f, x = on ? in[v] : 0.0f;
@@ -412,6 +407,25 @@ __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const 
                 run.A[v] *= a;
             }
         }
+    };
+    int64_t i0 = 0;
+    if constexpr (kWholeRuns) {   // the first block by itself, its positions without a token taken at the first one
+        word gf[TT], xf[TT];
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            const int64_t r = max(i, first);
+            gf[i] = *reinterpret_cast<const word *>(gp + r * step * gs.ld);
+            xf[i] = *reinterpret_cast<const word *>(xp + r * step * xs.ld);
+        }
+        i0 = TT;
+        if (i0 < per) load(gw, xw, i0);
+        walk(gf, xf, std::true_type{});
+    } else {
+        load(gw, xw, 0);
+    }
+    for (; i0 < per; i0 += TT) {
+        load(gn, xn, i0 + TT < per ? i0 + TT : i0);
+        walk(gw, xw, std::false_type{});
 #pragma unroll
         for (int i = 0; i < TT; ++i) gw[i] = gn[i], xw[i] = xn[i];
     }
