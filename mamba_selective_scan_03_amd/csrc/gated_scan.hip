@@ -344,7 +344,7 @@ jscan_status backward(BackwardArgs a, int64_t workspace_bytes, jscan_gate_form f
     return launch_args<kSaved>(a, t, dtype, form, true);
 }
 
-// Four channels a thread where D, the strides and the addresses allow it (256 x 8192 bf16 4.8 us, 6.1 TB/s), or one
+// Four channels a thread where D, the strides and the addresses allow it (256 x 8192 bf16 5.1 us, 5.8 TB/s), or one
 // (256 x 8191: 6.9 us).
 template <typename E, GateForm F>
 jscan_status launch_step(float *h, const void *g, const void *u, void *y, int64_t batch, int64_t D, int64_t ld_g,

@@ -447,7 +447,7 @@ __global__ __launch_bounds__(NW * 64) void gated_summary_kernel(TokenRows<const 
 
 // Forward scan of a strip.  Memory bounds it: 16 x 4096 x 8192 bf16 sigmoid in 587 us, 5.5 TB/s, with the
 // traffic of the algorithm (2.15 GB read, 1.07 GB written); 1 x 65536 x 1024 in 32 segments in 73 us behind
-// their maps, 5.5 TB/s.
+// their maps, 5.5 TB/s.  Few strips leave one chain a CU: 3 x 6225 x 3864 decay with states 119 us, 4.2 TB/s.
 // kSave: the state before each thread's run is kept for the backward pass, 0.5 bytes an element beside 6 (8 x 4096 x
 // 8192 336 us, without 308); four waves a SIMD are asked for, which the kernels of 64 lanes have without it (else
 // 140 VGPRs, one work-group a CU).
@@ -748,7 +748,7 @@ __global__ __launch_bounds__(NW * 64) void gated_backward_kernel(
 
 // One decode token, the state in place: kVec channels of one sequence per thread, in accesses of up to 16
 // bytes where all rows start on kVec elements (14 bytes an element of bf16, 8 of them the state).  256 x
-// 8192 bf16 in 4.8 us, 6.1 TB/s; one sequence is a launch's latency, 2.1 us.
+// 8192 bf16 in 5.1 us, 5.8 TB/s; one sequence is a launch's latency, 2.3 us.
 template <typename E, GateForm F, int kVec>
 __global__ __launch_bounds__(256) void gated_step_kernel(float *__restrict__ h,
                                                          const typename E::store_t *__restrict__ g,

@@ -69,7 +69,7 @@ __device__ __forceinline__ uint32_t pack4(const float *v, float r) {
 
 // Rows that start on 16 bytes, at most 64 kWaves kChunks chunks of 16 bytes long: a row stays in the registers of
 // kWaves waves between its maximum and its quantisation, so x is read once.  Memory bounds it (3 bytes
-// an element of bf16): 65536 x 8192 bf16 in 259 us, 6.2 TB/s.
+// an element of bf16): 65536 x 8192 bf16 in 242 us, 6.7 TB/s.
 template <typename E, int kWaves, int kChunks>
 __global__ __launch_bounds__(kWaves * 64) void quantize_rows_kernel(const typename E::store_t *__restrict__ x,
                                                                     int8_t *__restrict__ q, float *__restrict__ scale,
@@ -222,9 +222,9 @@ template <int NT> __device__ __forceinline__ int w_row(int t, int r) { return (r
 // A BM x BN tile per work-group, K in stages of 128 bytes.  WR x WC waves make the tile; with KG > 1 as
 // many groups of waves take every KG-th stage each and add their sums through LDS at the end, which
 // shortens the chain of stages where tiles are too few to fill the chip. 16384 x 16384 x 4096 with 256 x
-// 256 tiles in 0.94 ms, 2.3 POP/s: the power limit holds the clock at about 1.6 GHz, and the matrix cores
-// are busy for 60% of it.  1 x 16384 x 4096 in 16 us with w read from memory, 4.2 TB/s (11.6 us from the
-// last-level cache).  77 x 4096 x 8192 in 13.7 us: the latency of the stages.  A stage's rows of q and w
+// 256 tiles in 0.95 ms, 2.3 POP/s: the power limit holds the clock at about 1.6 GHz, and the matrix cores
+// are busy for 57 to 60% of it.  1 x 16384 x 4096 in 17.6 us with w read from memory, 3.8 TB/s (11.9 us from the
+// last-level cache).  77 x 4096 x 8192 in 14.5 us (13.0): the latency of the stages.  A stage's rows of q and w
 // go from memory straight into LDS, kBufs - 1 stages (one to three) ahead of the products.  A row's eight 16-byte
 // chunks are permuted by (row / 2) % 8, so that the 16 rows of one operand read fall on distinct banks.
 namespace tiled {
