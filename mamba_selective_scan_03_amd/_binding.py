@@ -684,16 +684,17 @@ def _check_states(states, g):
 
 
 def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, workspace=None, states=None):
-    """Gated recurrence over whole sequences (``jscan_gated_scan``), not recorded by autograd (its gradients are
-    :func:`gated_scan_backward`'s; tensors that require them are refused outside of ``torch.no_grad()``).  g, u ``[batch, L, D]`` (bf16 or
+    """Gated recurrence over whole sequences (``jscan_gated_scan``).  g, u ``[batch, L, D]`` (bf16 or
     fp32; rows may be slices of a wider projection): ``h_t = a h_{t-1} + u_t`` with ``a = exp(g_t)``
     (form "decay"), or ``h_t = a h_{t-1} + (1 - a) u_t`` with ``a = sigmoid(g_t)`` (form "sigmoid").  h0
     ``[batch, D]`` fp32; ``lengths`` int32 ``[batch]`` for padded sequences (y is zero in the padding).
     Returns ``(y [batch, L, D] in g's dtype, h_final [batch, D] fp32)``; ``h_final`` may be ``h0``.  For training
-    in bf16, ``states`` from :func:`gated_scan_states` keeps fp32 states for the backward pass.  ``g = -inf`` drops a
-    finite state (a reset inside a row); an infinity or a NaN stays in its channel to the end of its sequence.  Decays above
-    one (g > 0 in the decay form) have to multiply to a finite fp32 number over any run of tokens: runs are
-    composed before they meet their starting state."""
+    in bf16, ``states`` from :func:`gated_scan_states` keeps fp32 states for the backward pass.
+
+    ``g = -inf`` drops a finite state (a reset inside a row); an infinity or a NaN stays in its channel to the
+    end of its sequence.  Decays above one (g > 0 in the decay form) have to multiply to a finite fp32 number over
+    any run of tokens: runs are composed before they meet their starting state.  Autograd does not record the
+    call: tensors that require gradients are refused where it would (:func:`gated_scan_backward` has them)."""
     if g.requires_grad or u.requires_grad or (h0 is not None and h0.requires_grad):
         _refuse_grad()
     _check_gated(g, form, lengths)
