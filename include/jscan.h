@@ -548,6 +548,67 @@ jscan_status jscan_matmul_i8(const int8_t *q, const float *q_scale, const int8_t
                              const float *w_scale, const float *bias, void *out, int64_t M, int64_t N,
                              int64_t K, int64_t ld_out, jscan_dtype dtype, void *stream);
 
+/*
+ * Activations of the calls below, applied in fp32 before a result is rounded:
+ *     JSCAN_ACT_SILU        v sigmoid(v)
+ *     JSCAN_ACT_GELU_TANH   v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2
+ */
+typedef enum { JSCAN_ACT_NONE = 0, JSCAN_ACT_SILU = 1, JSCAN_ACT_GELU_TANH = 2 } jscan_activation;
+
+/*
+ * Short causal convolution in front of a scan: every channel over its own last W tokens (W = 2, 3 or 4).
+ *     y_t[d] = act(bias[d] + sum_{k < W} w[d][k] e_{t+k}[d])
+ * with e the W - 1 tokens of `state` followed by x_0, x_1, ..., so w[d][W-1] weighs the token itself.  Sums are
+ * fp32.  act is JSCAN_ACT_NONE or JSCAN_ACT_SILU (JSCAN_ERR_FORM otherwise).
+ *   x, y       batch * L token rows of D values in `dtype`, row strides ld_x, ld_y >= D as for
+ *              jscan_gated_scan: x may be a half of a wider projection.  Any D >= 0; pointers are aligned to their
+ *              elements
+ *   state      [batch][W-1][D] in `dtype`, the tokens before the first (oldest first), or NULL for zeros
+ *   w, bias    [D][W] and [D] fp32; bias may be NULL
+ *   lengths    [batch] int32 or NULL, as for jscan_gated_scan: later rows of x are not read, later rows of y are
+ *              set to zero
+ *   state_out  [batch][W-1][D] out, the last W - 1 tokens of every sequence (the starting state's among them where
+ *              it is shorter), or NULL when it is not wanted; may equal state
+ * With L == 0, x and y may be NULL.  Errors as above.
+ */
+jscan_status jscan_causal_conv(const void *x, const void *state, const float *w, const float *bias,
+                               const int32_t *lengths, void *y, void *state_out, int64_t batch,
+                               int64_t L, int64_t D, int64_t W, int64_t ld_x, int64_t ld_y,
+                               jscan_activation activation, jscan_dtype dtype, void *stream);
+
+/*
+ * Backward pass of jscan_causal_conv.  With z_t = dy_t act'(v_t), v_t the sum that the activation takes,
+ *     de_i = sum_k w[k] z_{i-k}  (and dstate_out's rows at the places that state_out was taken from)
+ *     dw[d][k] = sum_t z_t e_{t+k},   dbias[d] = sum_t z_t       over all tokens of all sequences
+ * v is formed anew from x, in fp32; z is not rounded; every sum is fp32, in a fixed order (no atomics).
+ *   x, state, w, bias, lengths   as given to the forward pass
+ *   dy          token rows like x;   dstate_out [batch][W-1][D] in `dtype`, NULL for zeros
+ *   dx          token rows out, zero in the padding;   dstate [batch][W-1][D] out, NULL when it is not wanted
+ *   dw, dbias   [D][W] and [D] fp32 out; dbias may be NULL
+ *   workspace   jscan_causal_conv_backward_workspace(batch, L, D, W) bytes, 16-byte aligned, overlapping nothing
+ *               else.  Contents on entry do not matter.  Calls that share it must be ordered on one stream.
+ * Without any sequence (batch == 0) dw and dbias are set to zeros.
+ */
+jscan_status jscan_causal_conv_backward(const void *x, const void *state, const float *w,
+                                        const float *bias, const int32_t *lengths, const void *dy,
+                                        const void *dstate_out, void *dx, void *dstate, float *dw,
+                                        float *dbias, int64_t batch, int64_t L, int64_t D, int64_t W,
+                                        int64_t ld_x, int64_t ld_dy, int64_t ld_dx, void *workspace,
+                                        int64_t workspace_bytes, jscan_activation activation,
+                                        jscan_dtype dtype, void *stream);
+
+/* Workspace bytes of jscan_causal_conv_backward for this shape, or -1 if the shape is invalid.  Host-only. */
+int64_t jscan_causal_conv_backward_workspace(int64_t batch, int64_t L, int64_t D, int64_t W);
+
+/*
+ * One decode token of the convolution for a batch: state [batch][W-1][D] in place (its oldest token leaves, x_t
+ * joins); x_t and y_t are batch rows of D values with row strides ld_x, ld_y >= D.
+ */
+jscan_status jscan_causal_conv_step(void *state, const void *x_t, const float *w, const float *bias,
+                                    void *y_t, int64_t batch, int64_t D, int64_t W, int64_t ld_x,
+                                    int64_t ld_y, jscan_activation activation, jscan_dtype dtype,
+                                    void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *jscan_status_string(jscan_status s);
 

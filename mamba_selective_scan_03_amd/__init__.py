@@ -26,12 +26,20 @@ There is no CPU fallback: without the built library every call raises.
     y_t = gated_step(h, g_t, u_t)                          # its decode token, h in place
     q, q_scale = quantize_rows(x)                          # activations to int8, a scale per token
     out = matmul_i8(q, q_scale, w, w_scale)                # int8 projection, a scale per output channel
+    y, state = causal_conv(x, w, bias, state)              # short causal convolution in front of a scan
+    dx, dw, dbias, dstate = causal_conv_backward(x, w, dy, bias, state)   # its gradients
+    y_t = causal_conv_step(state, x_t, w, bias)            # its decode token, the state in place
 """
 from ._binding import (  # noqa: F401
     A_FORMS,
+    ACTIVATIONS,
     D_STATE,
     GATE_FORMS,
     JScanError,
+    causal_conv,
+    causal_conv_backward,
+    causal_conv_step,
+    causal_conv_workspace_bytes,
     chunked_workspace_bytes,
     gated_scan,
     gated_scan_backward,

@@ -77,13 +77,20 @@ def library():
     lib.jscan_gated_scan_workspace.restype = i64
     lib.jscan_quantize_rows.argtypes = [vp, vp, fp, i64, i64, i64, i32, vp]
     lib.jscan_matmul_i8.argtypes = [vp, fp, vp, fp, fp, vp, i64, i64, i64, i64, i32, vp]
+    lib.jscan_causal_conv.argtypes = [vp, vp, fp, fp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i32, i32, vp]
+    lib.jscan_causal_conv_backward.argtypes = [vp, vp, fp, fp, vp, vp, vp, vp, vp, fp, fp, i64, i64, i64, i64, i64, i64,
+                                               i64, vp, i64, i32, i32, vp]
+    lib.jscan_causal_conv_step.argtypes = [vp, vp, fp, fp, vp, i64, i64, i64, i64, i64, i32, i32, vp]
+    lib.jscan_causal_conv_backward_workspace.argtypes = [i64, i64, i64, i64]
+    lib.jscan_causal_conv_backward_workspace.restype = i64
     lib.jscan_prefill_chunked_workspace.restype = i64
     for f in (lib.jscan_prefill, lib.jscan_prefill_resume, lib.jscan_step, lib.jscan_prefill_chunked,
               lib.jscan_prefill_scalar_a, lib.jscan_step_scalar_a, lib.jscan_prefill_complex, lib.jscan_step_complex,
               lib.jscan_prefill_trapezoid, lib.jscan_step_trapezoid, lib.jscan_prefill_mimo, lib.jscan_step_mimo,
               lib.jscan_prefill_mimo_trapezoid, lib.jscan_step_mimo_trapezoid, lib.jscan_gated_scan,
               lib.jscan_gated_scan_backward, lib.jscan_gated_scan_save, lib.jscan_gated_scan_backward_saved,
-              lib.jscan_gated_step, lib.jscan_quantize_rows, lib.jscan_matmul_i8):
+              lib.jscan_gated_step, lib.jscan_quantize_rows, lib.jscan_matmul_i8, lib.jscan_causal_conv,
+              lib.jscan_causal_conv_backward, lib.jscan_causal_conv_step):
         f.restype = i32
     lib.jscan_status_string.argtypes = [i32]
     lib.jscan_status_string.restype = ctypes.c_char_p
@@ -598,7 +605,7 @@ def _refuse_grad():
     """For calls on tensors that require gradients, which autograd would lose without a word where it records."""
     if torch.is_grad_enabled():
         _bad("autograd does not record this call: make it under torch.no_grad(), on detached tensors, or inside a "
-             "torch.autograd.Function whose backward gives its gradients (gated_scan_backward for gated_scan)")
+             "torch.autograd.Function whose backward gives its gradients (gated_scan_backward for gated_scan, and so on)")
 
 
 def _check_like(name, t, shape, dtype, dev):
@@ -657,7 +664,11 @@ def gated_scan_workspace_bytes(batch: int, L: int, D: int) -> int:
 
 
 def _gated_workspace(workspace, batch, L, D, dev):
-    need = gated_scan_workspace_bytes(batch, L, D)
+    return _workspace(workspace, gated_scan_workspace_bytes(batch, L, D), dev)
+
+
+def _workspace(workspace, need, dev):
+    """The caller's workspace, or a new one of `need` bytes (None for 0), and its size."""
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is None:
@@ -880,3 +891,145 @@ def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
     _launch("jscan_matmul_i8", dev, q.data_ptr(), q_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
             _addr(bias), out.data_ptr(), lead.numel(), N, K, ld_out, _DTYPES[out.dtype])
     return out
+
+
+# ---- short causal convolution ----------------------------------------------------------------
+# jscan_activation values.
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu_tanh": 2}
+
+
+def _conv_activation(name):
+    if name not in ("none", "silu"):
+        _bad('activation must be "none" or "silu"')
+    return ACTIVATIONS[name]
+
+
+def _check_conv(x, w, bias, state, lengths):
+    """The width W of the taps and the shape of the state."""
+    if not x.is_cuda:
+        _bad("inputs must be CUDA (HIP) tensors")
+    if x.dtype not in _DTYPES:
+        _bad("x must be bfloat16 or float32")
+    if x.dim() != 3:
+        _bad("x must be [batch, L, D]")
+    dev = x.device
+    batch, L, D = x.shape
+    if w.dim() != 2 or not 2 <= w.shape[1] <= 4:
+        _bad(f"w must be [D, W] with W = 2, 3 or 4, got {tuple(w.shape)}")
+    W = w.shape[1]
+    _check_flat("w", w, (D, W), _F32, dev)
+    _check_flat("bias", bias, (D,), _F32, dev)
+    _check_flat("state", state, (batch, W - 1, D), x.dtype, dev)
+    _check_flat("lengths", lengths, (batch,), _I32, dev)
+    return W
+
+
+def causal_conv(x, w, bias=None, state=None, lengths=None, activation="silu", y=None, state_out=None):
+    """Short causal convolution of every channel over its own last W tokens (``jscan_causal_conv``), as it stands before
+    a scan: ``y_t = act(bias + sum_k w[:, k] x_{t - (W - 1) + k})``.  x ``[batch, L, D]`` (bf16 or fp32; rows may be
+    slices of a wider projection), w ``[D, W]`` and bias ``[D]`` fp32 with W = 2, 3 or 4, ``activation`` "silu" or
+    "none".  ``state`` ``[batch, W - 1, D]`` in x's dtype are the tokens before the first, oldest first (None: zeros);
+    ``lengths`` int32 ``[batch]`` for padded sequences (y is zero in the padding).  Returns ``(y, state_out)``:
+    ``state_out`` holds each sequence's last W - 1 tokens, for the next call or :func:`causal_conv_step`, and may be
+    ``state`` itself.  Autograd does not record the call (:func:`causal_conv_backward` has its gradients)."""
+    if x.requires_grad or any(t is not None and t.requires_grad for t in (w, bias, state)):
+        _refuse_grad()
+    code = _conv_activation(activation)
+    W = _check_conv(x, w, bias, state, lengths)
+    shape, dev, dtype = x.shape, x.device, x.dtype
+    batch, L, D = shape
+    ld_x = _token_rows("x", x, x, shape)
+    if y is None:
+        y, ld_y = torch.empty(batch, L, D, dtype=dtype, device=dev), D
+    else:
+        ld_y = _token_rows("y", y, x, shape)
+    if state_out is None:
+        state_out = torch.empty(batch, W - 1, D, dtype=dtype, device=dev)
+    else:
+        _check_flat("state_out", state_out, (batch, W - 1, D), dtype, dev)
+    _launch("jscan_causal_conv", dev, x.data_ptr(), _addr(state), w.data_ptr(), _addr(bias), _addr(lengths), y.data_ptr(),
+            state_out.data_ptr(), batch, L, D, W, ld_x, ld_y, code, _DTYPES[dtype])
+    return y, state_out
+
+
+def causal_conv_workspace_bytes(batch: int, L: int, D: int, W: int) -> int:
+    """Bytes of workspace ``causal_conv_backward`` needs."""
+    n = library().jscan_causal_conv_backward_workspace(batch, L, D, W)
+    if n < 0:
+        raise ValueError(f"invalid shape: batch={batch} L={L} D={D} W={W}")
+    return n
+
+
+def causal_conv_backward(x, w, dy, bias=None, state=None, dstate_out=None, lengths=None, activation="silu", dx=None,
+                         dw=None, dbias=None, dstate=None, workspace=None):
+    """Gradients of :func:`causal_conv` (``jscan_causal_conv_backward``): x, w, bias, state, lengths and activation as
+    given to it, dy ``[batch, L, D]`` and optionally dstate_out ``[batch, W - 1, D]`` (x's dtype) the gradients of its
+    results.  Returns ``(dx, dw, dbias, dstate)``: dx and dstate in x's dtype, dw ``[D, W]`` and dbias ``[D]`` fp32
+    sums over all tokens; dbias is None without a bias and dstate without a state.  dx may be given as a slice of a
+    wider gradient."""
+    if any(t is not None and t.requires_grad for t in (x, w, dy, bias, state, dstate_out)):
+        _refuse_grad()
+    code = _conv_activation(activation)
+    W = _check_conv(x, w, bias, state, lengths)
+    shape, dev, dtype = x.shape, x.device, x.dtype
+    batch, L, D = shape
+    past = (batch, W - 1, D)
+    ld_x, ld_dy = _token_rows("x", x, x, shape), _token_rows("dy", dy, x, shape)
+    _check_flat("dstate_out", dstate_out, past, dtype, dev)
+    if dx is None:
+        dx, ld_dx = torch.empty(batch, L, D, dtype=dtype, device=dev), D
+    else:
+        ld_dx = _token_rows("dx", dx, x, shape)
+    if dw is None:
+        dw = torch.empty(D, W, dtype=_F32, device=dev)
+    else:
+        _check_flat("dw", dw, (D, W), _F32, dev)
+    if bias is None:
+        if dbias is not None:
+            _bad("dbias goes with a bias")
+    elif dbias is None:
+        dbias = torch.empty(D, dtype=_F32, device=dev)
+    else:
+        _check_flat("dbias", dbias, (D,), _F32, dev)
+    if state is None:
+        if dstate is not None:
+            _bad("dstate goes with a state")
+    elif dstate is None:
+        dstate = torch.empty(batch, W - 1, D, dtype=dtype, device=dev)
+    else:
+        _check_flat("dstate", dstate, past, dtype, dev)
+    workspace, ws_bytes = _workspace(workspace, causal_conv_workspace_bytes(batch, L, D, W), dev)
+    _launch("jscan_causal_conv_backward", dev, x.data_ptr(), _addr(state), w.data_ptr(), _addr(bias), _addr(lengths),
+            dy.data_ptr(), _addr(dstate_out), dx.data_ptr(), _addr(dstate), dw.data_ptr(), _addr(dbias), batch, L, D, W,
+            ld_x, ld_dy, ld_dx, _addr(workspace), ws_bytes, code, _DTYPES[dtype])
+    return dx, dw, dbias, dstate
+
+
+def causal_conv_step(state, x_t, w, bias=None, activation="silu", y_t=None):
+    """One decode token of the convolution (``jscan_causal_conv_step``): state ``[batch, W - 1, D]`` in x_t's dtype is
+    updated in place (x_t joins, the oldest token leaves); x_t ``[batch, D]`` may be a strided view, e.g. ``x[:, t]``.
+    Returns y_t ``[batch, D]``: a new contiguous tensor, or the given ``y_t``, whose rows may be strided too."""
+    if state.requires_grad or x_t.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad):
+        _refuse_grad()
+    code = _conv_activation(activation)
+    if not state.is_cuda or state.dtype not in _DTYPES or state.dim() != 3 or not state.is_contiguous():
+        _bad("state must be a contiguous bfloat16 or float32 [batch, W - 1, D] CUDA tensor")
+    dev, dtype = state.device, state.dtype
+    batch, past, D = state.shape
+    if not 1 <= past <= 3:
+        _bad(f"state must be [batch, W - 1, D] with W = 2, 3 or 4, got {tuple(state.shape)}")
+    _check_flat("w", w, (D, past + 1), _F32, dev)
+    _check_flat("bias", bias, (D,), _F32, dev)
+    shape = (batch, D)
+    ld_x, one_x = _matrix("x_t", x_t, shape, dtype, dev)
+    if y_t is None:
+        y_t, ld_y, one_y = torch.empty(batch, D, dtype=dtype, device=dev), D, 1
+    else:
+        ld_y, one_y = _matrix("y_t", y_t, shape, dtype, dev)
+    if D > 1 and not one_x == one_y == 1:
+        _bad("the rows of x_t and y_t must be contiguous")
+    if batch <= 1:
+        ld_x = ld_y = D
+    _launch("jscan_causal_conv_step", dev, state.data_ptr(), x_t.data_ptr(), w.data_ptr(), _addr(bias), y_t.data_ptr(), batch,
+            D, past + 1, ld_x, ld_y, code, _DTYPES[dtype])
+    return y_t

@@ -1,0 +1,39 @@
+// activation.h - the activations that the layer's kernels apply in fp32 before a result is rounded.
+//
+//     silu(v)      = v sigmoid(v)
+//     gelu_tanh(v) = v (1 + tanh(u)) / 2 = v sigmoid(2 u),   u = sqrt(2 / pi) (v + 0.044715 v^3)
+#pragma once
+
+#include "scan_update.h"
+
+namespace jscan {
+
+enum class Act : int { None, Silu, GeluTanh };
+
+// 1 / (1 + e^-v) with the hardware exponential and reciprocal, one unit each; relative precision holds on both sides
+// down to the smallest normal number (e^-v = inf gives 0).
+__device__ __forceinline__ float sigmoid_f32(float v) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
+}
+
+template <Act A> __device__ __forceinline__ float activate(float v) {
+    if constexpr (A == Act::Silu) return v * sigmoid_f32(v);
+    if constexpr (A == Act::GeluTanh) {
+        constexpr float kTwoRoot = 1.59576912160573071176f;   // 2 sqrt(2 / pi)
+        return v * sigmoid_f32(kTwoRoot * __builtin_fmaf(0.044715f * v * v, v, v));
+    }
+    return v;
+}
+
+// The same with the activation as a value that is the same in every lane.
+__device__ __forceinline__ float activate(float v, Act a) {
+    return a == Act::Silu ? activate<Act::Silu>(v) : a == Act::GeluTanh ? activate<Act::GeluTanh>(v) : v;
+}
+
+// d silu(v) / dv = g (1 + v (1 - g)), g = sigmoid(v)
+__device__ __forceinline__ float silu_slope(float v) {
+    const float g = sigmoid_f32(v);
+    return g * __builtin_fmaf(v, 1.0f - g, 1.0f);
+}
+
+}  // namespace jscan

@@ -11,33 +11,6 @@ namespace {
 
 bool form_ok(jscan_gate_form f) { return f == JSCAN_GATE_DECAY || f == JSCAN_GATE_SIGMOID; }
 
-// Sizes that the index arithmetic of the kernels holds: rows of D and grids in 32 bits, byte
-// offsets in 63.
-bool shape_ok(int64_t batch, int64_t L, int64_t D) {
-    return batch >= 0 && L >= 0 && D >= 0 && D <= (1 << 24) && batch <= (1 << 20) && L < ((int64_t)1 << 31) &&
-           batch * ((D + 63) / 64) <= kMaxBlocks;
-}
-bool ld_ok(int64_t ld, int64_t rows, int64_t D) { return ld >= D && (rows == 0 || ld <= ((int64_t)1 << 58) / rows); }
-
-struct Pair {
-    const void *p;
-    int64_t ld;
-};
-
-Rows rows_of(Pair t, int64_t rows, int64_t D, int64_t es) { return Rows{t.p, t.p ? rows : 0, D * es, t.ld * es}; }
-Rows flat(const void *p, int64_t bytes) { return Rows{p, p && bytes > 0 ? 1 : 0, bytes, bytes}; }
-
-// Whether an output shares memory with an input or with another output.
-template <int NO, int NI> bool any_overlap(const Rows (&out)[NO], const Rows (&in)[NI]) {
-    for (int i = 0; i < NO; ++i) {
-        for (int j = 0; j < NI; ++j)
-            if (overlaps(out[i], in[j])) return true;
-        for (int j = i + 1; j < NO; ++j)
-            if (overlaps(out[i], out[j])) return true;
-    }
-    return false;
-}
-
 // How a call is laid out: strips of `lanes` lanes, `waves` waves a work-group, n_seg segments of seg_len tokens.
 struct Plan {
     int lanes, waves;

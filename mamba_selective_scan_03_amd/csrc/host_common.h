@@ -66,5 +66,32 @@ constexpr int64_t kMaxBlocks = (int64_t)1 << 30;
 // Work-items that one dimension of a launch can count.
 constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;
 
+// Sizes of padded batches that the index arithmetic of the kernels holds: rows of D and grids in 32 bits, byte
+// offsets in 63.
+inline bool shape_ok(int64_t batch, int64_t L, int64_t D) {
+    return batch >= 0 && L >= 0 && D >= 0 && D <= (1 << 24) && batch <= (1 << 20) && L < ((int64_t)1 << 31) &&
+           batch * ((D + 63) / 64) <= kMaxBlocks;
+}
+inline bool ld_ok(int64_t ld, int64_t rows, int64_t D) { return ld >= D && (rows == 0 || ld <= ((int64_t)1 << 58) / rows); }
+
+struct Pair {
+    const void *p;
+    int64_t ld;
+};
+
+inline Rows rows_of(Pair t, int64_t rows, int64_t D, int64_t es) { return Rows{t.p, t.p ? rows : 0, D * es, t.ld * es}; }
+inline Rows flat(const void *p, int64_t bytes) { return Rows{p, p && bytes > 0 ? 1 : 0, bytes, bytes}; }
+
+// Whether an output shares memory with an input or with another output.
+template <int NO, int NI> bool any_overlap(const Rows (&out)[NO], const Rows (&in)[NI]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NI; ++j)
+            if (overlaps(out[i], in[j])) return true;
+        for (int j = i + 1; j < NO; ++j)
+            if (overlaps(out[i], out[j])) return true;
+    }
+    return false;
+}
+
 }  // namespace host
 }  // namespace jscan
