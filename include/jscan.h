@@ -609,6 +609,37 @@ jscan_status jscan_causal_conv_step(void *state, const void *x_t, const float *w
                                     int64_t ld_y, jscan_activation activation, jscan_dtype dtype,
                                     void *stream);
 
+/*
+ * The selective scan with what follows it in its layer, the skip and the output gate, in one pass:
+ *     y_t[d] = (sum_n C_t[n] h_t[d,n] + skip[d] x_t[d]) silu(z_t[d])
+ * in fp32, rounded once.  skip or z may be NULL (its part is left out; not both).  h is the scan's, bit for bit.
+ *   skip      [D] fp32
+ *   z         batch * L token rows of D values in `dtype`, row stride ld_z >= D (a multiple of 8, at most 2^25), in the
+ *             order of x's rows: z may be a half of a wider projection
+ *   chunk     -1: token by token (jscan_prefill_resume, or the prefill of a_form); 0 or more: time-parallel as
+ *             jscan_prefill_chunked (0 = automatic), for JSCAN_A_DIAGONAL; for the other forms 0 is
+ *             token by token and a given length is JSCAN_ERR_FORM
+ *   workspace jscan_prefill_chunked_workspace(batch, L, D, N, chunk) bytes where chunk >= 0 and a_form is
+ *             JSCAN_A_DIAGONAL; else it may be NULL
+ *   h0        [batch][D][N] fp32 or NULL for zeros; may equal h_final
+ * The other arguments and the errors are those of jscan_prefill_chunked.
+ */
+jscan_status jscan_prefill_gate(const void *x, const void *delta, const float *A, const void *B,
+                                const void *C, const float *h0, const float *skip, const void *z,
+                                void *y, float *h_final, int64_t batch, int64_t L, int64_t D, int64_t N,
+                                int64_t ld_z, int64_t chunk, void *workspace, int64_t workspace_bytes,
+                                jscan_a_form a_form, jscan_dtype dtype, void *stream);
+
+/*
+ * One decode token of it for a batch: jscan_step (or the step of a_form) with the skip and the gate.  z_t's rows
+ * have the stride ld_z >= D (a multiple of 8, at most 2^25).
+ */
+jscan_status jscan_step_gate(float *h, const void *x_t, const void *delta_t, const float *A,
+                             const void *B_t, const void *C_t, const float *skip, const void *z_t,
+                             void *y_t, int64_t batch, int64_t D, int64_t N, int64_t ld_xd,
+                             int64_t ld_bc, int64_t ld_z, int64_t ld_y, jscan_a_form a_form,
+                             jscan_dtype dtype, void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *jscan_status_string(jscan_status s);
 

@@ -26,6 +26,8 @@ There is no CPU fallback: without the built library every call raises.
     y_t = gated_step(h, g_t, u_t)                          # its decode token, h in place
     q, q_scale = quantize_rows(x)                          # activations to int8, a scale per token
     out = matmul_i8(q, q_scale, w, w_scale)                # int8 projection, a scale per output channel
+    y, h_final = prefill_gate(x, delta, A, B, C, skip, z)  # (scan + skip x) silu(z) in one pass
+    y_t = step_gate(h, x_t, delta_t, A, B_t, C_t, skip, z_t)
     y, state = causal_conv(x, w, bias, state)              # short causal convolution in front of a scan
     dx, dw, dbias, dstate = causal_conv_backward(x, w, dy, bias, state)   # its gradients
     y_t = causal_conv_step(state, x_t, w, bias)            # its decode token, the state in place
@@ -54,6 +56,7 @@ from ._binding import (  # noqa: F401
     prefill_chunked_noalloc,
     prefill_complex,
     prefill_fused,
+    prefill_gate,
     prefill_mimo,
     prefill_mimo_trapezoid,
     prefill_scalar_a,
@@ -62,6 +65,7 @@ from ._binding import (  # noqa: F401
     ssm_inputs,
     step,
     step_complex,
+    step_gate,
     step_mimo,
     step_mimo_trapezoid,
     step_raw,

@@ -83,6 +83,9 @@ def library():
     lib.jscan_causal_conv_step.argtypes = [vp, vp, fp, fp, vp, i64, i64, i64, i64, i64, i32, i32, vp]
     lib.jscan_causal_conv_backward_workspace.argtypes = [i64, i64, i64, i64]
     lib.jscan_causal_conv_backward_workspace.restype = i64
+    lib.jscan_prefill_gate.argtypes = [vp, vp, fp, vp, vp, fp, fp, vp, vp, fp, i64, i64, i64, i64, i64, i64, vp, i64, i32,
+                                       i32, vp]
+    lib.jscan_step_gate.argtypes = [fp, vp, vp, fp, vp, vp, fp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i32, i32, vp]
     lib.jscan_prefill_chunked_workspace.restype = i64
     for f in (lib.jscan_prefill, lib.jscan_prefill_resume, lib.jscan_step, lib.jscan_prefill_chunked,
               lib.jscan_prefill_scalar_a, lib.jscan_step_scalar_a, lib.jscan_prefill_complex, lib.jscan_step_complex,
@@ -90,7 +93,7 @@ def library():
               lib.jscan_prefill_mimo_trapezoid, lib.jscan_step_mimo_trapezoid, lib.jscan_gated_scan,
               lib.jscan_gated_scan_backward, lib.jscan_gated_scan_save, lib.jscan_gated_scan_backward_saved,
               lib.jscan_gated_step, lib.jscan_quantize_rows, lib.jscan_matmul_i8, lib.jscan_causal_conv,
-              lib.jscan_causal_conv_backward, lib.jscan_causal_conv_step):
+              lib.jscan_causal_conv_backward, lib.jscan_causal_conv_step, lib.jscan_prefill_gate, lib.jscan_step_gate):
         f.restype = i32
     lib.jscan_status_string.argtypes = [i32]
     lib.jscan_status_string.restype = ctypes.c_char_p
@@ -891,6 +894,89 @@ def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
     _launch("jscan_matmul_i8", dev, q.data_ptr(), q_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
             _addr(bias), out.data_ptr(), lead.numel(), N, K, ld_out, _DTYPES[out.dtype])
     return out
+
+
+# ---- scan with skip and output gate ----------------------------------------------------------
+
+
+def prefill_gate(x, delta, A, B, C, skip=None, z=None, h0=None, form="diagonal", chunk=None, y=None, h_final=None,
+                 workspace=None):
+    """Selective scan with its skip and output gate in one pass (``jscan_prefill_gate``):
+    ``y = (scan(x) + skip * x) * silu(z)``, with ``skip`` ``[D]`` fp32 and z ``[batch, L, D]`` in x's dtype (rows may be a
+    half of a wider projection); either may be None.  Other arguments and results as for :func:`prefill`, A as the
+    ``form`` has it.  ``chunk`` None scans token by token (h_final is bit for bit :func:`prefill`'s); a segment length, or 0
+    for an automatic one, scans as :func:`prefill_chunked` does (form "diagonal"; the others take 0 as None), with a
+    ``workspace`` of :func:`chunked_workspace_bytes` or one that is allocated.  Autograd does not record the call."""
+    if any(t is not None and t.requires_grad for t in (x, delta, A, B, C, skip, z, h0)):
+        _refuse_grad()
+    code = A_FORMS.get(form)
+    if code is None:
+        _bad(f"form must be one of {tuple(A_FORMS)}")
+    batch, L, D = _check_prefill_args(x, delta, A, B, C, h0, scalar_a=form == "scalar")
+    if skip is None and z is None:
+        _bad("skip or z is needed (prefill has neither)")
+    if chunk is not None and chunk < 0:
+        _bad("chunk must be None, 0 or a segment length")
+    dev = x.device
+    _check_flat("skip", skip, (D,), _F32, dev)
+    ld_z = D if z is None else _token_rows("z", z, x, x.shape)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _check_flat("y", y, x.shape, x.dtype, dev)
+    state = (batch, D, D_STATE)
+    if h_final is None:
+        h_final = torch.empty(state, dtype=_F32, device=dev)
+    else:
+        _check_flat("h_final", h_final, state, _F32, dev)
+    cut = chunk is not None and form == "diagonal"
+    workspace, ws_bytes = _workspace(workspace, chunked_workspace_bytes(batch, L, D, chunk) if cut else 0, dev)
+    _launch("jscan_prefill_gate", dev, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(h0),
+            _addr(skip), _addr(z), y.data_ptr(), h_final.data_ptr(), batch, L, D, D_STATE, ld_z, -1 if chunk is None else chunk,
+            _addr(workspace), ws_bytes, code, _DTYPES[x.dtype])
+    return y, h_final
+
+
+def step_gate(h, x_t, delta_t, A, B_t, C_t, skip=None, z_t=None, form="diagonal", y_t=None):
+    """One decode token of :func:`prefill_gate` (``jscan_step_gate``): h ``[batch, D, 16]`` fp32 in place; x_t, delta_t
+    and z_t ``[batch, D]``, B_t and C_t ``[batch, 16]`` (rows may be strided, x_t's and delta_t's alike and B_t's and C_t's
+    alike).  Returns y_t ``[batch, D]``: a new contiguous tensor, or the given ``y_t``, whose rows may be strided too."""
+    if any(t is not None and t.requires_grad for t in (h, x_t, delta_t, A, B_t, C_t, skip, z_t)):
+        _refuse_grad()
+    code = A_FORMS.get(form)
+    if code is None:
+        _bad(f"form must be one of {tuple(A_FORMS)}")
+    if not h.is_cuda or h.dtype != _F32 or h.dim() != 3 or h.shape[2] != D_STATE or not h.is_contiguous():
+        _bad("h must be a contiguous fp32 [batch, D, 16] CUDA tensor")
+    dev, dtype = h.device, x_t.dtype
+    if dtype not in _DTYPES:
+        _bad("x_t must be bfloat16 or float32")
+    if skip is None and z_t is None:
+        _bad("skip or z_t is needed (step has neither)")
+    batch, D, _ = h.shape
+    shape, pair = (batch, D), (batch, D_STATE)
+    _check_flat("A", A, (D,) if form == "scalar" else (D, D_STATE), _F32, dev)
+    _check_flat("skip", skip, (D,), _F32, dev)
+    ld_x, one_x = _matrix("x_t", x_t, shape, dtype, dev)
+    ld_d, one_d = _matrix("delta_t", delta_t, shape, dtype, dev)
+    ld_b, one_b = _matrix("B_t", B_t, pair, dtype, dev)
+    ld_c, one_c = _matrix("C_t", C_t, pair, dtype, dev)
+    ld_z, one_z = (D, 1) if z_t is None else _matrix("z_t", z_t, shape, dtype, dev)
+    if y_t is None:
+        y_t, ld_y, one_y = torch.empty(batch, D, dtype=dtype, device=dev), D, 1
+    else:
+        ld_y, one_y = _matrix("y_t", y_t, shape, dtype, dev)
+    if not one_x == one_d == one_b == one_c == one_z == one_y == 1:
+        _bad("the rows of x_t, delta_t, B_t, C_t, z_t and y_t must be contiguous")
+    if batch <= 1:
+        ld_x = ld_d = ld_z = ld_y = D
+        ld_b = ld_c = D_STATE
+    if ld_x != ld_d or ld_b != ld_c:
+        _bad("x_t and delta_t must share a row stride, and so must B_t and C_t")
+    _launch("jscan_step_gate", dev, h.data_ptr(), x_t.data_ptr(), delta_t.data_ptr(), A.data_ptr(), B_t.data_ptr(),
+            C_t.data_ptr(), _addr(skip), _addr(z_t), y_t.data_ptr(), batch, D, D_STATE, ld_x, ld_b, ld_z, ld_y, code,
+            _DTYPES[dtype])
+    return y_t
 
 
 # ---- short causal convolution ----------------------------------------------------------------

@@ -36,4 +36,16 @@ __device__ __forceinline__ float silu_slope(float v) {
     return g * __builtin_fmaf(v, 1.0f - g, 1.0f);
 }
 
+// What follows the scan in its layer: out = (y + skip x) silu(z), skip one value per channel.
+// Without a skip or without a gate their part is left out.  z rows start every ld_z elements, in the order of x's.
+struct OutGate {
+    const float *skip;
+    const void *z;
+    int64_t ld_z;
+};
+__device__ __forceinline__ float gated_output(float y, bool skipped, float skip, float x, bool gated, float z) {
+    if (skipped) y = __builtin_fmaf(skip, x, y);
+    return gated ? y * activate<Act::Silu>(z) : y;
+}
+
 }  // namespace jscan

@@ -31,7 +31,7 @@ constexpr int kThreads = kGroups * kPairs;
 // kPairs + p, i = (b * D + d) * N + n, and segment group g of sequence b.  hbuf[row][D][N]
 // holds h_loc on entry and h_in on exit (row = b * n_seg + s); dsum[row][D] holds the
 // segments' delta sums.
-__global__ __launch_bounds__(carry::kThreads) void chunk_carry_kernel(float *__restrict__ hbuf,
+static __global__ __launch_bounds__(carry::kThreads) void chunk_carry_kernel(float *__restrict__ hbuf,
                                                                       const float *__restrict__ dsum,
                                                                       const float *__restrict__ A,
                                                                       const float *__restrict__ h0, int64_t count,

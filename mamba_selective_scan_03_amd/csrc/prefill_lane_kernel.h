@@ -8,6 +8,7 @@
 // token.
 #pragma once
 
+#include "activation.h"
 #include "scan_update.h"
 
 namespace jscan {
@@ -18,13 +19,13 @@ namespace jscan {
 // state, states 2k and 2k+1 form one complex state advanced by advance_complex().  With the
 // exponential-trapezoidal rule (Trap, see trap_left_in) each token also takes in the previous
 // token's input; the token before the row's first is (xp[row][D], bp[row][16]), or none.
-template <typename E, AForm AF = AForm::Diagonal, bool kTrap = false>
+template <typename E, AForm AF = AForm::Diagonal, bool kTrap = false, bool kGate = false>
 __global__ __launch_bounds__(64) void prefill_lane_kernel(
     const typename E::store_t *__restrict__ x, const typename E::store_t *__restrict__ dl,
     const float *__restrict__ A, const typename E::store_t *__restrict__ B,
     const typename E::store_t *__restrict__ C, const float *__restrict__ h0,
     typename E::store_t *__restrict__ y, float *__restrict__ h_final, Segments sg, int D, int blocks_per_row,
-    Trap tr) {
+    Trap tr, OutGate og) {
     const int vrow = blockIdx.x / blocks_per_row;
     const int d = (blockIdx.x - vrow * blocks_per_row) * 64 + threadIdx.x;
     if (d >= D) return;  // no cross-lane work below, so idle lanes may leave
@@ -60,7 +61,12 @@ __global__ __launch_bounds__(64) void prefill_lane_kernel(
         for (int n = 0; n < kDState; ++n) bprev[n] = E::load(static_cast<const S *>(tr.B_prev) + vrow * kDState + n);
     }
 
+    const bool skipped = kGate && og.skip != nullptr, gated = kGate && og.z != nullptr;
+    const S *zr = gated ? static_cast<const S *>(og.z) + row * og.ld_z + d : nullptr;
+    const float skip = skipped ? og.skip[d] : 0.0f;
+
     for (int64_t t = 0; t < span.len; ++t) {
+        const float zv = gated ? E::load(zr + t * og.ld_z) : 0.0f;
         const float xv = E::load(xr + t * D), dv = E::load(dr + t * D);
         float dx = delta_x(dv, xv);
         if constexpr (kTrap) {   // left end point in; q replaces delta * x below
@@ -92,6 +98,7 @@ __global__ __launch_bounds__(64) void prefill_lane_kernel(
                 acc = __builtin_fmaf(E::load(Cr + t * kDState + n), h[n], acc);
             }
         }
+        if constexpr (kGate) acc = gated_output(acc, skipped, skip, xv, gated, zv);
         E::store(yr + t * D, acc);
     }
     if (span.state >= 0) {
@@ -101,8 +108,8 @@ __global__ __launch_bounds__(64) void prefill_lane_kernel(
 }
 
 // Fills the final state when there are no tokens: copies h0, or writes zeros.
-__global__ __launch_bounds__(256) void copy_state_kernel(const float *__restrict__ h0,
-                                                         float *__restrict__ h_final, int64_t count) {
+static __global__ __launch_bounds__(256) void copy_state_kernel(const float *__restrict__ h0,
+                                                                float *__restrict__ h_final, int64_t count) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i < count) h_final[i] = h0 ? h0[i] : 0.0f;
 }

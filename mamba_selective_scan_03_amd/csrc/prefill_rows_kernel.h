@@ -36,12 +36,14 @@
 // leave every state bit-identical (decay 2^0 = 1, input term -0) and their y is not stored.
 //
 // Modes (template parameters): delta computed on the load path from the low-rank projection
-// (kFused), the form of A (AF: diagonal, scaled identity, complex pairs) and the
+// (kFused), the form of A (AF: diagonal, scaled identity, complex pairs), the skip and output gate
+// (kGate: the helper waves, which round y, have x and z of the same tokens at hand) and the
 // exponential-trapezoidal rule
 // (kTrap: the helper waves also stage the left-end weights and the previous token's B, and the
 // scan lane takes the left end point in first, one more DPP-fused FMA per state element).
 #pragma once
 
+#include "activation.h"
 #include "mfma_common.h"
 #include "scan_update.h"
 
@@ -579,9 +581,25 @@ __device__ __forceinline__ void read_final(FinalRegs &F, const float *y_tile, in
         F.w[j] = *reinterpret_cast<const float4 *>(y1 + 4 * j);
     }
 }
+// x and z of the same token and channels, for the skip and the gate.
+template <typename E> struct GateRegs {
+    typename Vec4<E>::raw x[2], z[2];
+};
 template <typename E>
+__device__ __forceinline__ void load_gate(GateRegs<E> &R, const typename E::store_t *xb, const typename E::store_t *zb,
+                                          int64_t t0, int64_t L, int D, int64_t ld_z, int tid) {
+    const int c8 = (tid & 3) * 8;
+    const int64_t t = min(t0 + (tid >> 2), L - 1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        R.x[j] = Vec4<E>::load(xb + t * D + c8 + 4 * j);
+        R.z[j] = Vec4<E>::load(zb + t * ld_z + c8 + 4 * j);
+    }
+}
+template <typename E, bool kGate = false>
 __device__ __forceinline__ void write_final(const FinalRegs &F, typename E::store_t *yb, int64_t t0, int64_t L, int D,
-                                            int tid) {
+                                            int tid, const GateRegs<E> &G = GateRegs<E>{}, const float *skip = nullptr,
+                                            bool skipped = false, bool gated = false) {
     const int t = tid >> 2, c8 = (tid & 3) * 8;
     float o[8];
 #pragma unroll
@@ -590,6 +608,14 @@ __device__ __forceinline__ void write_final(const FinalRegs &F, typename E::stor
         o[4 * j + 1] = F.u[j].y + F.w[j].y;
         o[4 * j + 2] = F.u[j].z + F.w[j].z;
         o[4 * j + 3] = F.u[j].w + F.w[j].w;
+        if constexpr (kGate) {
+            float xv[4], zv[4];
+            Vec4<E>::widen(G.x[j], xv);
+            Vec4<E>::widen(G.z[j], zv);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[4 * j + i] = gated_output(o[4 * j + i], skipped, skip[4 * j + i], xv[i], gated, zv[i]);
+        }
     }
     const int64_t tt = t0 + t;
     if (tt < L) {
@@ -610,14 +636,16 @@ __device__ __forceinline__ void write_final(const FinalRegs &F, typename E::stor
 // (zero when h0 is null).  With kFused, delta is not read: the helper waves compute it from dp (bf16 only).  With
 // a scaled-identity A (AF), A is a[D] (one value per channel) instead of A[D][16]; with a
 // complex state, A[D][16] holds 8 complex entries per channel as (real, imaginary) pairs.  With
-// kTrap the exponential-trapezoidal rule replaces the Euler rule (extra inputs in tr).
-template <typename E, bool kFused = false, AForm AF = AForm::Diagonal, bool kTrap = false>
+// kTrap the exponential-trapezoidal rule replaces the Euler rule (extra inputs in tr); with kGate y
+// leaves through the skip and the gate (og).
+template <typename E, bool kFused = false, AForm AF = AForm::Diagonal, bool kTrap = false, bool kGate = false>
 __global__ __launch_bounds__(rows::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void prefill_rows_kernel(
     const typename E::store_t *__restrict__ x, const typename E::store_t *__restrict__ dl,
     const float *__restrict__ A, const typename E::store_t *__restrict__ B,
     const typename E::store_t *__restrict__ C, const float *__restrict__ h0,
     typename E::store_t *__restrict__ y, float *__restrict__ h_final, Segments sg, int D, int blocks_per_row,
-    int xcd_stride, DeltaProj dp, Trap tr) {
+    int xcd_stride, DeltaProj dp, Trap tr, OutGate og) {
+    static_assert(!kFused || !kGate, "the fused delta path has no output gate");
     static_assert(!kFused || sizeof(typename E::store_t) == 2, "the fused delta path is bf16 only");
     static_assert((AF == AForm::Diagonal && !kTrap) || !kFused,
                   "the other forms of A and the trapezoidal rule run the plain prefill");
@@ -692,6 +720,18 @@ __global__ __launch_bounds__(rows::kThreads) __attribute__((amdgpu_waves_per_eu(
                 bias[u] = *reinterpret_cast<const float4 *>(dp.b_dt + d0 + 16 * u + 4 * (l >> 4));
             }
         }
+        // the gate: tile k's x (again, from the L2) and z arrive while tile k is scanned.  A missing gate reads x
+        const bool skipped = kGate && og.skip != nullptr, gated = kGate && og.z != nullptr;
+        const S *zb = nullptr;
+        int64_t ld_z = D;
+        float skip[8];
+        GateRegs<E> GR[2];
+        if constexpr (kGate) {
+            zb = gated ? static_cast<const S *>(og.z) + row * og.ld_z + d0 : xb;
+            if (gated) ld_z = og.ld_z;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) skip[i] = skipped ? og.skip[d0 + (tid & 3) * 8 + i] : 0.0f;
+        }
         load_tile<E, !kFused, kTrap>(R[0], xb, db, bcb, 0, L, D, tid, pr);
         if constexpr (kCOps) {
             // the C operand tables start as zeros; staging only ever writes each entry's live register
@@ -719,27 +759,30 @@ __global__ __launch_bounds__(rows::kThreads) __attribute__((amdgpu_waves_per_eu(
         // tile earlier.  In the fused mode every tile therefore issues tile k + 3's loads (past the
         // last tile they reload clamped rows, unused) and the loop runs whole pairs of tiles, so
         // that every wait leaves the next tile's loads in flight (fused prefill 2.42 -> 2.16 ms on
-        // 64K x 8192).  The other modes, bound by their scan waves, keep the plain loop.
+        // 64K x 8192).  With the gate every tile issues its loads too, so that tile k's x and z, which
+        // go ahead of tile k + 3's, are waited for while those stay in flight.  The other modes, bound by
+        // their scan waves, keep the plain loop.
+        constexpr bool kEveryLoad = kFused || kGate;
         auto tile = [&](auto cur_c, int k) {
             constexpr int cur = decltype(cur_c)::value, nxt = cur ^ 1;
             if (k + 1 < ntiles) {
                 if constexpr (kFused) fused_delta(dfr[nxt], wf, bias, xch, R[nxt], l);
                 stage_tile<E, AF, kTrap, kCOps>(R[nxt], dx_s[nxt], bc_s[nxt], p_s[nxt], cs_s[nxt],
                                                   (int64_t)(k + 1) * rows::kT, L, tid, a2q, prev_given);
-                if (!kFused && k + 3 < ntiles)
+                if (!kEveryLoad && k + 3 < ntiles)
                     load_tile<E, !kFused, kTrap>(R[nxt], xb, db, bcb, (int64_t)(k + 3) * rows::kT, L, D, tid, pr);
             }
-            if constexpr (kFused) {
+            if constexpr (kGate) load_gate<E>(GR[cur], xb, zb, (int64_t)k * rows::kT, L, D, ld_z, tid);
+            if constexpr (kEveryLoad)
                 load_tile<E, !kFused, kTrap>(R[nxt], xb, db, bcb, (int64_t)(k + 3) * rows::kT, L, D, tid, pr);
-                load_dlow(dfr[nxt], dp.d_low, row, (int64_t)(k + 3) * rows::kT, L, hw, l);
-            }
+            if constexpr (kFused) load_dlow(dfr[nxt], dp.d_low, row, (int64_t)(k + 3) * rows::kT, L, hw, l);
             if (k > 0) {
                 read_final(F, y_s[nxt], tid, kYS);
-                write_final<E>(F, yb, (int64_t)(k - 1) * rows::kT, L, D, tid);
+                write_final<E, kGate>(F, yb, (int64_t)(k - 1) * rows::kT, L, D, tid, GR[nxt], skip, skipped, gated);
             }
             __syncthreads();
         };
-        if constexpr (kFused) {
+        if constexpr (kEveryLoad) {
             int k = 0;
             for (; k + 1 < ntiles; k += 2) {
                 tile(IntConst<0>{}, k);
@@ -753,7 +796,10 @@ __global__ __launch_bounds__(rows::kThreads) __attribute__((amdgpu_waves_per_eu(
             }
         }
         read_final(F, y_s[(ntiles - 1) & 1], tid, kYS);
-        write_final<E>(F, yb, (int64_t)(ntiles - 1) * rows::kT, L, D, tid);
+        if (kGate && ((ntiles - 1) & 1))
+            write_final<E, kGate>(F, yb, (int64_t)(ntiles - 1) * rows::kT, L, D, tid, GR[1], skip, skipped, gated);
+        else
+            write_final<E, kGate>(F, yb, (int64_t)(ntiles - 1) * rows::kT, L, D, tid, GR[0], skip, skipped, gated);
         return;
     }
 
@@ -909,18 +955,18 @@ __global__ __launch_bounds__(rows::kThreads) __attribute__((amdgpu_waves_per_eu(
 inline bool rows_kernel_applies(int64_t /*batch*/, int64_t D) { return D % rows::kCh == 0; }
 
 // Launches one work-group per 32 channels of each of the `nrows` rows described by sg.
-template <typename E, bool kFused = false, AForm AF = AForm::Diagonal, bool kTrap = false>
+template <typename E, bool kFused = false, AForm AF = AForm::Diagonal, bool kTrap = false, bool kGate = false>
 void launch_prefill_rows(const typename E::store_t *x, const typename E::store_t *dl, const float *A,
                          const typename E::store_t *B, const typename E::store_t *C, const float *h0,
                          typename E::store_t *y, float *h_final, const Segments &sg, int64_t nrows,
                          int D, hipStream_t stream, DeltaProj dp = DeltaProj{nullptr, nullptr, nullptr},
-                         Trap tr = Trap{nullptr, nullptr, nullptr}) {
+                         Trap tr = Trap{nullptr, nullptr, nullptr}, OutGate og = OutGate{nullptr, nullptr, 0}) {
     const int blocks_per_row = D / rows::kCh;
     const int64_t blocks = nrows * blocks_per_row;
     const int xcd_stride = (blocks % 8 == 0) ? (int)(blocks / 8) : 0;
-    hipLaunchKernelGGL((prefill_rows_kernel<E, kFused, AF, kTrap>), dim3((unsigned)blocks),
+    hipLaunchKernelGGL((prefill_rows_kernel<E, kFused, AF, kTrap, kGate>), dim3((unsigned)blocks),
                        dim3(rows::kThreads), 0, stream, x, dl, A, B, C, h0, y, h_final, sg, D, blocks_per_row,
-                       xcd_stride, dp, tr);
+                       xcd_stride, dp, tr, og);
 }
 
 }  // namespace jscan

@@ -32,6 +32,7 @@
 
 #include <type_traits>
 
+#include "activation.h"
 #include "scan_update.h"
 
 namespace jscan {
@@ -131,15 +132,17 @@ template <typename E> __device__ __forceinline__ float contract_seq(const float 
 // when h0 is null).  A segment-summary launch (kSummary) writes no y; it writes the row's
 // final state and the sum of the row's delta values to dsum[row][D].  A work-group is
 // kThreads consecutive channels of one row; its waves share no data but the scalar cache.
-// kRowsOrder picks the first segment's summation order (see the file comment).  Offsets are 32-bit:
-// a token row is D * 4 <= 2^26 bytes and no offset spans more than 16 token rows.
-template <typename E, bool kSummary, bool kRowsOrder>
+// kRowsOrder picks the first segment's summation order (see the file comment).  With kGate y leaves
+// through the skip and the gate (og), z read like x.  Offsets are 32-bit:
+// a token row is D * 4 <= 2^26 bytes (z: ld_z * 4 <= 2^27) and no offset spans more than 16 token rows.
+template <typename E, bool kSummary, bool kRowsOrder, bool kGate = false>
 __global__ __launch_bounds__(seglane::kThreads) __attribute__((amdgpu_waves_per_eu(seglane::kWavesPerSimd))) void
 prefill_seg_lane_kernel(const typename E::store_t *__restrict__ x, const typename E::store_t *__restrict__ dl,
                         const float *__restrict__ A, const typename E::store_t *__restrict__ B,
                         const typename E::store_t *__restrict__ C, const float *__restrict__ h0,
                         typename E::store_t *__restrict__ y, float *__restrict__ h_final, float *__restrict__ dsum,
-                        Segments sg, int D, int blocks_per_row) {
+                        Segments sg, int D, int blocks_per_row, OutGate og) {
+    static_assert(!kSummary || !kGate, "a summary writes no y");
     using S = typename E::store_t;
     using IO = SegIO<E>;
     using seglane::kBlock;
@@ -162,20 +165,30 @@ prefill_seg_lane_kernel(const typename E::store_t *__restrict__ x, const typenam
     const S *Bb = B + span.tok0 * kDState, *Cb = C + span.tok0 * kDState;
     const uint32_t rowb = (uint32_t)D * (uint32_t)sizeof(S), vo = (uint32_t)d * (uint32_t)sizeof(S);
 
+    // the gate: a missing one reads x's own rows
+    const bool skipped = kGate && og.skip != nullptr, gated = kGate && og.z != nullptr;
+    const S *zb = gated ? static_cast<const S *>(og.z) + span.tok0 * og.ld_z : xb;
+    const int64_t ld_z = gated ? og.ld_z : D;
+    const uint32_t rowz = (uint32_t)ld_z * (uint32_t)sizeof(S);
+    const float skip = skipped ? og.skip[d] : 0.0f;
+
     // The scan of the row, with the output summed in the rows kernel's order (kRo) or in state
     // order.  One token: the state update and (unless kSummary) the output.
     float dacc = 0.0f;
     auto scan = [&](auto rows_order) {
         constexpr bool kRo = decltype(rows_order)::value;
-        auto token = [&](float xv, float dv, const BcRow<E> &bc, const BcRow<E> &cc, __amdgpu_buffer_rsrc_t ry,
-                         uint32_t so) {
+        auto token = [&](float xv, float dv, float zv, const BcRow<E> &bc, const BcRow<E> &cc,
+                         __amdgpu_buffer_rsrc_t ry, uint32_t so) {
             const float dx = delta_x(dv, xv);
 #pragma unroll
             for (int n = 0; n < kDState; ++n) h[n] = advance(h[n], dv, a2[n], dx, bc[n]);
-            if constexpr (kSummary)
+            if constexpr (kSummary) {
                 dacc += dv;
-            else
-                IO::store(ry, kRo ? contract_row<E>(h, cc) : contract_seq<E>(h, cc), vo, so);
+            } else {
+                float yv = kRo ? contract_row<E>(h, cc) : contract_seq<E>(h, cc);
+                if constexpr (kGate) yv = gated_output(yv, skipped, skip, xv, gated, zv);
+                IO::store(ry, yv, vo, so);
+            }
         };
 
         // x and delta of kSet tokens from t0 (indexes past the row end re-read its last token,
@@ -186,9 +199,10 @@ prefill_seg_lane_kernel(const typename E::store_t *__restrict__ x, const typenam
         constexpr int kRowBytes = kDState * (int)sizeof(S);
         constexpr int kLines = kSet * kRowBytes / 128;
         constexpr int kTouches = seglane::kTouch ? (kSummary ? 1 : 2) * kLines : 0;
-        uint32_t xr[2][kSet], dr[2][kSet], tq[2][kTouches > 0 ? kTouches : 1];
-        auto fetch = [&](uint32_t(&xs)[kSet], uint32_t(&ds)[kSet], uint32_t(&tch)[kTouches > 0 ? kTouches : 1],
-                         int t0) {
+        constexpr int kZ = kGate ? kSet : 1;
+        uint32_t xr[2][kSet], dr[2][kSet], zr[2][kZ], tq[2][kTouches > 0 ? kTouches : 1];
+        auto fetch = [&](uint32_t(&xs)[kSet], uint32_t(&ds)[kSet], uint32_t(&zs)[kZ],
+                         uint32_t(&tch)[kTouches > 0 ? kTouches : 1], int t0) {
             const int tb = t0 < len ? t0 : len - 1;
             if constexpr (kTouches > 0) {
                 const __amdgpu_buffer_rsrc_t rb = seglane::rsrc(Bb + (int64_t)tb * kDState);
@@ -211,13 +225,21 @@ prefill_seg_lane_kernel(const typename E::store_t *__restrict__ x, const typenam
                 xs[j] = IO::load(rx, vo, so);
                 ds[j] = IO::load(rd, vo, so);
             }
+            if constexpr (kGate) {
+                const __amdgpu_buffer_rsrc_t rz = seglane::rsrc(zb + (int64_t)tb * ld_z);
+#pragma unroll
+                for (int j = 0; j < kSet; ++j) {
+                    const int t = t0 + j < len ? t0 + j : len - 1;
+                    zs[j] = IO::load(rz, vo, (uint32_t)(t - tb) * rowz);
+                }
+            }
         };
         // B rows: token t's in set t & 1 (t0 is even), the next token's loaded right after the
         // wait for this token's.  The C row of a token is loaded at the same point and is first
         // used after the token's 16 state updates.
         BcRow<E> bc[2], cc;
         bc[0].load(Bb);
-        auto run = [&](const uint32_t(&xs)[kSet], const uint32_t(&ds)[kSet],
+        auto run = [&](const uint32_t(&xs)[kSet], const uint32_t(&ds)[kSet], const uint32_t(&zs)[kZ],
                        const uint32_t(&tch)[kTouches > 0 ? kTouches : 1], int t0) {
             const __amdgpu_buffer_rsrc_t ry = seglane::rsrc(yb + (int64_t)t0 * D);
 #pragma unroll
@@ -230,7 +252,8 @@ prefill_seg_lane_kernel(const typename E::store_t *__restrict__ x, const typenam
                 bc[cur ^ 1].load(Bb + (int64_t)tn * kDState);
                 if constexpr (!kSummary) cc.load(Cb + (int64_t)(t0 + j) * kDState);
                 __builtin_amdgcn_sched_barrier(0);
-                token(IO::value(xs[j]), IO::value(ds[j]), bc[cur], cc, ry, (uint32_t)j * rowb);
+                token(IO::value(xs[j]), IO::value(ds[j]), kGate ? IO::value(zs[kGate ? j : 0]) : 0.0f, bc[cur], cc, ry,
+                      (uint32_t)j * rowb);
                 if (j == 0) {
                     // the touches are older than this token's x, so they have arrived: retire them
 #pragma unroll
@@ -239,7 +262,7 @@ prefill_seg_lane_kernel(const typename E::store_t *__restrict__ x, const typenam
             }
         };
         const int whole = len - len % kBlock;
-        fetch(xr[0], dr[0], tq[0], 0);
+        fetch(xr[0], dr[0], zr[0], tq[0], 0);
         for (int t0 = 0; t0 < whole; t0 += kBlock) {
             // The SIMD issues from its oldest wave first, so without this the first of its
             // waves would run far ahead and the last would finish alone, at the slow one-wave
@@ -253,12 +276,12 @@ prefill_seg_lane_kernel(const typename E::store_t *__restrict__ x, const typenam
                 __builtin_amdgcn_s_setprio(1);
             else
                 __builtin_amdgcn_s_setprio(0);
-            fetch(xr[1], dr[1], tq[1], t0 + kSet);
+            fetch(xr[1], dr[1], zr[1], tq[1], t0 + kSet);
             __builtin_amdgcn_sched_barrier(0);
-            run(xr[0], dr[0], tq[0], t0);
-            fetch(xr[0], dr[0], tq[0], t0 + kBlock);
+            run(xr[0], dr[0], zr[0], tq[0], t0);
+            fetch(xr[0], dr[0], zr[0], tq[0], t0 + kBlock);
             __builtin_amdgcn_sched_barrier(0);
-            run(xr[1], dr[1], tq[1], t0 + kSet);
+            run(xr[1], dr[1], zr[1], tq[1], t0 + kSet);
         }
         // the last len % 16 tokens, one at a time
         for (int t = whole; t < len; ++t) {
@@ -267,7 +290,9 @@ prefill_seg_lane_kernel(const typename E::store_t *__restrict__ x, const typenam
             if constexpr (!kSummary) c1.load(Cb + (int64_t)t * kDState);
             const int64_t at = (int64_t)t * D;
             const __amdgpu_buffer_rsrc_t rx = seglane::rsrc(xb + at), rd = seglane::rsrc(db + at);
-            token(IO::value(IO::load(rx, vo, 0)), IO::value(IO::load(rd, vo, 0)), b1, c1, seglane::rsrc(yb + at),
+            float zv = 0.0f;
+            if constexpr (kGate) zv = IO::value(IO::load(seglane::rsrc(zb + (int64_t)t * ld_z), vo, 0));
+            token(IO::value(IO::load(rx, vo, 0)), IO::value(IO::load(rd, vo, 0)), zv, b1, c1, seglane::rsrc(yb + at),
                   0);
         }
     };
@@ -285,14 +310,15 @@ prefill_seg_lane_kernel(const typename E::store_t *__restrict__ x, const typenam
     if constexpr (kSummary) dsum[(int64_t)vrow * D + d] = dacc;
 }
 
-template <typename E, bool kSummary, bool kRowsOrder>
+template <typename E, bool kSummary, bool kRowsOrder, bool kGate = false>
 void launch_prefill_seg_lane(const typename E::store_t *x, const typename E::store_t *dl, const float *A,
                              const typename E::store_t *B, const typename E::store_t *C, const float *h0,
                              typename E::store_t *y, float *h_final, float *dsum, const Segments &sg, int64_t nrows,
-                             int D, hipStream_t stream) {
+                             int D, hipStream_t stream, OutGate og = OutGate{nullptr, nullptr, 0}) {
     const int blocks_per_row = (D + seglane::kThreads - 1) / seglane::kThreads;
-    hipLaunchKernelGGL((prefill_seg_lane_kernel<E, kSummary, kRowsOrder>), dim3((unsigned)(nrows * blocks_per_row)),
-                       dim3(seglane::kThreads), 0, stream, x, dl, A, B, C, h0, y, h_final, dsum, sg, D, blocks_per_row);
+    hipLaunchKernelGGL((prefill_seg_lane_kernel<E, kSummary, kRowsOrder, kGate>),
+                       dim3((unsigned)(nrows * blocks_per_row)), dim3(seglane::kThreads), 0, stream, x, dl, A, B, C, h0, y,
+                       h_final, dsum, sg, D, blocks_per_row, og);
 }
 
 }  // namespace jscan

@@ -12,6 +12,7 @@
 // two DPP quad exchanges add (q0+q1)+(q2+q3); every lane of the quad ends with the same sum.
 #pragma once
 
+#include "activation.h"
 #include "scan_update.h"
 
 namespace jscan {
@@ -47,8 +48,9 @@ template <> struct Quad<F32> {
 // With a scaled-identity A (AF), A is a[D]: one decay per (row, channel) serves the quad.  With
 // a complex state the quad is two complex states, (4q, 4q+1) and (4q+2, 4q+3).  With the
 // exponential-trapezoidal rule (kTrap) the previous token's x (xp, rows like x) and B (bp, rows
-// like B) enter as the step's left end point, weighted by 1 - lam (lam, rows like x).
-template <typename E, AForm AF = AForm::Diagonal, bool kTrap = false>
+// like B) enter as the step's left end point, weighted by 1 - lam (lam, rows like x).  With kGate y
+// leaves through the skip and the gate (og; the quad's four lanes read the same z).
+template <typename E, AForm AF = AForm::Diagonal, bool kTrap = false, bool kGate = false>
 __global__ __launch_bounds__(256) void step_kernel(float *__restrict__ h,
                                                    const typename E::store_t *__restrict__ x,
                                                    const typename E::store_t *__restrict__ dl,
@@ -59,7 +61,7 @@ __global__ __launch_bounds__(256) void step_kernel(float *__restrict__ h,
                                                    int blocks_per_rows, int64_t ld_xd, int64_t ld_bc, int64_t ld_y,
                                                    const typename E::store_t *__restrict__ lam,
                                                    const typename E::store_t *__restrict__ xp,
-                                                   const typename E::store_t *__restrict__ bp) {
+                                                   const typename E::store_t *__restrict__ bp, OutGate og) {
     constexpr int NR = step::kRows;
     const int rg = blockIdx.x / blocks_per_rows;   // group of NR batch rows
     const int lane_in_row = (blockIdx.x - rg * blocks_per_rows) * 256 + threadIdx.x;
@@ -72,7 +74,9 @@ __global__ __launch_bounds__(256) void step_kernel(float *__restrict__ h,
     const float a0 = scaled_A(av.x), a1 = scaled_A(av.y), a2 = scaled_A(av.z), a3 = scaled_A(av.w);
     const ComplexA ca0 = complex_A(av.x, av.y), ca1 = complex_A(av.z, av.w);
     float4 hv[NR], bv[NR], cv[NR], bpv[NR];
-    float xv[NR], dv[NR], lv[NR], xpv[NR];
+    float xv[NR], dv[NR], lv[NR], xpv[NR], zv[NR];
+    const bool skipped = kGate && og.skip != nullptr, gated = kGate && og.z != nullptr;
+    const float skip = skipped ? og.skip[d] : 0.0f;
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
         // a missing last row re-reads the row before it and stores nothing
@@ -80,6 +84,7 @@ __global__ __launch_bounds__(256) void step_kernel(float *__restrict__ h,
         hv[j] = load_state(h + ((int64_t)b * D + d) * kDState + q * 4);
         xv[j] = E::load(x + (int64_t)b * ld_xd + d);
         dv[j] = E::load(dl + (int64_t)b * ld_xd + d);
+        zv[j] = gated ? E::load(static_cast<const typename E::store_t *>(og.z) + (int64_t)b * og.ld_z + d) : 0.0f;
         bv[j] = Quad<E>::load(Bt + (int64_t)b * ld_bc + q * 4);
         cv[j] = Quad<E>::load(Ct + (int64_t)b * ld_bc + q * 4);
         if constexpr (kTrap) {
@@ -124,6 +129,7 @@ __global__ __launch_bounds__(256) void step_kernel(float *__restrict__ h,
         // quad_perm [1,0,3,2] then [2,3,0,1]
         p = p + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, p), 0xB1, 0xF, 0xF, true));
         p = p + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, p), 0x4E, 0xF, 0xF, true));
+        if constexpr (kGate) p = gated_output(p, skipped, skip, xv[j], gated, zv[j]);
         if (b < batch) {
             store_state(h + ((int64_t)b * D + d) * kDState + q * 4, hn);
             if (q == 0) E::store(y + (int64_t)b * ld_y + d, p);
