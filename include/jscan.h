@@ -640,6 +640,65 @@ jscan_status jscan_step_gate(float *h, const void *x_t, const void *delta_t, con
                              int64_t ld_bc, int64_t ld_z, int64_t ld_y, jscan_a_form a_form,
                              jscan_dtype dtype, void *stream);
 
+/*
+ * Root-mean-square norm with the residual's addition in front of it, row by row (token by token):
+ *     total = x + residual, rounded to `dtype` (the residual stream as it is kept)
+ *     y = total gain / sqrt(mean_k total^2 + eps)
+ * in fp32 (as (total gain) r with r = 1 / sqrt(...)), rounded once.  So the call on x and residual gives what the call on total
+ * alone gives, bit for bit.  A row that holds a NaN or an infinity, or whose sum of squares overflows fp32, has no
+ * norm; no other row is touched.
+ *   x, residual   M rows of K values in `dtype`, row strides ld_x, ld_residual >= K; residual may be NULL: total is then x
+ *   gain          [K] fp32
+ *   y             M rows out, stride ld_y
+ *   total         M rows out, stride ld_total, or NULL when it is not wanted; goes with a residual.  It may be x or residual
+ *                 itself (the same rows at the same stride)
+ * 1 <= K <= 2^24, 0 <= M <= 2^30, eps >= 0; any K, any stride, pointers aligned to their elements.
+ */
+jscan_status jscan_rms_norm(const void *x, const void *residual, const float *gain, void *y,
+                            void *total, int64_t M, int64_t K, int64_t ld_x, int64_t ld_residual,
+                            int64_t ld_y, int64_t ld_total, float eps, jscan_dtype dtype, void *stream);
+
+/*
+ * The same with y in 8 bits, as jscan_quantize_rows would take it from y before it is rounded: the first input
+ * of jscan_matmul_i8.  q [M][K] int8, 16-byte aligned; scale [M] fp32.  A row without a norm (see above) gets
+ * scale NaN and q = 0.  K a multiple of 16, 16 <= K <= 131056.
+ */
+jscan_status jscan_rms_norm_quantize(const void *x, const void *residual, const float *gain, int8_t *q,
+                                     float *scale, void *total, int64_t M, int64_t K, int64_t ld_x,
+                                     int64_t ld_residual, int64_t ld_total, float eps,
+                                     jscan_dtype dtype, void *stream);
+
+/*
+ * Backward pass of jscan_rms_norm from total.  With r = 1 / sqrt(mean total^2 + eps) and g = dy gain,
+ *     dx = r (g - total r mean_k(g total r)) + dtotal,   dgain = sum over rows of dy total r
+ * dx is the gradient of x and of residual alike.  Sums are fp32, in a fixed order (no atomics).
+ *   dtotal      M rows, the gradient that comes from total's other uses, or NULL for zeros
+ *   dx          M rows out; may be dtotal itself;   dgain [K] fp32 out (zeros with M == 0)
+ *   workspace   jscan_rms_norm_backward_workspace(M, K) bytes, 16-byte aligned, overlapping nothing else.  Contents on
+ *               entry do not matter.  Calls that share it must be ordered on one stream.
+ */
+jscan_status jscan_rms_norm_backward(const void *total, const float *gain, const void *dy,
+                                     const void *dtotal, void *dx, float *dgain, int64_t M, int64_t K,
+                                     int64_t ld_total, int64_t ld_dy, int64_t ld_dtotal, int64_t ld_dx,
+                                     void *workspace, int64_t workspace_bytes, float eps,
+                                     jscan_dtype dtype, void *stream);
+
+/* Workspace bytes of jscan_rms_norm_backward for this shape, or -1 if the shape is invalid.  Host-only. */
+int64_t jscan_rms_norm_backward_workspace(int64_t M, int64_t K);
+
+/*
+ * jscan_matmul_i8 with an epilogue: an activation of the scaled sum with its bias, then a residual,
+ *     out[m][n] = act((sum_k q[m][k] w[n][k]) * q_scale[m] * w_scale[n] + bias[n]) + residual[m][n]
+ * in fp32, rounded once.  activation is any jscan_activation (JSCAN_ERR_FORM otherwise).
+ *   residual   M rows of N values in `dtype`, row stride ld_residual >= N, or NULL; it may be out itself (the same
+ *              rows at the same stride)
+ */
+jscan_status jscan_matmul_i8_epilogue(const int8_t *q, const float *q_scale, const int8_t *w,
+                                      const float *w_scale, const float *bias, const void *residual,
+                                      void *out, int64_t M, int64_t N, int64_t K, int64_t ld_residual,
+                                      int64_t ld_out, jscan_activation activation, jscan_dtype dtype,
+                                      void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *jscan_status_string(jscan_status s);
 

@@ -26,8 +26,12 @@ There is no CPU fallback: without the built library every call raises.
     y_t = gated_step(h, g_t, u_t)                          # its decode token, h in place
     q, q_scale = quantize_rows(x)                          # activations to int8, a scale per token
     out = matmul_i8(q, q_scale, w, w_scale)                # int8 projection, a scale per output channel
+    out = matmul_i8(q, q_scale, w, w_scale, activation="silu", residual=r)   # act(...) + r in its epilogue
     y, h_final = prefill_gate(x, delta, A, B, C, skip, z)  # (scan + skip x) silu(z) in one pass
     y_t = step_gate(h, x_t, delta_t, A, B_t, C_t, skip, z_t)
+    y, total = rms_norm(x, gain, residual)                 # total = x + residual and its norm
+    q, q_scale, total = rms_norm_quantize(x, gain, residual)   # the same into 8 bits, for matmul_i8
+    dx, dgain = rms_norm_backward(total, gain, dy, dtotal) # its gradients
     y, state = causal_conv(x, w, bias, state)              # short causal convolution in front of a scan
     dx, dw, dbias, dstate = causal_conv_backward(x, w, dy, bias, state)   # its gradients
     y_t = causal_conv_step(state, x_t, w, bias)            # its decode token, the state in place
@@ -62,6 +66,10 @@ from ._binding import (  # noqa: F401
     prefill_scalar_a,
     prefill_trapezoid,
     quantize_rows,
+    rms_norm,
+    rms_norm_backward,
+    rms_norm_quantize,
+    rms_norm_workspace_bytes,
     ssm_inputs,
     step,
     step_complex,

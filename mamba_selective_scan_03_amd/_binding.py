@@ -83,6 +83,13 @@ def library():
     lib.jscan_causal_conv_step.argtypes = [vp, vp, fp, fp, vp, i64, i64, i64, i64, i64, i32, i32, vp]
     lib.jscan_causal_conv_backward_workspace.argtypes = [i64, i64, i64, i64]
     lib.jscan_causal_conv_backward_workspace.restype = i64
+    f32 = ctypes.c_float
+    lib.jscan_matmul_i8_epilogue.argtypes = [vp, fp, vp, fp, fp, vp, vp, i64, i64, i64, i64, i64, i32, i32, vp]
+    lib.jscan_rms_norm.argtypes = [vp, vp, fp, vp, vp, i64, i64, i64, i64, i64, i64, f32, i32, vp]
+    lib.jscan_rms_norm_quantize.argtypes = [vp, vp, fp, vp, fp, vp, i64, i64, i64, i64, i64, f32, i32, vp]
+    lib.jscan_rms_norm_backward.argtypes = [vp, fp, vp, vp, vp, fp, i64, i64, i64, i64, i64, i64, vp, i64, f32, i32, vp]
+    lib.jscan_rms_norm_backward_workspace.argtypes = [i64, i64]
+    lib.jscan_rms_norm_backward_workspace.restype = i64
     lib.jscan_prefill_gate.argtypes = [vp, vp, fp, vp, vp, fp, fp, vp, vp, fp, i64, i64, i64, i64, i64, i64, vp, i64, i32,
                                        i32, vp]
     lib.jscan_step_gate.argtypes = [fp, vp, vp, fp, vp, vp, fp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i32, i32, vp]
@@ -93,7 +100,8 @@ def library():
               lib.jscan_prefill_mimo_trapezoid, lib.jscan_step_mimo_trapezoid, lib.jscan_gated_scan,
               lib.jscan_gated_scan_backward, lib.jscan_gated_scan_save, lib.jscan_gated_scan_backward_saved,
               lib.jscan_gated_step, lib.jscan_quantize_rows, lib.jscan_matmul_i8, lib.jscan_causal_conv,
-              lib.jscan_causal_conv_backward, lib.jscan_causal_conv_step, lib.jscan_prefill_gate, lib.jscan_step_gate):
+              lib.jscan_causal_conv_backward, lib.jscan_causal_conv_step, lib.jscan_prefill_gate, lib.jscan_step_gate,
+              lib.jscan_matmul_i8_epilogue, lib.jscan_rms_norm, lib.jscan_rms_norm_quantize, lib.jscan_rms_norm_backward):
         f.restype = i32
     lib.jscan_status_string.argtypes = [i32]
     lib.jscan_status_string.restype = ctypes.c_char_p
@@ -822,6 +830,8 @@ def gated_step(h, g_t, u_t, y_t=None, form="decay"):
 
 
 # ---- int8 projection -------------------------------------------------------------------------
+# jscan_activation values.
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu_tanh": 2}
 
 
 def _row_stride(name, t):
@@ -865,13 +875,18 @@ def quantize_rows(x, q=None, scale=None):
     return q, scale
 
 
-def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloat16):
+def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloat16, activation="none", residual=None):
     """``out = (q @ w.T) * q_scale * w_scale + bias`` from int8 q ``[..., K]`` and w ``[N, K]`` with fp32 scales
     ``[...]`` (a token each) and ``[N]`` (an output channel each) and an optional fp32 bias ``[N]``
     (``jscan_matmul_i8``).  Returns out ``[..., N]`` in out_dtype; a given ``out`` may be a slice of a wider
-    tensor."""
-    if q_scale.requires_grad or w_scale.requires_grad or (bias is not None and bias.requires_grad):
+    tensor.  An ``activation`` ("silu" or "gelu_tanh") and a ``residual`` ``[..., N]`` in out's dtype are applied before the
+    one rounding, ``act(...) + residual`` (``jscan_matmul_i8_epilogue``); ``out`` may be the residual itself."""
+    if q_scale.requires_grad or w_scale.requires_grad or (bias is not None and bias.requires_grad) or \
+            (residual is not None and residual.requires_grad):
         _refuse_grad()
+    code = ACTIVATIONS.get(activation)
+    if code is None:
+        _bad(f"activation must be one of {tuple(ACTIVATIONS)}")
     if not q.is_cuda or q.dtype != torch.int8 or q.dim() < 1 or not q.is_contiguous():
         _bad("q must be a contiguous int8 CUDA tensor")
     dev, K, lead = q.device, q.shape[-1], q.shape[:-1]
@@ -891,6 +906,15 @@ def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
             _bad("out must be bfloat16 or float32")
         _check_like("out", out, (*lead, N), out.dtype, dev)
         ld_out = _row_stride("out", out)
+    if code or residual is not None:
+        ld_residual = N
+        if residual is not None:
+            _check_like("residual", residual, out.shape, out.dtype, dev)
+            ld_residual = _row_stride("residual", residual)
+        _launch("jscan_matmul_i8_epilogue", dev, q.data_ptr(), q_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                _addr(bias), _addr(residual), out.data_ptr(), lead.numel(), N, K, ld_residual, ld_out, code,
+                _DTYPES[out.dtype])
+        return out
     _launch("jscan_matmul_i8", dev, q.data_ptr(), q_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
             _addr(bias), out.data_ptr(), lead.numel(), N, K, ld_out, _DTYPES[out.dtype])
     return out
@@ -980,8 +1004,6 @@ def step_gate(h, x_t, delta_t, A, B_t, C_t, skip=None, z_t=None, form="diagonal"
 
 
 # ---- short causal convolution ----------------------------------------------------------------
-# jscan_activation values.
-ACTIVATIONS = {"none": 0, "silu": 1, "gelu_tanh": 2}
 
 
 def _conv_activation(name):
@@ -1119,3 +1141,110 @@ def causal_conv_step(state, x_t, w, bias=None, activation="silu", y_t=None):
     _launch("jscan_causal_conv_step", dev, state.data_ptr(), x_t.data_ptr(), w.data_ptr(), _addr(bias), y_t.data_ptr(), batch,
             D, past + 1, ld_x, ld_y, code, _DTYPES[dtype])
     return y_t
+
+
+# ---- norm ------------------------------------------------------------------------------------
+
+
+def _check_norm(x, gain, name="x"):
+    """The width and the leading shape of x."""
+    if not x.is_cuda or x.dtype not in _DTYPES:
+        _bad(f"{name} must be a bfloat16 or float32 CUDA tensor")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        _bad(f"{name} must have a last dimension")
+    K, lead = x.shape[-1], x.shape[:-1]
+    _check_flat("gain", gain, (K,), _F32, x.device)
+    return K, lead
+
+
+def _norm_rows(name, t, like):
+    """The row stride of a tensor that has x's shape, dtype and device."""
+    if t is not like:
+        _check_like(name, t, like.shape, like.dtype, like.device)
+    return _row_stride(name, t)
+
+
+def _norm_total(x, residual, total):
+    """total's tensor and the row strides of residual and total."""
+    if residual is None:
+        if total is not None:
+            _bad("total goes with a residual (without one it is x)")
+        return None, 0, 0
+    ld_residual = _norm_rows("residual", residual, x)
+    if total is None:
+        return torch.empty(*x.shape, dtype=x.dtype, device=x.device), ld_residual, x.shape[-1]
+    return total, ld_residual, _norm_rows("total", total, x)
+
+
+def rms_norm(x, gain, residual=None, eps=1e-6, y=None, total=None):
+    """Root-mean-square norm with the residual's addition in front of it (``jscan_rms_norm``): ``total = x + residual``
+    (rounded to x's dtype), ``y = total * gain / sqrt(mean(total ** 2) + eps)`` over the last dimension.  x and residual
+    ``[..., K]`` (bf16 or fp32; slices of wider tensors too), gain ``[K]`` fp32.  Returns ``(y, total)``; without a
+    residual ``total`` is x.  A given ``total`` may be x or residual itself.  Autograd does not record the call
+    (:func:`rms_norm_backward` has its gradients)."""
+    if x.requires_grad or gain.requires_grad or (residual is not None and residual.requires_grad):
+        _refuse_grad()
+    K, lead = _check_norm(x, gain)
+    ld_x = _row_stride("x", x)
+    total, ld_residual, ld_total = _norm_total(x, residual, total)
+    if y is None:
+        y, ld_y = torch.empty(*x.shape, dtype=x.dtype, device=x.device), K
+    else:
+        ld_y = _norm_rows("y", y, x)
+    _launch("jscan_rms_norm", x.device, x.data_ptr(), _addr(residual), gain.data_ptr(), y.data_ptr(), _addr(total),
+            lead.numel(), K, ld_x, ld_residual, ld_y, ld_total, eps, _DTYPES[x.dtype])
+    return y, x if total is None else total
+
+
+def rms_norm_quantize(x, gain, residual=None, eps=1e-6, q=None, scale=None, total=None):
+    """:func:`rms_norm` with its output in 8 bits (``jscan_rms_norm_quantize``): returns ``(q [..., K] int8, scale [...]
+    fp32, total)``, q and scale the first inputs of :func:`matmul_i8`.  K a multiple of 16."""
+    if x.requires_grad or gain.requires_grad or (residual is not None and residual.requires_grad):
+        _refuse_grad()
+    K, lead = _check_norm(x, gain)
+    dev = x.device
+    ld_x = _row_stride("x", x)
+    total, ld_residual, ld_total = _norm_total(x, residual, total)
+    if q is None:
+        q = torch.empty(*x.shape, dtype=_I8, device=dev)
+    else:
+        _check_flat("q", q, x.shape, _I8, dev)
+    if scale is None:
+        scale = torch.empty(*(lead or ((),)), dtype=_F32, device=dev)   # () is no list of sizes
+    else:
+        _check_flat("scale", scale, lead, _F32, dev)
+    _launch("jscan_rms_norm_quantize", dev, x.data_ptr(), _addr(residual), gain.data_ptr(), q.data_ptr(), scale.data_ptr(),
+            _addr(total), lead.numel(), K, ld_x, ld_residual, ld_total, eps, _DTYPES[x.dtype])
+    return q, scale, x if total is None else total
+
+
+def rms_norm_workspace_bytes(M: int, K: int) -> int:
+    """Bytes of workspace ``rms_norm_backward`` of M rows of K values needs."""
+    n = library().jscan_rms_norm_backward_workspace(M, K)
+    if n < 0:
+        raise ValueError(f"invalid shape: M={M} K={K}")
+    return n
+
+
+def rms_norm_backward(total, gain, dy, dtotal=None, eps=1e-6, dx=None, dgain=None, workspace=None):
+    """Gradients of :func:`rms_norm` (``jscan_rms_norm_backward``) from its ``total`` (x where there was no residual): dy
+    the gradient of y, dtotal that of total's other uses (None: zeros).  Returns ``(dx, dgain)``: dx the gradient of
+    x and of residual alike, in their dtype; dgain ``[K]`` fp32.  A given ``dx`` may be dtotal itself."""
+    if any(t is not None and t.requires_grad for t in (total, gain, dy, dtotal)):
+        _refuse_grad()
+    K, lead = _check_norm(total, gain, "total")
+    dev, M = total.device, lead.numel()
+    ld_total, ld_dy = _row_stride("total", total), _norm_rows("dy", dy, total)
+    ld_dtotal = 0 if dtotal is None else _norm_rows("dtotal", dtotal, total)
+    if dx is None:
+        dx, ld_dx = torch.empty(*total.shape, dtype=total.dtype, device=dev), K
+    else:
+        ld_dx = _norm_rows("dx", dx, total)
+    if dgain is None:
+        dgain = torch.empty(K, dtype=_F32, device=dev)
+    else:
+        _check_flat("dgain", dgain, (K,), _F32, dev)
+    workspace, ws_bytes = _workspace(workspace, rms_norm_workspace_bytes(M, K), dev)
+    _launch("jscan_rms_norm_backward", dev, total.data_ptr(), gain.data_ptr(), dy.data_ptr(), _addr(dtotal), dx.data_ptr(),
+            dgain.data_ptr(), M, K, ld_total, ld_dy, ld_dtotal, ld_dx, _addr(workspace), ws_bytes, eps, _DTYPES[total.dtype])
+    return dx, dgain

@@ -12,9 +12,9 @@ import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # the library's sources: the selective scan and its producer, the scan with its output gate, the gated recurrence, the
-# int8 projection, the short causal convolution
+# int8 projection, the short causal convolution, the norm
 SRCS = [os.path.join(HERE, "csrc", f) for f in ("jscan.hip", "prefill_gate.hip", "gated_scan.hip",
-                                                 "int8_linear.hip", "causal_conv.hip")]
+                                                 "int8_linear.hip", "causal_conv.hip", "norm.hip")]
 LIB = os.path.join(HERE, "libjscan.so")
 # the microbenchmarks of the chip's ALU, matrix-core, LDS and HBM rates (measurement only)
 MICRO_SRC = os.path.join(HERE, "csrc", "micro.hip")

@@ -5,9 +5,10 @@
 //     out[m][n] = (sum_k q[m][k] w[n][k]) * s[m] * s_w[n] + bias[n]
 //
 // The sum is exact (K <= 131056 keeps 128 * 128 * K below 2^31); it is rounded to fp32 once, and the
-// scales and the bias are applied in fp32 before the one rounding to the output type.
+// scales, the bias, an activation and a residual are applied in fp32 before the one rounding to the output type.
 #pragma once
 
+#include "activation.h"
 #include "mfma_common.h"
 
 namespace jscan {
@@ -157,14 +158,22 @@ __global__ __launch_bounds__(kWaves * 64) void quantize_any_rows_kernel(const ty
     if (threadIdx.x == 0) scale[m] = s;
 }
 
-// Four consecutive results to LDS.
+// Four consecutive results to LDS, or a residual's values from there.
 template <typename E> struct Results;
 template <> struct Results<BF16> {
+    static __device__ __forceinline__ void load4(const uint16_t *p, float (&v)[4]) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
+    }
     static __device__ __forceinline__ void store4(uint16_t *p, const float (&v)[4]) {
         *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
 };
 template <> struct Results<F32> {
+    static __device__ __forceinline__ void load4(const float *p, float (&v)[4]) {
+        const float4 w = *reinterpret_cast<const float4 *>(p);
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+    }
     static __device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
         *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
     }
@@ -212,6 +221,52 @@ __device__ __forceinline__ void store_rows(T *out, const int8_t *lds, int l, int
         }
     }
 }
+
+// What the product adds to its results: an activation of the scaled sum with its bias, then a residual of the
+// output's type, rows ld elements apart (NULL: none).
+struct Epilogue {
+    Act act;
+    const void *residual;
+    int64_t ld;
+};
+
+// The same 16 rows of the residual on their way to LDS, 16 bytes a lane at a time from any address, through
+// registers: the next rows' are loaded while one set of rows is computed.
+template <typename E, int kCols, int kRow> struct ResidualRows {
+    using T = typename E::store_t;
+    typedef uint32_t piece __attribute__((ext_vector_type(4), aligned(2)));   // any element
+    static constexpr int kPer = (int)(16 / sizeof(T)), kPieces = kCols / kPer, kLane = (16 * kPieces + 63) / 64;
+    piece w[kLane];
+    __device__ __forceinline__ void load(const Epilogue &e, int l, int64_t m0, int64_t n0, int64_t M, int64_t N) {
+#pragma unroll
+        for (int j = 0; j < kLane; ++j) {
+            const int c = l + 64 * j;
+            const int64_t m = m0 + c / kPieces, n = n0 + c % kPieces * kPer;
+            w[j] = piece{0, 0, 0, 0};
+            if ((16 * kPieces % 64 != 0 && c >= 16 * kPieces) || m >= M || n >= N) continue;
+            const T *src = static_cast<const T *>(e.residual) + m * e.ld + n;
+            if (n + kPer <= N) {
+                w[j] = *reinterpret_cast<const piece *>(src);
+            } else {   // the row ends inside the piece
+                uint32_t part[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (n + i < N) part[i * sizeof(T) / 4] |= (uint32_t)(uint64_t)as_bits(src[i]) << (8 * (i * sizeof(T) % 4));
+                w[j] = piece{part[0], part[1], part[2], part[3]};
+            }
+        }
+    }
+    static __device__ __forceinline__ uint32_t as_bits(uint16_t v) { return v; }
+    static __device__ __forceinline__ uint32_t as_bits(float v) { return __float_as_uint(v); }
+    __device__ __forceinline__ void to_lds(int8_t *lds, int l) const {
+#pragma unroll
+        for (int j = 0; j < kLane; ++j) {
+            const int c = l + 64 * j;
+            if (16 * kPieces % 64 != 0 && c >= 16 * kPieces) break;
+            *reinterpret_cast<u32x4_t *>(lds + c / kPieces * kRow + c % kPieces * 16) = u32x4_t{w[j].x, w[j].y, w[j].z, w[j].w};
+        }
+    }
+};
 
 // ---- the product --------------------------------------------------------------------------------
 // w is the row operand and q the column operand, so a lane's four sums of a 16 x 16 tile are four columns n of one
@@ -264,12 +319,12 @@ constexpr int waves_per_simd(int waves, int lds_bytes) {
     return n < 1 ? 1 : n > 8 ? 8 : n;
 }
 
-template <typename E, int BM, int BN, int WR, int WC, int KG, int kBufs>
+template <typename E, int BM, int BN, int WR, int WC, int KG, int kBufs, bool kEpilogue>
 __global__ __launch_bounds__(KG * WR * WC * 64,
                              waves_per_simd(KG * WR * WC, KG * kBufs * (BM + BN) * 128)) void matmul_i8_tiled_kernel(
     const int8_t *__restrict__ q, const float *__restrict__ sq, const int8_t *__restrict__ w,
     const float *__restrict__ sw, const float *__restrict__ bias, typename E::store_t *__restrict__ out, int64_t M,
-    int64_t N, int64_t K, int64_t ld_out, int m_tiles, int n_tiles, int wide) {
+    int64_t N, int64_t K, int64_t ld_out, int m_tiles, int n_tiles, int wide, Epilogue ep) {
     using namespace tiled;
     constexpr int MT = BM / WR / 16, NT = BN / WC / 16, kWaves = WR * WC;
     // DMA instructions of a stage (8 rows each), dealt out to the waves in turn
@@ -402,16 +457,33 @@ __global__ __launch_bounds__(KG * WR * WC * 64,
     int8_t *mine = &stages_of[0][0][0] + wave * 16 * kRow;
     const int64_t nw = n0 + wc * kCols;
     const Columns<4 * NT> col(sw, bias, min(nw + g4 * 4 * NT, N - 1), N);
+    ResidualRows<E, kCols, kRow> rest;
+    const bool adds = kEpilogue && ep.residual != nullptr;
+    if (adds) rest.load(ep, l, m0 + wr * 16 * MT, nw, M, N);
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
         const int64_t mu = m0 + wr * 16 * MT + 16 * u;
         const float s = sq[min(mu + r16, M - 1)];
+        if (adds) {
+            rest.to_lds(mine, l);
+            if (u + 1 < MT) rest.load(ep, l, mu + 16, nw, M, N);
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = col(acc[t][u][i], s, 4 * t + i);
-            Results<E>::store4(reinterpret_cast<T *>(mine + r16 * kRow) + g4 * 4 * NT + 4 * t, v);
+            T *place = reinterpret_cast<T *>(mine + r16 * kRow) + g4 * 4 * NT + 4 * t;
+            if constexpr (kEpilogue) {
+                float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (adds) Results<E>::load4(place, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = activate(v[i], ep.act) + r[i];
+            }
+            Results<E>::store4(place, v);
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();

@@ -91,32 +91,72 @@ struct MatmulArgs {
     void *out;
     int64_t M, N, K, ld_out;
     hipStream_t stream;
+    jscan::Epilogue epilogue;
 };
 
-template <typename E, int BM, int BN, int WR, int WC, int KG, int kBufs> void launch_tiled(const MatmulArgs &a) {
+template <typename E, bool kEpilogue, int BM, int BN, int WR, int WC, int KG, int kBufs>
+void launch_tiled(const MatmulArgs &a) {
     using T = typename E::store_t;
     const int m_tiles = (int)((a.M + BM - 1) / BM), n_tiles = (int)((a.N + BN - 1) / BN);
     // the widest store that every output row starts on
     const uint64_t start = reinterpret_cast<uint64_t>(a.out) | (uint64_t)(a.ld_out * (int64_t)sizeof(T));
     const int wide = start % 16 == 0 ? 16 : start % 4 == 0 ? 4 : 2;
-    hipLaunchKernelGGL((jscan::matmul_i8_tiled_kernel<E, BM, BN, WR, WC, KG, kBufs>),
+    hipLaunchKernelGGL((jscan::matmul_i8_tiled_kernel<E, BM, BN, WR, WC, KG, kBufs, kEpilogue>),
                        dim3((unsigned)((int64_t)m_tiles * n_tiles)), dim3(KG * WR * WC * 64), 0, a.stream, a.q, a.sq,
-                       a.w, a.sw, a.bias, static_cast<T *>(a.out), a.M, a.N, a.K, a.ld_out, m_tiles, n_tiles, wide);
+                       a.w, a.sw, a.bias, static_cast<T *>(a.out), a.M, a.N, a.K, a.ld_out, m_tiles, n_tiles, wide,
+                       a.epilogue);
 }
 
-template <typename E> void launch_matmul(const MatmulArgs &a) {
+template <typename E, bool kEpilogue> void launch_matmul(const MatmulArgs &a) {
     switch (choose_tile(a.M, a.N, a.K)) {
-    case 0: launch_tiled<E, 16, 16, 1, 1, 8, 3>(a); break;
-    case 1: launch_tiled<E, 16, 32, 1, 2, 4, 3>(a); break;
-    case 2: launch_tiled<E, 32, 32, 2, 1, 4, 4>(a); break;
-    case 3: launch_tiled<E, 64, 32, 2, 1, 4, 3>(a); break;
-    case 4: launch_tiled<E, 64, 64, 2, 2, 2, 3>(a); break;
-    case 5: launch_tiled<E, 64, 64, 2, 2, 1, 3>(a); break;
-    case 6: launch_tiled<E, 64, 128, 2, 2, 1, 3>(a); break;
-    case 7: launch_tiled<E, 128, 128, 2, 4, 1, 2>(a); break;
-    case 8: launch_tiled<E, 128, 144, 4, 1, 1, 2>(a); break;
-    default: launch_tiled<E, 256, 256, 4, 4, 1, 2>(a); break;
+    case 0: launch_tiled<E, kEpilogue, 16, 16, 1, 1, 8, 3>(a); break;
+    case 1: launch_tiled<E, kEpilogue, 16, 32, 1, 2, 4, 3>(a); break;
+    case 2: launch_tiled<E, kEpilogue, 32, 32, 2, 1, 4, 4>(a); break;
+    case 3: launch_tiled<E, kEpilogue, 64, 32, 2, 1, 4, 3>(a); break;
+    case 4: launch_tiled<E, kEpilogue, 64, 64, 2, 2, 2, 3>(a); break;
+    case 5: launch_tiled<E, kEpilogue, 64, 64, 2, 2, 1, 3>(a); break;
+    case 6: launch_tiled<E, kEpilogue, 64, 128, 2, 2, 1, 3>(a); break;
+    case 7: launch_tiled<E, kEpilogue, 128, 128, 2, 4, 1, 2>(a); break;
+    case 8: launch_tiled<E, kEpilogue, 128, 144, 4, 1, 1, 2>(a); break;
+    default: launch_tiled<E, kEpilogue, 256, 256, 4, 4, 1, 2>(a); break;
     }
+}
+
+// The product, with an activation and a residual where one is given (which may be out itself: a tile is read before
+// it is written, by the wave that writes it).
+jscan_status matmul_impl(const int8_t *q, const float *q_scale, const int8_t *w, const float *w_scale, const float *bias,
+                         const void *residual, void *out, int64_t M, int64_t N, int64_t K, int64_t ld_residual,
+                         int64_t ld_out, jscan_activation activation, jscan_dtype dtype, void *stream) {
+    if (dtype != JSCAN_F32 && dtype != JSCAN_BF16) return JSCAN_ERR_DTYPE;
+    if (!dims_ok(M, K) || K == 0 || N < 0 || N > (1 << 24))
+        return JSCAN_ERR_SHAPE;
+    if (M == 0 || N == 0) return JSCAN_OK;
+    if (choose_tile(M, N, K) < 0) return JSCAN_ERR_SHAPE;
+    if (!ld_ok(ld_out, M, N) || (residual && !ld_ok(ld_residual, M, N))) return JSCAN_ERR_SHAPE;
+    if (!q || !q_scale || !w || !w_scale || !out) return JSCAN_ERR_NULL;
+    const int64_t es = elem_bytes(dtype);
+    if (!aligned16(q) || !aligned16(w) || !aligned(out, es) || !aligned(q_scale, 4) || !aligned(w_scale, 4) ||
+        !aligned(bias, 4) || !aligned(residual, es))
+        return JSCAN_ERR_ALIGN;
+    const bool same = residual == out && (ld_residual == ld_out || M == 1);
+    const Span so = span(Rows{out, M, N * es, ld_out * es});
+    const Span in[] = {span(q, M * K), span(q_scale, M * 4), span(w, N * K), span(w_scale, N * 4),
+                       span(bias, bias ? N * 4 : 0)};
+    for (const Span &i : in)
+        if (overlaps(so, i)) return JSCAN_ERR_ALIAS;
+    if (residual && !same && overlaps(Rows{out, M, N * es, ld_out * es}, Rows{residual, M, N * es, ld_residual * es}))
+        return JSCAN_ERR_ALIAS;
+    const jscan::Act act = activation == JSCAN_ACT_SILU        ? jscan::Act::Silu
+                           : activation == JSCAN_ACT_GELU_TANH ? jscan::Act::GeluTanh
+                                                               : jscan::Act::None;
+    const MatmulArgs a{q, q_scale, w, w_scale, bias, out, M, N, K, ld_out, static_cast<hipStream_t>(stream),
+                       jscan::Epilogue{act, residual, ld_residual}};
+    const bool plain = activation == JSCAN_ACT_NONE && !residual;
+    if (dtype == JSCAN_BF16 && plain) launch_matmul<jscan::BF16, false>(a);
+    else if (dtype == JSCAN_BF16) launch_matmul<jscan::BF16, true>(a);
+    else if (plain) launch_matmul<jscan::F32, false>(a);
+    else launch_matmul<jscan::F32, true>(a);
+    return launch_status();
 }
 
 }  // namespace
@@ -143,26 +183,16 @@ jscan_status jscan_quantize_rows(const void *x, int8_t *q, float *scale, int64_t
 jscan_status jscan_matmul_i8(const int8_t *q, const float *q_scale, const int8_t *w, const float *w_scale,
                              const float *bias, void *out, int64_t M, int64_t N, int64_t K, int64_t ld_out,
                              jscan_dtype dtype, void *stream) {
-    if (dtype != JSCAN_F32 && dtype != JSCAN_BF16) return JSCAN_ERR_DTYPE;
-    if (!dims_ok(M, K) || K == 0 || N < 0 || N > (1 << 24))
-        return JSCAN_ERR_SHAPE;
-    if (M == 0 || N == 0) return JSCAN_OK;
-    if (choose_tile(M, N, K) < 0) return JSCAN_ERR_SHAPE;
-    if (ld_out < N || ld_out > ((int64_t)1 << 58) / M) return JSCAN_ERR_SHAPE;
-    if (!q || !q_scale || !w || !w_scale || !out) return JSCAN_ERR_NULL;
-    const int64_t es = elem_bytes(dtype);
-    if (!aligned16(q) || !aligned16(w) || !aligned(out, es) || !aligned(q_scale, 4) || !aligned(w_scale, 4) ||
-        !aligned(bias, 4))
-        return JSCAN_ERR_ALIGN;
-    const Span so = span(Rows{out, M, N * es, ld_out * es});
-    const Span in[] = {span(q, M * K), span(q_scale, M * 4), span(w, N * K), span(w_scale, N * 4),
-                       span(bias, bias ? N * 4 : 0)};
-    for (const Span &i : in)
-        if (overlaps(so, i)) return JSCAN_ERR_ALIAS;
-    const MatmulArgs a{q, q_scale, w, w_scale, bias, out, M, N, K, ld_out, static_cast<hipStream_t>(stream)};
-    if (dtype == JSCAN_BF16) launch_matmul<jscan::BF16>(a);
-    else launch_matmul<jscan::F32>(a);
-    return launch_status();
+    return matmul_impl(q, q_scale, w, w_scale, bias, nullptr, out, M, N, K, 0, ld_out, JSCAN_ACT_NONE, dtype, stream);
+}
+
+jscan_status jscan_matmul_i8_epilogue(const int8_t *q, const float *q_scale, const int8_t *w, const float *w_scale,
+                                      const float *bias, const void *residual, void *out, int64_t M, int64_t N, int64_t K,
+                                      int64_t ld_residual, int64_t ld_out, jscan_activation activation, jscan_dtype dtype,
+                                      void *stream) {
+    if (activation != JSCAN_ACT_NONE && activation != JSCAN_ACT_SILU && activation != JSCAN_ACT_GELU_TANH)
+        return JSCAN_ERR_FORM;
+    return matmul_impl(q, q_scale, w, w_scale, bias, residual, out, M, N, K, ld_residual, ld_out, activation, dtype, stream);
 }
 
 }  // extern "C"

@@ -118,3 +118,53 @@ def conv_backward(x, w, dy, bias=None, state=None, dstate_out=None, lengths=None
         dx[i, n[i]:] = 0
         e_dx[i, n[i]:] = 0
     return dict(dx=dx, dw=dw, dbias=db, dstate=dstate), dict(dx=e_dx, dw=e_dw, dbias=e_db, dstate=e_ds)
+
+
+def rms_norm(total, gain, eps):
+    """(y, bound of |y - exact| before y's rounding) of rows of total.  The sum of squares is of one sign, so its
+    relative error is that of its additions: at most 32 in a thread, a dozen joining them (up to 2^14 for rows that
+    are taken element by element, K / 64 in a thread); the root halves it, the reciprocal root is good to one unit
+    (2^-23), and two products round."""
+    t, g = _f64(total), _f64(gain)
+    K = t.shape[-1]
+    r = 1.0 / np.sqrt((t ** 2).mean(-1, keepdims=True) + eps)
+    y = t * g * r
+    adds = min(K, 64 + K // 64)
+    return y, np.abs(y) * ((adds + 4) / 2 + 2 + 2) * U + 1e-37
+
+
+def rms_norm_backward(total, gain, dy, dtotal, eps):
+    """(dx, dgain, bounds of their errors before dx's rounding)."""
+    t, g, dy = _f64(total), _f64(gain), _f64(dy)
+    K, rows = t.shape[-1], int(np.prod(t.shape[:-1]))
+    r = 1.0 / np.sqrt((t ** 2).mean(-1, keepdims=True) + eps)
+    n, v = t * r, dy * g
+    mean = (v * n).mean(-1, keepdims=True)
+    dx = r * (v - n * mean)
+    e_r = ((min(K, 64 + K // 64) + 4) / 2 + 2) * U   # relative, as above
+    size = np.abs(v * n).mean(-1, keepdims=True)
+    e_mean = size * ((min(K, 64 + K // 64) + 4) * U + 2 * e_r)
+    part = np.abs(v) + np.abs(n * mean)
+    e_dx = r * (part * (e_r + 4 * U) + np.abs(n) * e_mean)
+    if dtotal is not None:
+        add = _f64(dtotal)
+        dx = dx + add
+        e_dx = e_dx + U * (np.abs(add) + np.abs(dx))
+    terms = np.abs(dy * n).reshape(rows, K)
+    dgain = (dy * n).reshape(rows, K).sum(0)
+    e_gain = terms.sum(0) * ((e_r + 2 * U) + min(rows, 600 + rows) * U)
+    return dx, dgain, e_dx, e_gain
+
+
+def matmul_i8(q, q_scale, w, w_scale, bias=None, act="none", residual=None):
+    """(out, bound of |out - exact| before the output's rounding): the integer sum is exact and rounds once, two
+    scale products and the bias sum round once each, the residual's sum once."""
+    s = (np.asarray(q, np.float64) @ np.asarray(w, np.float64).T) * _f64(q_scale)[..., None] * _f64(w_scale)
+    v = s if bias is None else s + _f64(bias)
+    e = 3 * U * np.abs(s) + U * np.abs(v)
+    out = activate(v, act)
+    e = activate_error(v, e, act)
+    if residual is not None:
+        out = out + _f64(residual)
+        e = e + U * (np.abs(out) + e)
+    return out, e
