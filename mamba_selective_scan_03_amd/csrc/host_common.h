@@ -11,7 +11,7 @@ namespace jscan {
 namespace host {
 
 // One variable for the whole library, not exported.
-extern thread_local int g_last_hip_error __attribute__((visibility("hidden")));
+extern __thread int g_last_hip_error __attribute__((visibility("hidden")));
 
 struct Span {
     uintptr_t lo = 0, hi = 0;  // [lo, hi), empty when lo == hi

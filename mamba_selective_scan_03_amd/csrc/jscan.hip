@@ -18,7 +18,7 @@
 #include "mimo_kernels.h"
 #include "prefill_mimo_rows_kernel.h"
 
-thread_local int jscan::host::g_last_hip_error = 0;
+__thread int jscan::host::g_last_hip_error = 0;
 using namespace jscan::host;
 
 namespace {
