@@ -31,8 +31,19 @@ jscan::conv::Split split_for(int64_t batch, int64_t L, int64_t D, int n, int64_t
     return {log, (int)strips, (int)segs(), run};
 }
 
-constexpr int64_t kForwardWaves = 4096, kForwardRun = 64;
-constexpr int64_t kBackwardWaves = 2048, kBackwardRun = 128;
+// Tensors beyond the last-level cache go by with the non-temporal hint (us, 8 x 4096 x 8192 bf16, without and with it:
+// forward 204 and 192, backward 329 and 298; from the cache the loads lose by it: 24 x 1000 x 500 11.6 and 14.8).
+constexpr int64_t kStreamBytes = (int64_t)256 << 20;
+bool streams(int64_t batch, int64_t L, int64_t D, int64_t es, int tensors, int n) {
+    return n > 1 && batch * L * D * es * tensors > kStreamBytes;
+}
+
+// Forward: runs of 64 tokens, 32 where the tensors stream (8 x 4096 x 8192: 204 us for 212; 1 x 32768 x 2048: 60 for 56).
+// Backward: a run computes W - 1 more tokens than it has, and its shares of the taps' gradients are written once (us
+// for 128 tokens, 256, 64: 8 x 4096 x 8192 329, 352, 378; with 1024 waves and with 2048: 24 x 1000 x 500 27 and 30,
+// 2 x 200 x 8192 14.3 and 15.4).
+constexpr int64_t kForwardWaves = 4096, kForwardRun = 64, kForwardStreamRun = 32;
+constexpr int64_t kBackwardWaves = 1024, kBackwardRun = 128;
 
 jscan::conv::Split backward_split(int64_t batch, int64_t L, int64_t D) {
     return split_for(batch, L, D, channels_of(D), kBackwardWaves, kBackwardRun);
@@ -54,6 +65,7 @@ struct ConvArgs {
     float *partial;
     int64_t batch, L, D;
     jscan::conv::Split split;
+    bool streams;
     hipStream_t stream;
 };
 
@@ -76,20 +88,26 @@ template <typename F> void by_sequences(const ConvArgs &a, F launch) {
     }
 }
 
-template <typename E, int N, int W, Act A> void launch_forward(const ConvArgs &a) {
+template <typename E, int N, int W, Act A, bool kNt> void launch_forward(const ConvArgs &a) {
     using T = typename E::store_t;
+    if constexpr (N > 1 && !kNt) {
+        if (a.streams) return launch_forward<E, N, W, A, true>(a);
+    }
     by_sequences(a, [&](int64_t b, dim3 grid) {
-        hipLaunchKernelGGL((jscan::causal_conv_kernel<E, N, W, A>), grid, dim3(jscan::conv::kThreads), 0, a.stream,
+        hipLaunchKernelGGL((jscan::causal_conv_kernel<E, N, W, A, kNt>), grid, dim3(jscan::conv::kThreads), 0, a.stream,
                            in_rows<T>(a.x, b * a.L), from<const T>(a.state, b * (W - 1) * a.D), a.w, a.bias,
                            from<const int32_t>(a.lengths, b), out_rows<T>(a.y, b * a.L),
                            from<T>(a.state_out, b * (W - 1) * a.D), a.L, (int)a.D, a.split);
     });
 }
 
-template <typename E, int N, int W, Act A> void launch_backward(const ConvArgs &a) {
+template <typename E, int N, int W, Act A, bool kNt> void launch_backward(const ConvArgs &a) {
     using T = typename E::store_t;
+    if constexpr (N > 1 && !kNt) {
+        if (a.streams) return launch_backward<E, N, W, A, true>(a);
+    }
     by_sequences(a, [&](int64_t b, dim3 grid) {
-        hipLaunchKernelGGL((jscan::causal_conv_backward_kernel<E, N, W, A>), grid, dim3(jscan::conv::kThreads), 0,
+        hipLaunchKernelGGL((jscan::causal_conv_backward_kernel<E, N, W, A, kNt>), grid, dim3(jscan::conv::kThreads), 0,
                            a.stream, in_rows<T>(a.x, b * a.L), from<const T>(a.state, b * (W - 1) * a.D), a.w, a.bias,
                            from<const int32_t>(a.lengths, b), in_rows<T>(a.dy, b * a.L),
                            from<const T>(a.dstate_out, b * (W - 1) * a.D), out_rows<T>(a.dx, b * a.L),
@@ -98,17 +116,28 @@ template <typename E, int N, int W, Act A> void launch_backward(const ConvArgs &
     });
 }
 
-template <typename E, int N, int W, Act A>
+// Sequences a thread takes in a step: four where that leaves a wave for every SIMD (their taps are 80 bytes a thread, against 8
+// of each token).
+constexpr int64_t kStepRows = 4, kStepWaves = 1024;
+
+template <typename E, int N, int W, Act A, int kRows>
 void launch_step(void *state, const void *x, const float *w, const float *bias, void *y, int64_t batch, int64_t D,
                  int64_t ld_x, int64_t ld_y, hipStream_t stream) {
     using T = typename E::store_t;
-    const int64_t words = D / N, rows = kMostGroups * jscan::conv::kThreads / words;   // of one launch
+    const int64_t words = D / N;
+    if constexpr (kRows == 1) {
+        if (batch * words >= kStepRows * kStepWaves * 64)
+            return launch_step<E, N, W, A, kStepRows>(state, x, w, bias, y, batch, D, ld_x, ld_y, stream);
+    }
+    const int64_t rows = kMostGroups * jscan::conv::kThreads / words * kRows;   // of one launch
     for (int64_t b = 0; b < batch; b += rows) {
         const int64_t count = rows < batch - b ? rows : batch - b;
-        const unsigned grid = (unsigned)((count * words + jscan::conv::kThreads - 1) / jscan::conv::kThreads);
-        hipLaunchKernelGGL((jscan::causal_conv_step_kernel<E, N, W, A>), dim3(grid), dim3(jscan::conv::kThreads), 0,
-                           stream, static_cast<T *>(state) + b * (W - 1) * D, static_cast<const T *>(x) + b * ld_x, w,
-                           bias, static_cast<T *>(y) + b * ld_y, count, (int)D, (int)words, ld_x, ld_y);
+        const int64_t threads = (count + kRows - 1) / kRows * words;
+        hipLaunchKernelGGL((jscan::causal_conv_step_kernel<E, N, W, A, kRows>),
+                           dim3((unsigned)((threads + jscan::conv::kThreads - 1) / jscan::conv::kThreads)),
+                           dim3(jscan::conv::kThreads), 0, stream, static_cast<T *>(state) + b * (W - 1) * D,
+                           static_cast<const T *>(x) + b * ld_x, w, bias, static_cast<T *>(y) + b * ld_y, count, (int)D,
+                           (int)words, ld_x, ld_y);
     }
 }
 
@@ -164,9 +193,10 @@ jscan_status jscan_causal_conv(const void *x, const void *state, const float *w,
     ConvArgs a{};
     a.x = {x, ld_x}, a.y = {y, ld_y}, a.state = state, a.state_out = state_out, a.w = w, a.bias = bias;
     a.lengths = lengths, a.batch = batch, a.L = L, a.D = D, a.stream = static_cast<hipStream_t>(stream);
-    a.split = split_for(batch, L, D, n, kForwardWaves, kForwardRun);
+    a.streams = streams(batch, L, D, es, 2, n);
+    a.split = split_for(batch, L, D, n, kForwardWaves, a.streams ? kForwardStreamRun : kForwardRun);
     dispatch(dtype, n, W, activation, [&](auto e, auto n_c, auto w_c, auto a_c) {
-        launch_forward<decltype(e), decltype(n_c)::value, decltype(w_c)::value, (Act)decltype(a_c)::value>(a);
+        launch_forward<decltype(e), decltype(n_c)::value, decltype(w_c)::value, (Act)decltype(a_c)::value, false>(a);
     });
     return launch_status();
 }
@@ -209,9 +239,10 @@ jscan_status jscan_causal_conv_backward(const void *x, const void *state, const 
     int64_t shares = 0;   // none without a sequence: the gradients of taps and bias are then zeros
     if (batch > 0) {
         a.split = backward_split(batch, L, D);
+        a.streams = streams(batch, L, D, es, 3, channels_of(D));
         shares = batch * a.split.segs;
         dispatch(dtype, channels_of(D), W, activation, [&](auto e, auto n_c, auto w_c, auto a_c) {
-            launch_backward<decltype(e), decltype(n_c)::value, decltype(w_c)::value, (Act)decltype(a_c)::value>(a);
+            launch_backward<decltype(e), decltype(n_c)::value, decltype(w_c)::value, (Act)decltype(a_c)::value, false>(a);
         });
         if (launch_status() != JSCAN_OK) return JSCAN_ERR_HIP;
     }
@@ -239,7 +270,7 @@ jscan_status jscan_causal_conv_step(void *state, const void *x_t, const float *w
     if (any_overlap(out, in)) return JSCAN_ERR_ALIAS;
     // the state is updated in place, so no two words may share a channel
     dispatch(dtype, D % 4 == 0 ? 4 : 1, W, activation, [&](auto e, auto n_c, auto w_c, auto a_c) {
-        launch_step<decltype(e), decltype(n_c)::value, decltype(w_c)::value, (Act)decltype(a_c)::value>(
+        launch_step<decltype(e), decltype(n_c)::value, decltype(w_c)::value, (Act)decltype(a_c)::value, 1>(
             state, x_t, w, bias, y_t, batch, D, ld_x, ld_y, static_cast<hipStream_t>(stream));
     });
     return launch_status();

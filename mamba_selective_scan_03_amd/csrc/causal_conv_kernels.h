@@ -22,6 +22,12 @@ namespace conv {
 
 constexpr int kThreads = 256;
 
+typedef float f32_pair __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16_pair __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {   // one conversion instruction for both
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32_pair{lo, hi}), bf16_pair));
+}
+
 // N channels of one token in memory: aligned to their element alone, so that any row stride takes the same
 // loads (the hardware takes any address).
 template <typename E, int N> struct Word;
@@ -31,17 +37,7 @@ template <> struct Word<BF16, 4> {
         f[0] = bf16_lo(w.x), f[1] = bf16_hi(w.x), f[2] = bf16_lo(w.y), f[3] = bf16_hi(w.y);
     }
     static __device__ __forceinline__ raw pack(const float (&f)[4]) {
-        return raw{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
-    }
-};
-template <> struct Word<BF16, 8> {
-    typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2)));
-    static __device__ __forceinline__ void unpack(raw w, float (&f)[8]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(w[i]), f[2 * i + 1] = bf16_hi(w[i]);
-    }
-    static __device__ __forceinline__ raw pack(const float (&f)[8]) {
-        return raw{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+        return raw{pack2(f[0], f[1]), pack2(f[2], f[3])};
     }
 };
 template <> struct Word<BF16, 1> {
@@ -62,12 +58,16 @@ template <> struct Word<F32, 1> {
     static __device__ __forceinline__ raw pack(const float (&f)[1]) { return f[0]; }
 };
 
-template <typename E, int N> __device__ __forceinline__ typename Word<E, N>::raw load(const typename E::store_t *p) {
+// kNt: with the non-temporal hint, for tensors that go by.
+template <typename E, int N, bool kNt = false>
+__device__ __forceinline__ typename Word<E, N>::raw load(const typename E::store_t *p) {
+    if constexpr (kNt) return __builtin_nontemporal_load(reinterpret_cast<const typename Word<E, N>::raw *>(p));
     return *reinterpret_cast<const typename Word<E, N>::raw *>(p);
 }
-template <typename E, int N>
+template <typename E, int N, bool kNt = false>
 __device__ __forceinline__ void store(typename E::store_t *p, typename Word<E, N>::raw v) {
-    *reinterpret_cast<typename Word<E, N>::raw *>(p) = v;
+    if constexpr (kNt) __builtin_nontemporal_store(v, reinterpret_cast<typename Word<E, N>::raw *>(p));
+    else *reinterpret_cast<typename Word<E, N>::raw *>(p) = v;
 }
 
 // How a call is dealt out: `lanes` (a power of two) lanes side by side take N channels each, the work-group's
@@ -83,10 +83,10 @@ template <int N> struct Place {
     int64_t b, t0;
     int strip, seg, row, col, c0;   // strip, work-group of the sequence, row of lanes, lane, first channel
     bool active;
-    __device__ __forceinline__ Place(const Split &sp, int D) {
-        // consecutive work-groups to one XCD (ids 8 apart): the tokens before a run are in its L2
+    // near: consecutive work-groups to one XCD (ids 8 apart), so that the tokens around a run are in its L2.
+    __device__ __forceinline__ Place(const Split &sp, int D, bool near) {
         const uint32_t per = gridDim.x / 8, id = blockIdx.x;
-        const uint32_t v = id < per * 8 ? (id % 8) * per + id / 8 : id;
+        const uint32_t v = near && id < per * 8 ? (id % 8) * per + id / 8 : id;
         const uint32_t rest = v / sp.strips;
         strip = v % sp.strips;
         seg = rest % sp.segs;
@@ -129,16 +129,17 @@ __device__ __forceinline__ void load_window(typename Word<E, N>::raw (&win)[W - 
 
 }  // namespace conv
 
-constexpr int kConvStage = 8;   // tokens that are on their way while as many are computed
+// Tokens that are on their way while as many are computed.
+constexpr int kForwardStage = 8, kBackwardStage = 4;
 
-template <typename E, int N, int W, Act A>
+template <typename E, int N, int W, Act A, bool kNt>
 __global__ __launch_bounds__(conv::kThreads) void causal_conv_kernel(
     TokenRows<const typename E::store_t> x, const typename E::store_t *state, const float *__restrict__ w,
     const float *__restrict__ bias, const int32_t *__restrict__ lengths, TokenRows<typename E::store_t> y,
     typename E::store_t *state_out, int64_t L, int D, conv::Split sp) {
     using raw = typename conv::Word<E, N>::raw;
-    constexpr int U = kConvStage;
-    const conv::Place<N> at(sp, D);
+    constexpr int U = kForwardStage;
+    const conv::Place<N> at(sp, D, true);
     if (!at.active || (at.t0 >= L && at.t0 > 0)) return;   // an empty sequence still hands its state on
     const int64_t n = tokens_of(lengths, at.b, L), t0 = at.t0;
     raw win[W - 1];
@@ -169,35 +170,46 @@ __global__ __launch_bounds__(conv::kThreads) void causal_conv_kernel(
         auto fetch = [&](int64_t i0) {   // tokens behind the run's end read its last one
             if (i0 + U <= count) {
 #pragma unroll
-                for (int i = 0; i < U; ++i) next[i] = conv::load<E, N>(xp + (i0 + i) * x.ld);
+                for (int i = 0; i < U; ++i) next[i] = conv::load<E, N, kNt>(xp + i0 * x.ld + i * x.ld);
             } else {
 #pragma unroll
-                for (int i = 0; i < U; ++i) next[i] = conv::load<E, N>(xp + min(i0 + i, count - 1) * x.ld);
+                for (int i = 0; i < U; ++i) next[i] = conv::load<E, N, kNt>(xp + min(i0 + i, count - 1) * x.ld);
             }
         };
-        fetch(0);
-        for (int64_t i0 = 0; i0 < count; i0 += U) {
+        auto block = [&](auto ends_c, int64_t i0) {   // U tokens; fewer at the run's end
+            constexpr bool ends = decltype(ends_c)::value;
             raw cur[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) cur[i] = next[i];
-            if (i0 + U < count) fetch(i0 + U);
+            if (!ends && i0 + U < count) fetch(i0 + U);
+            float ew[W - 1 + U][N];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int v = 0; v < N; ++v) ew[j][v] = e[j][v];
+            typename E::store_t *dst = yp + i0 * y.ld;
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                float f[N], o[N];
-                conv::Word<E, N>::unpack(cur[i], f);
+                float o[N];
+                conv::Word<E, N>::unpack(cur[i], ew[W - 1 + i]);
 #pragma unroll
                 for (int v = 0; v < N; ++v) {
                     float s = taps.bias[v];
 #pragma unroll
-                    for (int k = 0; k < W - 1; ++k) s = __builtin_fmaf(taps.w[k][v], e[k][v], s);
-                    o[v] = activate<A>(__builtin_fmaf(taps.w[W - 1][v], f[v], s));
-#pragma unroll
-                    for (int k = 0; k < W - 2; ++k) e[k][v] = e[k + 1][v];
-                    e[W - 2][v] = f[v];
+                    for (int k = 0; k < W; ++k) s = __builtin_fmaf(taps.w[k][v], ew[i + k][v], s);
+                    o[v] = activate<A>(s);
                 }
-                if (i0 + i < count) conv::store<E, N>(yp + (i0 + i) * y.ld, conv::Word<E, N>::pack(o));
+                if (!ends || i0 + i < count) conv::store<E, N, kNt>(dst + i * y.ld, conv::Word<E, N>::pack(o));
             }
-        }
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int v = 0; v < N; ++v) e[j][v] = ew[U + j][v];
+        };
+        fetch(0);
+        int64_t i0 = 0;
+        for (; i0 + U <= count; i0 += U) block(std::false_type{}, i0);
+        if (i0 < count) block(std::true_type{}, i0);
     }
     for (int64_t t = max(t0, n); t < end; ++t) conv::store<E, N>(yp + (t - t0) * y.ld, raw{});
 }
@@ -206,16 +218,16 @@ __global__ __launch_bounds__(conv::kThreads) void causal_conv_kernel(
 // t - (W - 1); W - 1 tokens behind the run complete its own.  Gradients of taps and bias are summed over the
 // run in registers, over the work-group's runs in LDS and over work-groups by conv_sum_kernel: fixed
 // orders, so results repeat bit for bit.  partial[sequence and work-group][W + 1][D].
-template <typename E, int N, int W, Act A>
+template <typename E, int N, int W, Act A, bool kNt>
 __global__ __launch_bounds__(conv::kThreads) void causal_conv_backward_kernel(
     TokenRows<const typename E::store_t> x, const typename E::store_t *__restrict__ state, const float *__restrict__ w,
     const float *__restrict__ bias, const int32_t *__restrict__ lengths, TokenRows<const typename E::store_t> dy,
     const typename E::store_t *__restrict__ dstate_out, TokenRows<typename E::store_t> dx,
     typename E::store_t *__restrict__ dstate, float *__restrict__ partial, int64_t L, int D, conv::Split sp) {
     using raw = typename conv::Word<E, N>::raw;
-    constexpr int U = kConvStage;
+    constexpr int U = kBackwardStage;
     __shared__ float sums[(W + 1) * N * conv::kThreads];
-    const conv::Place<N> at(sp, D);
+    const conv::Place<N> at(sp, D, !kNt);
     float dw[W + 1][N];   // taps, then bias
 #pragma unroll
     for (int k = 0; k <= W; ++k)
@@ -239,88 +251,86 @@ __global__ __launch_bounds__(conv::kThreads) void causal_conv_backward_kernel(
             }
             const typename E::store_t *xp = x.p + at.b * L * x.ld + at.c0, *dyp = dy.p + at.b * L * dy.ld + at.c0;
             const int64_t first = t0 == 0 ? -(W - 1) : t0;   // the first gradient that this run writes
-            // the gradient of token s from z_s .. z_{s+W-1}, of which zt is the last
-            auto out = [&](int64_t s, const float (&zt)[N]) {
-                float g[N];
-#pragma unroll
-                for (int v = 0; v < N; ++v) {
-                    g[v] = taps.w[0][v] * zt[v];
-#pragma unroll
-                    for (int k = 1; k < W; ++k) g[v] = __builtin_fmaf(taps.w[k][v], z[W - 1 - k][v], g[v]);
-                }
-                if (s < first) return;
-                if (s + (W - 1) >= n && dstate_out) {
-                    float f[N];
-                    conv::Word<E, N>::unpack(
-                        conv::load<E, N>(dstate_out + (at.b * (W - 1) + s + (W - 1) - n) * D + at.c0), f);
-#pragma unroll
-                    for (int v = 0; v < N; ++v) g[v] += f[v];
-                }
-                if (s >= 0) conv::store<E, N>(dxp + s * dx.ld, conv::Word<E, N>::pack(g));
-                else if (dstate) conv::store<E, N>(dstate + (at.b * (W - 1) + s + (W - 1)) * D + at.c0, conv::Word<E, N>::pack(g));
-            };
-            auto shift = [&](const float (&zt)[N]) {
-#pragma unroll
-                for (int v = 0; v < N; ++v) {
-#pragma unroll
-                    for (int k = 0; k < W - 2; ++k) z[k][v] = z[k + 1][v];
-                    z[W - 2][v] = zt[v];
-                }
-            };
-            // one token: z_t, its share of the taps' gradients where it is the run's own
-            auto token = [&](int64_t t, raw xw, raw dyw, bool mine) {
-                float f[N], zt[N];
-                conv::Word<E, N>::unpack(xw, f);
-                conv::Word<E, N>::unpack(dyw, zt);
-#pragma unroll
-                for (int v = 0; v < N; ++v) {
-                    if constexpr (A == Act::Silu) {
-                        float s = taps.bias[v];
-#pragma unroll
-                        for (int k = 0; k < W - 1; ++k) s = __builtin_fmaf(taps.w[k][v], e[k][v], s);
-                        zt[v] *= silu_slope(__builtin_fmaf(taps.w[W - 1][v], f[v], s));
-                    }
-                    if (mine) {
-#pragma unroll
-                        for (int k = 0; k < W - 1; ++k) dw[k][v] = __builtin_fmaf(zt[v], e[k][v], dw[k][v]);
-                        dw[W - 1][v] = __builtin_fmaf(zt[v], f[v], dw[W - 1][v]);
-                        dw[W][v] += zt[v];
-                    }
-#pragma unroll
-                    for (int k = 0; k < W - 2; ++k) e[k][v] = e[k + 1][v];
-                    e[W - 2][v] = f[v];
-                }
-                out(t - (W - 1), zt);
-                shift(zt);
-            };
+            const int64_t stop = live + W - 1;               // tokens from which its gradients come
             raw nx[U], ny[U];
-            auto fetch = [&](int64_t t) {
+            auto fetch = [&](int64_t t) {   // tokens behind the sequence read its last one
+                if (t + U <= n) {
 #pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const int64_t c = min(t + i, live - 1);
-                    nx[i] = conv::load<E, N>(xp + c * x.ld);
-                    ny[i] = conv::load<E, N>(dyp + c * dy.ld);
+                    for (int i = 0; i < U; ++i) {
+                        nx[i] = conv::load<E, N, kNt>(xp + t * x.ld + i * x.ld);
+                        ny[i] = conv::load<E, N, kNt>(dyp + t * dy.ld + i * dy.ld);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const int64_t c = min(t + i, n - 1);
+                        nx[i] = conv::load<E, N, kNt>(xp + c * x.ld);
+                        ny[i] = conv::load<E, N, kNt>(dyp + c * dy.ld);
+                    }
                 }
             };
-            if (t0 < live) fetch(t0);
-            for (int64_t t = t0; t < live; t += U) {
+            // U tokens from t.  Whole blocks are the run's own; what is left of it, and the tokens behind it, go
+            // token by token (`ends`), z zero behind the sequence.
+            auto block = [&](auto ends_c, int64_t t) {
+                constexpr bool ends = decltype(ends_c)::value;
                 raw cx[U], cy[U];
 #pragma unroll
                 for (int i = 0; i < U; ++i) cx[i] = nx[i], cy[i] = ny[i];
-                if (t + U < live) fetch(t + U);
+                if (t + U < (ends ? min(stop, n) : stop)) fetch(t + U);
+                float ew[W - 1 + U][N], zw[W - 1 + U][N];   // windows over the block
 #pragma unroll
-                for (int i = 0; i < U; ++i)
-                    if (t + i < live) token(t + i, cx[i], cy[i], true);
-            }
-            for (int64_t t = live; t < live + W - 1; ++t) {   // behind the run: zero behind the sequence's end
-                if (t < n) {
-                    token(t, conv::load<E, N>(xp + t * x.ld), conv::load<E, N>(dyp + t * dy.ld), false);
-                } else {
-                    const float zero[N] = {};
-                    out(t - (W - 1), zero);
-                    shift(zero);
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int v = 0; v < N; ++v) ew[j][v] = e[j][v], zw[j][v] = z[j][v];
+                typename E::store_t *dst = dxp + t * dx.ld;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    if (ends && t + i >= stop) return;
+                    float g[N];
+                    conv::Word<E, N>::unpack(cx[i], ew[W - 1 + i]);
+                    conv::Word<E, N>::unpack(cy[i], zw[W - 1 + i]);
+#pragma unroll
+                    for (int v = 0; v < N; ++v) {
+                        float zt = zw[W - 1 + i][v];
+                        if constexpr (A == Act::Silu) {
+                            float s = taps.bias[v];
+#pragma unroll
+                            for (int k = 0; k < W; ++k) s = __builtin_fmaf(taps.w[k][v], ew[i + k][v], s);
+                            zt *= silu_slope(s);
+                        }
+                        if (ends) zt = t + i < n ? zt : 0.0f;
+                        zw[W - 1 + i][v] = zt;
+                        if (!ends || t + i < live) {
+#pragma unroll
+                            for (int k = 0; k < W; ++k) dw[k][v] = __builtin_fmaf(zt, ew[i + k][v], dw[k][v]);
+                            dw[W][v] += zt;
+                        }
+                        g[v] = taps.w[0][v] * zt;   // of token t + i - (W - 1), of whose z this is the last
+#pragma unroll
+                        for (int k = 1; k < W; ++k) g[v] = __builtin_fmaf(taps.w[k][v], zw[W - 1 + i - k][v], g[v]);
+                    }
+                    const int64_t s = t + i - (W - 1);
+                    if ((ends || i < W - 1) && s < first) continue;
+                    if (ends && t + i >= n && dstate_out) {   // a token of the outgoing state
+                        float f[N];
+                        conv::Word<E, N>::unpack(conv::load<E, N>(dstate_out + (at.b * (W - 1) + t + i - n) * D + at.c0), f);
+#pragma unroll
+                        for (int v = 0; v < N; ++v) g[v] += f[v];
+                    }
+                    if (!(ends || i < W - 1) || s >= 0)
+                        conv::store<E, N, kNt>(dst + (i - (W - 1)) * dx.ld, conv::Word<E, N>::pack(g));
+                    else if (dstate)
+                        conv::store<E, N>(dstate + (at.b * (W - 1) + t + i) * D + at.c0, conv::Word<E, N>::pack(g));
                 }
-            }
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int v = 0; v < N; ++v) e[j][v] = ew[U + j][v], z[j][v] = zw[U + j][v];
+            };
+            if (t0 < n) fetch(t0);
+            int64_t t = t0;
+            for (; t + U <= live; t += U) block(std::false_type{}, t);
+            for (; t < stop; t += U) block(std::true_type{}, t);
         }
         for (int64_t t = max(t0, n); t < end; ++t) conv::store<E, N>(dxp + t * dx.ld, raw{});
     }
@@ -362,37 +372,48 @@ __global__ __launch_bounds__(256) void conv_sum_kernel(const float *__restrict__
     else if (dbias) dbias[d] = s;
 }
 
-// One decode token: a thread has N channels of one sequence.
-template <typename E, int N, int W, Act A>
+// One decode token: a thread has N channels of kRows sequences, one set of taps for them all.  A missing last
+// sequence reads the one before it and stores nothing.
+template <typename E, int N, int W, Act A, int kRows>
 __global__ __launch_bounds__(conv::kThreads) void causal_conv_step_kernel(
     typename E::store_t *__restrict__ state, const typename E::store_t *__restrict__ x, const float *__restrict__ w,
     const float *__restrict__ bias, typename E::store_t *__restrict__ y, int64_t batch, int D, int words, int64_t ld_x,
     int64_t ld_y) {
     using raw = typename conv::Word<E, N>::raw;
-    const int64_t id = (int64_t)blockIdx.x * conv::kThreads + threadIdx.x, b = id / words;
-    if (b >= batch) return;
-    const int c0 = (int)(id - b * words) * N;
-    typename E::store_t *st = state + b * (W - 1) * D + c0;
-    raw win[W];
+    const int64_t id = (int64_t)blockIdx.x * conv::kThreads + threadIdx.x, b0 = id / words * kRows;
+    if (b0 >= batch) return;
+    const int c0 = (int)(id % words) * N;
+    raw win[kRows][W];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) win[j] = conv::load<E, N>(st + (int64_t)j * D);
-    win[W - 1] = conv::load<E, N>(x + b * ld_x + c0);
-    const conv::Taps<W, N> taps(w, bias, c0);
-    float o[N];
+    for (int r = 0; r < kRows; ++r) {
+        const int64_t b = min(b0 + r, batch - 1);
+        const typename E::store_t *st = state + b * (W - 1) * D + c0;
 #pragma unroll
-    for (int v = 0; v < N; ++v) o[v] = taps.bias[v];
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-        float f[N];
-        conv::Word<E, N>::unpack(win[k], f);
-#pragma unroll
-        for (int v = 0; v < N; ++v) o[v] = __builtin_fmaf(taps.w[k][v], f[v], o[v]);
+        for (int j = 0; j < W - 1; ++j) win[r][j] = conv::load<E, N>(st + (int64_t)j * D);
+        win[r][W - 1] = conv::load<E, N>(x + b * ld_x + c0);
     }
+    const conv::Taps<W, N> taps(w, bias, c0);
 #pragma unroll
-    for (int v = 0; v < N; ++v) o[v] = activate<A>(o[v]);
+    for (int r = 0; r < kRows; ++r) {
+        const int64_t b = b0 + r;
+        if (b >= batch) break;
+        float o[N];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) conv::store<E, N>(st + (int64_t)j * D, win[j + 1]);
-    conv::store<E, N>(y + b * ld_y + c0, conv::Word<E, N>::pack(o));
+        for (int v = 0; v < N; ++v) o[v] = taps.bias[v];
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            float f[N];
+            conv::Word<E, N>::unpack(win[r][k], f);
+#pragma unroll
+            for (int v = 0; v < N; ++v) o[v] = __builtin_fmaf(taps.w[k][v], f[v], o[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < N; ++v) o[v] = activate<A>(o[v]);
+        typename E::store_t *st = state + b * (W - 1) * D + c0;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) conv::store<E, N>(st + (int64_t)j * D, win[r][j + 1]);
+        conv::store<E, N>(y + b * ld_y + c0, conv::Word<E, N>::pack(o));
+    }
 }
 
 }  // namespace jscan
