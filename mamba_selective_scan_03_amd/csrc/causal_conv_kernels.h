@@ -22,12 +22,6 @@ namespace conv {
 
 constexpr int kThreads = 256;
 
-typedef float f32_pair __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16_pair __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {   // one conversion instruction for both
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32_pair{lo, hi}), bf16_pair));
-}
-
 // N channels of one token in memory: aligned to their element alone, so that any row stride takes the same
 // loads (the hardware takes any address).
 template <typename E, int N> struct Word;

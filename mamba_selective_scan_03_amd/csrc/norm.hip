@@ -23,13 +23,21 @@ Layout layout_for(int64_t K, int64_t es) {
     return {waves, (int)((pieces + waves * 64 - 1) / (waves * 64))};
 }
 
-// Work-groups of a call: each goes on to further rows.
-int64_t groups_for(const Layout &l, int64_t M, int64_t waves_at_once) {
-    const int64_t most = waves_at_once / l.waves;
-    return M < most ? M : most;
+constexpr int64_t kMostGroups = (int64_t)1 << 20;   // of a launch
+
+// Work-groups of the forward call: a row each, more only beyond the largest launch.
+int64_t forward_groups(int64_t M) { return M < kMostGroups ? M : kMostGroups; }
+
+// Work-groups of the backward pass, each of which goes on to further rows and leaves a share of the gain's gradient.
+int64_t backward_groups(const Layout &l, int64_t M) {
+    const int64_t each = l.chunks == 0 ? 1 : jscan::norm::rows_at_once(l.waves, l.chunks);
+    const int64_t most = l.waves == 1 ? 1024 : l.waves == 4 ? 512 : 256;   // four, eight, sixteen waves a CU
+    const int64_t rows = (M + each - 1) / each;
+    return rows < most ? rows : most;
 }
 
-constexpr int64_t kForwardWaves = 8192, kBackwardWaves = 2048;
+// Tensors beyond the last-level cache go by with the non-temporal hint.
+constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 
 struct NormArgs {
     Pair x, residual, y, total, dy, dtotal, dx;
@@ -45,6 +53,7 @@ template <typename T> NormRows<const T> in_rows(Pair t) { return {static_cast<co
 template <typename T> NormRows<T> out_rows(Pair t) { return {static_cast<T *>(const_cast<void *>(t.p)), t.ld}; }
 
 template <typename E, int kWaves, int kChunks, bool kInt8> void launch_forward(const NormArgs &a) {
+    constexpr int64_t kEach = (int64_t)sizeof(typename E::store_t);
     using T = typename E::store_t;
     const jscan::NormOut<E> out{out_rows<T>(a.y), a.q, a.scale};
     auto launch = [&](auto kernel) {
@@ -52,19 +61,26 @@ template <typename E, int kWaves, int kChunks, bool kInt8> void launch_forward(c
                            in_rows<T>(a.residual), a.gain, out, out_rows<T>(a.total), a.M, (int)a.K, a.eps);
     };
     if constexpr (kChunks == 0) launch(jscan::rms_norm_any_kernel<E, kWaves, kInt8>);
-    else if (a.residual.p) launch(jscan::rms_norm_kernel<E, kWaves, kChunks, kInt8, true>);
-    else launch(jscan::rms_norm_kernel<E, kWaves, kChunks, kInt8, false>);
+    else if (a.residual.p && a.M * a.K * kEach * 4 > kStreamBytes)
+        launch(jscan::rms_norm_kernel<E, kWaves, kChunks, kInt8, true, true>);
+    else if (a.residual.p) launch(jscan::rms_norm_kernel<E, kWaves, kChunks, kInt8, true, false>);
+    else if (a.M * a.K * kEach * 2 > kStreamBytes)
+        launch(jscan::rms_norm_kernel<E, kWaves, kChunks, kInt8, false, true>);
+    else launch(jscan::rms_norm_kernel<E, kWaves, kChunks, kInt8, false, false>);
 }
 
 template <typename E, int kWaves, int kChunks> void launch_backward(const NormArgs &a) {
+    const bool streams = a.M * a.K * (int64_t)sizeof(typename E::store_t) * 4 > kStreamBytes;
     using T = typename E::store_t;
     auto launch = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)a.groups), dim3(kWaves * 64), 0, a.stream, in_rows<T>(a.total), a.gain,
                            in_rows<T>(a.dy), in_rows<T>(a.dtotal), out_rows<T>(a.dx), a.partial, a.M, (int)a.K, a.eps);
     };
     if constexpr (kChunks == 0) launch(jscan::rms_norm_backward_any_kernel<E, kWaves>);
-    else if (a.dtotal.p) launch(jscan::rms_norm_backward_kernel<E, kWaves, kChunks, true>);
-    else launch(jscan::rms_norm_backward_kernel<E, kWaves, kChunks, false>);
+    else if (a.dtotal.p && streams) launch(jscan::rms_norm_backward_kernel<E, kWaves, kChunks, true, true>);
+    else if (a.dtotal.p) launch(jscan::rms_norm_backward_kernel<E, kWaves, kChunks, true, false>);
+    else if (streams) launch(jscan::rms_norm_backward_kernel<E, kWaves, kChunks, false, true>);
+    else launch(jscan::rms_norm_backward_kernel<E, kWaves, kChunks, false, false>);
 }
 
 // Calls f<waves, chunks>() for a layout.
@@ -91,7 +107,7 @@ template <typename F> void with_layout(const Layout &l, F f) {
 
 template <bool kInt8> void run_forward(NormArgs &a, jscan_dtype dtype) {
     const Layout l = layout_for(a.K, elem_bytes(dtype));
-    a.groups = groups_for(l, a.M, kForwardWaves);
+    a.groups = forward_groups(a.M);
     with_layout(l, [&](auto w, auto c) {
         if (dtype == JSCAN_BF16) launch_forward<jscan::BF16, decltype(w)::value, decltype(c)::value, kInt8>(a);
         else launch_forward<jscan::F32, decltype(w)::value, decltype(c)::value, kInt8>(a);
@@ -163,7 +179,7 @@ jscan_status jscan_rms_norm_quantize(const void *x, const void *residual, const 
 // Room for the groups of either type: rows of fp32 take four waves where those of bf16 take one.
 int64_t jscan_rms_norm_backward_workspace(int64_t M, int64_t K) {
     if (!sizes_ok(M, K, 0.0f)) return -1;
-    const int64_t a = groups_for(layout_for(K, 2), M, kBackwardWaves), b = groups_for(layout_for(K, 4), M, kBackwardWaves);
+    const int64_t a = backward_groups(layout_for(K, 2), M), b = backward_groups(layout_for(K, 4), M);
     return (a > b ? a : b) * K * 4;
 }
 
@@ -193,14 +209,14 @@ jscan_status jscan_rms_norm_backward(const void *total, const float *gain, const
     a.stream = static_cast<hipStream_t>(stream);
     if (M > 0) {
         const Layout l = layout_for(K, es);
-        a.groups = groups_for(l, M, kBackwardWaves);
+        a.groups = backward_groups(l, M);
         with_layout(l, [&](auto w, auto c) {
             if (dtype == JSCAN_BF16) launch_backward<jscan::BF16, decltype(w)::value, decltype(c)::value>(a);
             else launch_backward<jscan::F32, decltype(w)::value, decltype(c)::value>(a);
         });
         if (launch_status() != JSCAN_OK) return JSCAN_ERR_HIP;
     }
-    hipLaunchKernelGGL(jscan::norm_gain_kernel, dim3((unsigned)((K + 63) / 64)), dim3(256), 0, a.stream, a.partial, dgain,
+    hipLaunchKernelGGL(jscan::norm_gain_kernel, dim3((unsigned)((K + 63) / 64)), dim3(1024), 0, a.stream, a.partial, dgain,
                        a.groups, (int)K);
     return launch_status();
 }

@@ -37,7 +37,7 @@ template <> struct Piece<BF16> {
         for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(w[i]), f[2 * i + 1] = bf16_hi(w[i]);
     }
     static __device__ __forceinline__ raw pack(const float (&f)[8]) {
-        return raw{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+        return raw{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
     }
 };
 template <> struct Piece<F32> {
@@ -54,11 +54,14 @@ template <> struct Piece<F32> {
 };
 template <typename E> using Raw = typename Piece<E>::raw;
 
-template <typename E> __device__ __forceinline__ Raw<E> load(const typename E::store_t *p) {
+// kNt: with the non-temporal hint, for tensors that go by.
+template <typename E, bool kNt> __device__ __forceinline__ Raw<E> load(const typename E::store_t *p) {
+    if constexpr (kNt) return __builtin_nontemporal_load(reinterpret_cast<const Raw<E> *>(p));
     return *reinterpret_cast<const Raw<E> *>(p);
 }
-template <typename E> __device__ __forceinline__ void store(typename E::store_t *p, Raw<E> v) {
-    *reinterpret_cast<Raw<E> *>(p) = v;
+template <typename E, bool kNt> __device__ __forceinline__ void store(typename E::store_t *p, Raw<E> v) {
+    if constexpr (kNt) __builtin_nontemporal_store(v, reinterpret_cast<Raw<E> *>(p));
+    else *reinterpret_cast<Raw<E> *>(p) = v;
 }
 
 // Which kChunks pieces of a row a thread of kWaves waves has: piece j kWaves 64 + thread.  Where the pieces do not divide the
@@ -82,26 +85,56 @@ template <typename E, int kWaves, int kChunks> struct Place {
     __device__ __forceinline__ bool live() const { return lo < n; }
 };
 
-// Sum of a and, by kMax, maximum or sum of b over a work-group; `part` holds kWaves pairs, of another parity for every
-// second call, so that one barrier a call is enough.
-template <int kWaves, bool kMax> __device__ __forceinline__ void group_reduce(float &a, float &b, float2 *part) {
+// A value of another lane: DPP inside rows of 16 lanes (quads by quad_perm, the other quad, the other half by mirrors),
+// permlane swaps across them.
+template <int kControl> __device__ __forceinline__ float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), kControl, 0xF, 0xF, true));
+}
+typedef unsigned u32_pair __attribute__((ext_vector_type(2)));
+// Every lane's v joined with the other rows': the two results of a swap of v with itself are v and its partner.
+template <bool kMax> __device__ __forceinline__ float join(float a, float b) { return kMax ? fmaxf(a, b) : a + b; }
+template <bool kMax> __device__ __forceinline__ float wave_reduce(float v) {
+    v = join<kMax>(v, dpp<0xB1>(v));    // quad_perm [1,0,3,2]
+    v = join<kMax>(v, dpp<0x4E>(v));    // quad_perm [2,3,0,1]
+    v = join<kMax>(v, dpp<0x141>(v));   // row_half_mirror
+    v = join<kMax>(v, dpp<0x140>(v));   // row_mirror
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto across16 = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = join<kMax>(__builtin_bit_cast(float, (unsigned)across16[0]), __builtin_bit_cast(float, (unsigned)across16[1]));
+    const unsigned w = __builtin_bit_cast(unsigned, v);
+    const auto across32 = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    return join<kMax>(__builtin_bit_cast(float, (unsigned)across32[0]), __builtin_bit_cast(float, (unsigned)across32[1]));
+}
+
+// Sums of a and, by kMax, maxima or sums of b over a work-group, for kRows rows at once; `part` holds their pairs of
+// every wave, another one for every second call, so that one barrier a call is enough.
+template <int kWaves, bool kMax, int kRows>
+__device__ __forceinline__ void group_reduce(float (&a)[kRows], float (&b)[kRows], float2 (&part)[kRows][kWaves]) {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        a += __shfl_xor(a, o);
-        const float other = __shfl_xor(b, o);
-        b = kMax ? fmaxf(b, other) : b + other;
+    for (int r = 0; r < kRows; ++r) {
+        a[r] = wave_reduce<false>(a[r]);
+        b[r] = wave_reduce<kMax>(b[r]);
     }
     if constexpr (kWaves > 1) {
-        if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = make_float2(a, b);
-        __syncthreads();
-        a = part[0].x, b = part[0].y;
+        if (threadIdx.x % 64 == 0) {
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) {
-            a += part[i].x;
-            b = kMax ? fmaxf(b, part[i].y) : b + part[i].y;
+            for (int r = 0; r < kRows; ++r) part[r][threadIdx.x / 64] = make_float2(a[r], b[r]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            a[r] = part[r][0].x, b[r] = part[r][0].y;
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i) a[r] += part[r][i].x, b[r] = join<kMax>(b[r], part[r][i].y);
         }
     }
 }
+
+// Rows that a work-group of the backward pass takes at a time: two where a thread has up to two pieces of each (us, one,
+// two and four: 65536 x 256 bf16 45, 39, 43; 65536 x 4096 384, 359).  Sixteen waves leave 128 registers a thread,
+// which hold one row and none on its way (20000 x 8192 fp32 468 us, with two rows 1922).
+constexpr int rows_at_once(int waves, int chunks) { return waves < 16 && chunks <= 2 ? 2 : 1; }
+constexpr bool fetches_ahead(int waves) { return waves < 16; }
 
 __device__ __forceinline__ float rms_scale(float sum, int K, float eps) {
     return __builtin_amdgcn_rsqf(sum / (float)K + eps);
@@ -125,7 +158,7 @@ template <typename E> struct NormOut {
 };
 
 // total may be x or residual itself: a row is stored after the work-group's last load of it.
-template <typename E, int kWaves, int kChunks, bool kInt8, bool kResidual>
+template <typename E, int kWaves, int kChunks, bool kInt8, bool kResidual, bool kNt>
 __global__ __launch_bounds__(kWaves * 64) void rms_norm_kernel(NormRows<const typename E::store_t> x,
                                                                NormRows<const typename E::store_t> residual,
                                                                const float *__restrict__ gain, NormOut<E> out,
@@ -134,57 +167,50 @@ __global__ __launch_bounds__(kWaves * 64) void rms_norm_kernel(NormRows<const ty
     using P = norm::Piece<E>;
     using raw = norm::Raw<E>;
     constexpr int n = P::n;
-    __shared__ float2 part[2][kWaves];
+    __shared__ float2 part[2][1][kWaves];
     const norm::Place<E, kWaves, kChunks> at(K);
-    raw xn[kChunks], rn[kChunks];
-    auto fetch = [&](int64_t m) {
+    float g[kChunks][n];
+    int parity = 0;
+    for (int64_t m = blockIdx.x; m < M; m += gridDim.x, parity ^= 1) {
+        raw t[kChunks], rest[kChunks];
 #pragma unroll
         for (int j = 0; j < kChunks; ++j) {
-            xn[j] = norm::load<E>(x.p + m * x.ld + at.at[j]);
-            if constexpr (kResidual) rn[j] = norm::load<E>(residual.p + m * residual.ld + at.at[j]);
+            t[j] = norm::load<E, kNt>(x.p + m * x.ld + at.at[j]);
+            if constexpr (kResidual) rest[j] = norm::load<E, kNt>(residual.p + m * residual.ld + at.at[j]);
         }
-    };
-    int64_t m = blockIdx.x;
-    fetch(m);
-    float g[kChunks][n];
-    norm::load_gain<E, kChunks>(g, gain, at.at);
-    for (int parity = 0; m < M; m += gridDim.x, parity ^= 1) {
-        raw t[kChunks];
-        float sum = 0.0f, amax = 0.0f, poison = 0.0f;
+        if (m == blockIdx.x) norm::load_gain<E, kChunks>(g, gain, at.at);
+        float sum[1] = {0.0f}, amax[1] = {0.0f}, poison = 0.0f;
 #pragma unroll
         for (int j = 0; j < kChunks; ++j) {
             if constexpr (kResidual) {
                 float a[n], b[n];
-                P::unpack(xn[j], a);
-                P::unpack(rn[j], b);
+                P::unpack(t[j], a);
+                P::unpack(rest[j], b);
 #pragma unroll
                 for (int i = 0; i < n; ++i) a[i] += b[i];
                 t[j] = P::pack(a);
-            } else {
-                t[j] = xn[j];
             }
             float f[n];
             P::unpack(at.counted(t[j], j), f);
 #pragma unroll
             for (int i = 0; i < n; ++i) {
-                sum = __builtin_fmaf(f[i], f[i], sum);
+                sum[0] = __builtin_fmaf(f[i], f[i], sum[0]);
                 if constexpr (kInt8) {
                     const float v = f[i] * g[j][i];
-                    amax = fmaxf(amax, fabsf(v));
+                    amax[0] = fmaxf(amax[0], fabsf(v));
                     poison = __builtin_fmaf(v, 0.0f, poison);
                 }
             }
         }
-        if (m + gridDim.x < M) fetch(m + gridDim.x);
-        if constexpr (kInt8) amax = poison == 0.0f ? amax : __builtin_inff();
-        norm::group_reduce<kWaves, true>(sum, amax, part[parity]);
-        const float r = norm::rms_scale(sum, K, eps);
-        float s = 0.0f, inv = 0.0f;
+        if constexpr (kInt8) amax[0] = poison == 0.0f ? amax[0] : __builtin_inff();
+        norm::group_reduce<kWaves, true, 1>(sum, amax, part[parity]);
+        const float r = norm::rms_scale(sum[0], K, eps);
+        float inv = 0.0f;
         bool finite = true;
         if constexpr (kInt8) {
             // (t gain) r rounds in order, so the row's largest |y| is that of its largest |t gain|
-            finite = sum < __builtin_inff() && amax * r < __builtin_inff();
-            s = finite ? quant::row_scale(amax * r) : __builtin_nanf("");
+            finite = sum[0] < __builtin_inff() && amax[0] * r < __builtin_inff();
+            const float s = finite ? quant::row_scale(amax[0] * r) : __builtin_nanf("");
             inv = 1.0f / s;
             if (threadIdx.x == 0) out.scale[m] = s;
         }
@@ -200,9 +226,9 @@ __global__ __launch_bounds__(kWaves * 64) void rms_norm_kernel(NormRows<const ty
 #pragma unroll
                 for (int i = 0; i < n / 4; ++i) dst[i] = finite ? quant::pack4(f + 4 * i, inv) : 0u;
             } else {
-                norm::store<E>(out.y.p + m * out.y.ld + at.at[j], P::pack(f));
+                norm::store<E, kNt>(out.y.p + m * out.y.ld + at.at[j], P::pack(f));
             }
-            if (kResidual && total.p) norm::store<E>(total.p + m * total.ld + at.at[j], t[j]);
+            if (kResidual && total.p) norm::store<E, kNt>(total.p + m * total.ld + at.at[j], t[j]);
         }
     }
 }
@@ -215,7 +241,7 @@ __global__ __launch_bounds__(kWaves * 64) void rms_norm_any_kernel(NormRows<cons
                                                                    const float *__restrict__ gain, NormOut<E> out,
                                                                    NormRows<typename E::store_t> total, int64_t M, int K,
                                                                    float eps) {
-    __shared__ float2 part[2][kWaves];
+    __shared__ float2 part[2][1][kWaves];
     int parity = 0;
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x, parity ^= 1) {
         const typename E::store_t *xr = x.p + m * x.ld;
@@ -229,19 +255,19 @@ __global__ __launch_bounds__(kWaves * 64) void rms_norm_any_kernel(NormRows<cons
             return v;
         };
         const bool kept = residual.p && total.p;
-        float sum = 0.0f, amax = 0.0f, poison = 0.0f;
+        float sum[1] = {0.0f}, amax[1] = {0.0f}, poison = 0.0f;
         for (int k = threadIdx.x; k < K; k += kWaves * 64) {
             const float t = value(k), v = t * gain[k];
             if (kept) E::store(total.p + m * total.ld + k, t);
-            sum = __builtin_fmaf(t, t, sum);
-            amax = fmaxf(amax, fabsf(v));
+            sum[0] = __builtin_fmaf(t, t, sum[0]);
+            amax[0] = fmaxf(amax[0], fabsf(v));
             poison = __builtin_fmaf(v, 0.0f, poison);
         }
-        amax = poison == 0.0f ? amax : __builtin_inff();
-        norm::group_reduce<kWaves, true>(sum, amax, part[parity]);
-        const float r = norm::rms_scale(sum, K, eps);
-        const bool finite = sum < __builtin_inff() && amax * r < __builtin_inff();
-        const float s = finite ? quant::row_scale(amax * r) : __builtin_nanf(""), inv = 1.0f / s;
+        amax[0] = poison == 0.0f ? amax[0] : __builtin_inff();
+        norm::group_reduce<kWaves, true, 1>(sum, amax, part[parity]);
+        const float r = norm::rms_scale(sum[0], K, eps);
+        const bool finite = sum[0] < __builtin_inff() && amax[0] * r < __builtin_inff();
+        const float s = finite ? quant::row_scale(amax[0] * r) : __builtin_nanf(""), inv = 1.0f / s;
         if (kInt8 && threadIdx.x == 0) out.scale[m] = s;
         for (int k = threadIdx.x; k < K; k += kWaves * 64) {
             const float t = kept ? E::load(total.p + m * total.ld + k) : value(k), y = t * gain[k] * r;
@@ -251,67 +277,93 @@ __global__ __launch_bounds__(kWaves * 64) void rms_norm_any_kernel(NormRows<cons
     }
 }
 
-// The backward pass; dx may be dtotal itself.  partial[work-group][K]: the gain's gradient of a work-group's rows.
-template <typename E, int kWaves, int kChunks, bool kAdd>
+// The backward pass; dx may be dtotal itself.  A work-group takes kRows rows at a time, the next ones on their way (kAhead); rows
+// behind the last one read it again and count nothing.  partial[work-group][K]: the gain's gradient of a
+// work-group's rows.
+template <typename E, int kWaves, int kChunks, bool kAdd, bool kNt>
 __global__ __launch_bounds__(kWaves * 64) void rms_norm_backward_kernel(
     NormRows<const typename E::store_t> total, const float *__restrict__ gain, NormRows<const typename E::store_t> dy,
     NormRows<const typename E::store_t> dtotal, NormRows<typename E::store_t> dx, float *__restrict__ partial, int64_t M,
     int K, float eps) {
     using P = norm::Piece<E>;
     using raw = norm::Raw<E>;
-    constexpr int n = P::n;
-    __shared__ float2 part[2][kWaves];
+    constexpr int n = P::n, kRows = norm::rows_at_once(kWaves, kChunks);
+    constexpr bool kAhead = norm::fetches_ahead(kWaves);
+    // the longest rows are read again for their gradients, from the caches: 128 registers do not hold them beside
+    // the gain and its gradient (us: 8000 x 30000 bf16 704, with spills 857; 8000 x 20000 255 and 307)
+    constexpr bool kAgain = kWaves == 16 && kChunks * n > 16;
+    __shared__ float2 part[2][kRows][kWaves];
     const norm::Place<E, kWaves, kChunks> at(K);
-    raw tn[kChunks], yn[kChunks], an[kChunks];
-    auto fetch = [&](int64_t m) {
+    raw tn[kRows][kChunks], yn[kRows][kChunks], an[kRows][kChunks];
+    auto fetch = [&](int64_t m0) {
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            tn[j] = norm::load<E>(total.p + m * total.ld + at.at[j]);
-            yn[j] = norm::load<E>(dy.p + m * dy.ld + at.at[j]);
-            if constexpr (kAdd) an[j] = norm::load<E>(dtotal.p + m * dtotal.ld + at.at[j]);
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t m = min(m0 + r, M - 1);
+#pragma unroll
+            for (int j = 0; j < kChunks; ++j) {
+                tn[r][j] = norm::load<E, kNt && !kAgain>(total.p + m * total.ld + at.at[j]);
+                yn[r][j] = norm::load<E, kNt && !kAgain>(dy.p + m * dy.ld + at.at[j]);
+                if constexpr (kAdd && !kAgain) an[r][j] = norm::load<E, kNt>(dtotal.p + m * dtotal.ld + at.at[j]);
+            }
         }
     };
-    int64_t m = blockIdx.x;
-    fetch(m);
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t m0 = (int64_t)blockIdx.x * kRows;
+    if constexpr (kAhead) fetch(m0);
     float g[kChunks][n], dg[kChunks][n];
     norm::load_gain<E, kChunks>(g, gain, at.at);
 #pragma unroll
     for (int j = 0; j < kChunks; ++j)
 #pragma unroll
         for (int i = 0; i < n; ++i) dg[j][i] = 0.0f;
-    for (int parity = 0; m < M; m += gridDim.x, parity ^= 1) {
-        raw t[kChunks], d[kChunks], a[kChunks];
-        float sum = 0.0f, along = 0.0f;
+    for (int parity = 0; m0 < M; m0 += step, parity ^= 1) {
+        raw t[kRows][kChunks], d[kRows][kChunks], a[kRows][kChunks];
+        float sum[kRows], along[kRows];
+        if constexpr (!kAhead) fetch(m0);
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            t[j] = tn[j], d[j] = yn[j];
-            if constexpr (kAdd) a[j] = an[j];
-            float f[n], e[n];
-            P::unpack(at.counted(t[j], j), f);
-            P::unpack(at.counted(d[j], j), e);
+        for (int r = 0; r < kRows; ++r) {
+            sum[r] = along[r] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < n; ++i) {
-                sum = __builtin_fmaf(f[i], f[i], sum);
-                along = __builtin_fmaf(e[i] * g[j][i], f[i], along);
+            for (int j = 0; j < kChunks; ++j) {
+                t[r][j] = tn[r][j], d[r][j] = yn[r][j];
+                if constexpr (kAdd && !kAgain) a[r][j] = an[r][j];
+                float f[n], e[n];
+                P::unpack(at.counted(t[r][j], j), f);
+                P::unpack(at.counted(d[r][j], j), e);
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    sum[r] = __builtin_fmaf(f[i], f[i], sum[r]);
+                    along[r] = __builtin_fmaf(e[i] * g[j][i], f[i], along[r]);
+                }
             }
         }
-        if (m + gridDim.x < M) fetch(m + gridDim.x);
-        norm::group_reduce<kWaves, false>(sum, along, part[parity]);
-        const float r = norm::rms_scale(sum, K, eps), c = along / (float)K * r;   // mean of g t r
+        if (kAhead && m0 + step < M) fetch(m0 + step);
+        norm::group_reduce<kWaves, false, kRows>(sum, along, part[parity]);
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            if (j == kChunks - 1 && !at.live()) break;
-            float f[n], e[n], o[n];
-            P::unpack(t[j], f);
-            P::unpack(d[j], e);
-            if constexpr (kAdd) P::unpack(a[j], o);
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t m = m0 + r;
+            if (m >= M) break;
+            const float rms = norm::rms_scale(sum[r], K, eps), c = along[r] / (float)K * rms;   // mean of g t rms
 #pragma unroll
-            for (int i = 0; i < n; ++i) {
-                const float t_r = f[i] * r, v = r * __builtin_fmaf(-t_r, c, e[i] * g[j][i]);
-                o[i] = kAdd ? v + o[i] : v;
-                dg[j][i] = __builtin_fmaf(e[i], t_r, dg[j][i]);
+            for (int j = 0; j < kChunks; ++j) {
+                if (j == kChunks - 1 && !at.live()) break;
+                if constexpr (kAgain) {
+                    t[r][j] = norm::load<E, false>(total.p + m * total.ld + at.at[j]);
+                    d[r][j] = norm::load<E, false>(dy.p + m * dy.ld + at.at[j]);
+                    if constexpr (kAdd) a[r][j] = norm::load<E, false>(dtotal.p + m * dtotal.ld + at.at[j]);
+                }
+                float f[n], e[n], o[n];
+                P::unpack(t[r][j], f);
+                P::unpack(d[r][j], e);
+                if constexpr (kAdd) P::unpack(a[r][j], o);
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const float t_r = f[i] * rms, v = rms * __builtin_fmaf(-t_r, c, e[i] * g[j][i]);
+                    o[i] = kAdd ? v + o[i] : v;
+                    dg[j][i] = __builtin_fmaf(e[i], t_r, dg[j][i]);
+                }
+                norm::store<E, kNt>(dx.p + m * dx.ld + at.at[j], P::pack(o));
             }
-            norm::store<E>(dx.p + m * dx.ld + at.at[j], P::pack(o));
         }
     }
     float *to = partial + (int64_t)blockIdx.x * K;
@@ -328,20 +380,20 @@ __global__ __launch_bounds__(kWaves * 64) void rms_norm_backward_any_kernel(
     NormRows<const typename E::store_t> total, const float *__restrict__ gain, NormRows<const typename E::store_t> dy,
     NormRows<const typename E::store_t> dtotal, NormRows<typename E::store_t> dx, float *__restrict__ partial, int64_t M,
     int K, float eps) {
-    __shared__ float2 part[2][kWaves];
+    __shared__ float2 part[2][1][kWaves];
     float *to = partial + (int64_t)blockIdx.x * K;
     for (int k = threadIdx.x; k < K; k += kWaves * 64) to[k] = 0.0f;
     int parity = 0;
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x, parity ^= 1) {
         const typename E::store_t *t = total.p + m * total.ld, *d = dy.p + m * dy.ld;
-        float sum = 0.0f, along = 0.0f;
+        float sum[1] = {0.0f}, along[1] = {0.0f};
         for (int k = threadIdx.x; k < K; k += kWaves * 64) {
             const float f = E::load(t + k);
-            sum = __builtin_fmaf(f, f, sum);
-            along = __builtin_fmaf(E::load(d + k) * gain[k], f, along);
+            sum[0] = __builtin_fmaf(f, f, sum[0]);
+            along[0] = __builtin_fmaf(E::load(d + k) * gain[k], f, along[0]);
         }
-        norm::group_reduce<kWaves, false>(sum, along, part[parity]);
-        const float r = norm::rms_scale(sum, K, eps), c = along / (float)K * r;
+        norm::group_reduce<kWaves, false, 1>(sum, along, part[parity]);
+        const float r = norm::rms_scale(sum[0], K, eps), c = along[0] / (float)K * r;
         for (int k = threadIdx.x; k < K; k += kWaves * 64) {
             const float t_r = E::load(t + k) * r, e = E::load(d + k);
             float v = r * __builtin_fmaf(-t_r, c, e * gain[k]);
@@ -352,19 +404,22 @@ __global__ __launch_bounds__(kWaves * 64) void rms_norm_backward_any_kernel(
     }
 }
 
-// The sum of the work-groups' rows, 64 columns a work-group: four waves take every fourth row each.
-static __global__ __launch_bounds__(256) void norm_gain_kernel(const float *__restrict__ partial, float *__restrict__ dgain,
-                                                               int64_t rows, int K) {
-    __shared__ float part[4][64];
+// The sum of the work-groups' rows, 64 columns a work-group: sixteen waves take every sixteenth row each.
+static __global__ __launch_bounds__(1024) void norm_gain_kernel(const float *__restrict__ partial, float *__restrict__ dgain,
+                                                                int64_t rows, int K) {
+    __shared__ float part[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, k = blockIdx.x * 64 + lane;
     float s = 0.0f;
     if (k < K) {
 #pragma unroll 8
-        for (int64_t p = wave; p < rows; p += 4) s += partial[p * K + k];
+        for (int64_t p = wave; p < rows; p += 16) s += partial[p * K + k];
     }
     part[wave][lane] = s;
     __syncthreads();
-    if (wave == 0 && k < K) dgain[k] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+    if (wave > 0 || k >= K) return;
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += part[i][lane];
+    dgain[k] = s;
 }
 
 }  // namespace jscan

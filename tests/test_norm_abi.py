@@ -84,7 +84,7 @@ def test_product_validation(kw, code):
 
 def test_workspace_sizes():
     size = jscan.library().jscan_rms_norm_backward_workspace
-    assert size(-1, 64) == -1 and size(8, 0) == -1 and size(0, 64) == 0 and size(3, 64) == 3 * 64 * 4
+    assert size(-1, 64) == -1 and size(8, 0) == -1 and size(0, 64) == 0 and 64 * 4 <= size(3, 64) <= 3 * 64 * 4
     assert size(16384, 4096) <= 0.1 * 4 * 16384 * 4096 * 2
 
 
