@@ -8,6 +8,8 @@
 // scales, the bias, an activation and a residual are applied in fp32 before the one rounding to the output type.
 #pragma once
 
+#include <type_traits>
+
 #include "activation.h"
 #include "mfma_common.h"
 
@@ -223,7 +225,9 @@ __device__ __forceinline__ void store_rows(T *out, const int8_t *lds, int l, int
 }
 
 // What the product adds to its results: an activation of the scaled sum with its bias, then a residual of the
-// output's type, rows ld elements apart (NULL: none).
+// output's type, rows ld elements apart.  Kernels come without either, with an activation, and with a residual (and any
+// activation), which takes registers of its own.
+enum class Finish : int { None, Activation, Residual };
 struct Epilogue {
     Act act;
     const void *residual;
@@ -231,7 +235,7 @@ struct Epilogue {
 };
 
 // The same 16 rows of the residual on their way to LDS, 16 bytes a lane at a time from any address, through
-// registers: the next rows' are loaded while one set of rows is computed.
+// registers.
 template <typename E, int kCols, int kRow> struct ResidualRows {
     using T = typename E::store_t;
     typedef uint32_t piece __attribute__((ext_vector_type(4), aligned(2)));   // any element
@@ -319,7 +323,7 @@ constexpr int waves_per_simd(int waves, int lds_bytes) {
     return n < 1 ? 1 : n > 8 ? 8 : n;
 }
 
-template <typename E, int BM, int BN, int WR, int WC, int KG, int kBufs, bool kEpilogue>
+template <typename E, int BM, int BN, int WR, int WC, int KG, int kBufs, Finish F>
 __global__ __launch_bounds__(KG * WR * WC * 64,
                              waves_per_simd(KG * WR * WC, KG * kBufs * (BM + BN) * 128)) void matmul_i8_tiled_kernel(
     const int8_t *__restrict__ q, const float *__restrict__ sq, const int8_t *__restrict__ w,
@@ -457,33 +461,44 @@ __global__ __launch_bounds__(KG * WR * WC * 64,
     int8_t *mine = &stages_of[0][0][0] + wave * 16 * kRow;
     const int64_t nw = n0 + wc * kCols;
     const Columns<4 * NT> col(sw, bias, min(nw + g4 * 4 * NT, N - 1), N);
-    ResidualRows<E, kCols, kRow> rest;
-    const bool adds = kEpilogue && ep.residual != nullptr;
-    if (adds) rest.load(ep, l, m0 + wr * 16 * MT, nw, M, N);
+    constexpr bool adds = F == Finish::Residual;
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
         const int64_t mu = m0 + wr * 16 * MT + 16 * u;
         const float s = sq[min(mu + r16, M - 1)];
-        if (adds) {
+        if constexpr (adds) {
+            // loaded here and not ahead, which takes registers that sixteen waves do not have (16384 x 16384 x 4096 1115
+            // us, so 1060; plain 954)
+            ResidualRows<E, kCols, kRow> rest;
+            rest.load(ep, l, mu, nw, M, N);
             rest.to_lds(mine, l);
-            if (u + 1 < MT) rest.load(ep, l, mu + 16, nw, M, N);
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         }
+        auto finish = [&](auto activation) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float v[4];
+            for (int t = 0; t < NT; ++t) {
+                float v[4], r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                T *place = reinterpret_cast<T *>(mine + r16 * kRow) + g4 * 4 * NT + 4 * t;
+                if constexpr (adds) Results<E>::load4(place, r);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = col(acc[t][u][i], s, 4 * t + i);
-            T *place = reinterpret_cast<T *>(mine + r16 * kRow) + g4 * 4 * NT + 4 * t;
-            if constexpr (kEpilogue) {
-                float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (adds) Results<E>::load4(place, r);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = activate(v[i], ep.act) + r[i];
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = activation(col(acc[t][u][i], s, 4 * t + i));
+                    if constexpr (adds) v[i] += r[i];
+                }
+                Results<E>::store4(place, v);
             }
-            Results<E>::store4(place, v);
+        };
+        // Without a residual, one branch on the activation for all results of the rows (us, 65536 x 2048 x 4096 silu 501,
+        // with a branch for each result 507); beside a residual's registers it spills (577, so 541).
+        if constexpr (F == Finish::None) {
+            finish([](float v) { return v; });
+        } else if constexpr (F == Finish::Activation) {
+            if (ep.act == Act::Silu) finish([](float v) { return activate<Act::Silu>(v); });
+            else finish([](float v) { return activate<Act::GeluTanh>(v); });
+        } else {
+            finish([&](float v) { return activate(v, ep.act); });
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();

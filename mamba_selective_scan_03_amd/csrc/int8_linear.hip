@@ -94,31 +94,31 @@ struct MatmulArgs {
     jscan::Epilogue epilogue;
 };
 
-template <typename E, bool kEpilogue, int BM, int BN, int WR, int WC, int KG, int kBufs>
+template <typename E, jscan::Finish F, int BM, int BN, int WR, int WC, int KG, int kBufs>
 void launch_tiled(const MatmulArgs &a) {
     using T = typename E::store_t;
     const int m_tiles = (int)((a.M + BM - 1) / BM), n_tiles = (int)((a.N + BN - 1) / BN);
     // the widest store that every output row starts on
     const uint64_t start = reinterpret_cast<uint64_t>(a.out) | (uint64_t)(a.ld_out * (int64_t)sizeof(T));
     const int wide = start % 16 == 0 ? 16 : start % 4 == 0 ? 4 : 2;
-    hipLaunchKernelGGL((jscan::matmul_i8_tiled_kernel<E, BM, BN, WR, WC, KG, kBufs, kEpilogue>),
+    hipLaunchKernelGGL((jscan::matmul_i8_tiled_kernel<E, BM, BN, WR, WC, KG, kBufs, F>),
                        dim3((unsigned)((int64_t)m_tiles * n_tiles)), dim3(KG * WR * WC * 64), 0, a.stream, a.q, a.sq,
                        a.w, a.sw, a.bias, static_cast<T *>(a.out), a.M, a.N, a.K, a.ld_out, m_tiles, n_tiles, wide,
                        a.epilogue);
 }
 
-template <typename E, bool kEpilogue> void launch_matmul(const MatmulArgs &a) {
+template <typename E, jscan::Finish F> void launch_matmul(const MatmulArgs &a) {
     switch (choose_tile(a.M, a.N, a.K)) {
-    case 0: launch_tiled<E, kEpilogue, 16, 16, 1, 1, 8, 3>(a); break;
-    case 1: launch_tiled<E, kEpilogue, 16, 32, 1, 2, 4, 3>(a); break;
-    case 2: launch_tiled<E, kEpilogue, 32, 32, 2, 1, 4, 4>(a); break;
-    case 3: launch_tiled<E, kEpilogue, 64, 32, 2, 1, 4, 3>(a); break;
-    case 4: launch_tiled<E, kEpilogue, 64, 64, 2, 2, 2, 3>(a); break;
-    case 5: launch_tiled<E, kEpilogue, 64, 64, 2, 2, 1, 3>(a); break;
-    case 6: launch_tiled<E, kEpilogue, 64, 128, 2, 2, 1, 3>(a); break;
-    case 7: launch_tiled<E, kEpilogue, 128, 128, 2, 4, 1, 2>(a); break;
-    case 8: launch_tiled<E, kEpilogue, 128, 144, 4, 1, 1, 2>(a); break;
-    default: launch_tiled<E, kEpilogue, 256, 256, 4, 4, 1, 2>(a); break;
+    case 0: launch_tiled<E, F, 16, 16, 1, 1, 8, 3>(a); break;
+    case 1: launch_tiled<E, F, 16, 32, 1, 2, 4, 3>(a); break;
+    case 2: launch_tiled<E, F, 32, 32, 2, 1, 4, 4>(a); break;
+    case 3: launch_tiled<E, F, 64, 32, 2, 1, 4, 3>(a); break;
+    case 4: launch_tiled<E, F, 64, 64, 2, 2, 2, 3>(a); break;
+    case 5: launch_tiled<E, F, 64, 64, 2, 2, 1, 3>(a); break;
+    case 6: launch_tiled<E, F, 64, 128, 2, 2, 1, 3>(a); break;
+    case 7: launch_tiled<E, F, 128, 128, 2, 4, 1, 2>(a); break;
+    case 8: launch_tiled<E, F, 128, 144, 4, 1, 1, 2>(a); break;
+    default: launch_tiled<E, F, 256, 256, 4, 4, 1, 2>(a); break;
     }
 }
 
@@ -151,11 +151,14 @@ jscan_status matmul_impl(const int8_t *q, const float *q_scale, const int8_t *w,
                                                                : jscan::Act::None;
     const MatmulArgs a{q, q_scale, w, w_scale, bias, out, M, N, K, ld_out, static_cast<hipStream_t>(stream),
                        jscan::Epilogue{act, residual, ld_residual}};
-    const bool plain = activation == JSCAN_ACT_NONE && !residual;
-    if (dtype == JSCAN_BF16 && plain) launch_matmul<jscan::BF16, false>(a);
-    else if (dtype == JSCAN_BF16) launch_matmul<jscan::BF16, true>(a);
-    else if (plain) launch_matmul<jscan::F32, false>(a);
-    else launch_matmul<jscan::F32, true>(a);
+    auto launch = [&](auto e) {
+        using E = decltype(e);
+        if (residual) launch_matmul<E, jscan::Finish::Residual>(a);
+        else if (act != jscan::Act::None) launch_matmul<E, jscan::Finish::Activation>(a);
+        else launch_matmul<E, jscan::Finish::None>(a);
+    };
+    if (dtype == JSCAN_BF16) launch(jscan::BF16{});
+    else launch(jscan::F32{});
     return launch_status();
 }
 
