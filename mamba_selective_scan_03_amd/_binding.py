@@ -1026,9 +1026,12 @@ def _check_conv(x, w, bias, state, lengths):
         _bad(f"w must be [D, W] with W = 2, 3 or 4, got {tuple(w.shape)}")
     W = w.shape[1]
     _check_flat("w", w, (D, W), _F32, dev)
-    _check_flat("bias", bias, (D,), _F32, dev)
-    _check_flat("state", state, (batch, W - 1, D), x.dtype, dev)
-    _check_flat("lengths", lengths, (batch,), _I32, dev)
+    if bias is not None:
+        _check_flat("bias", bias, (D,), _F32, dev)
+    if state is not None:
+        _check_flat("state", state, (batch, W - 1, D), x.dtype, dev)
+    if lengths is not None:
+        _check_flat("lengths", lengths, (batch,), _I32, dev)
     return W
 
 
@@ -1040,7 +1043,8 @@ def causal_conv(x, w, bias=None, state=None, lengths=None, activation="silu", y=
     ``lengths`` int32 ``[batch]`` for padded sequences (y is zero in the padding).  Returns ``(y, state_out)``:
     ``state_out`` holds each sequence's last W - 1 tokens, for the next call or :func:`causal_conv_step`, and may be
     ``state`` itself.  Autograd does not record the call (:func:`causal_conv_backward` has its gradients)."""
-    if x.requires_grad or any(t is not None and t.requires_grad for t in (w, bias, state)):
+    if x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or \
+            (state is not None and state.requires_grad):
         _refuse_grad()
     code = _conv_activation(activation)
     W = _check_conv(x, w, bias, state, lengths)

@@ -247,9 +247,9 @@ jscan_status jscan_causal_conv_backward(const void *x, const void *state, const 
         if (launch_status() != JSCAN_OK) return JSCAN_ERR_HIP;
     }
     const dim3 grid((unsigned)((D + 63) / 64), (unsigned)(W + 1));
-    if (W == 2) hipLaunchKernelGGL(jscan::conv_sum_kernel<2>, grid, dim3(256), 0, a.stream, a.partial, dw, dbias, shares, (int)D);
-    else if (W == 3) hipLaunchKernelGGL(jscan::conv_sum_kernel<3>, grid, dim3(256), 0, a.stream, a.partial, dw, dbias, shares, (int)D);
-    else hipLaunchKernelGGL(jscan::conv_sum_kernel<4>, grid, dim3(256), 0, a.stream, a.partial, dw, dbias, shares, (int)D);
+    if (W == 2) hipLaunchKernelGGL(jscan::conv_sum_kernel<2>, grid, dim3(1024), 0, a.stream, a.partial, dw, dbias, shares, (int)D);
+    else if (W == 3) hipLaunchKernelGGL(jscan::conv_sum_kernel<3>, grid, dim3(1024), 0, a.stream, a.partial, dw, dbias, shares, (int)D);
+    else hipLaunchKernelGGL(jscan::conv_sum_kernel<4>, grid, dim3(1024), 0, a.stream, a.partial, dw, dbias, shares, (int)D);
     return launch_status();
 }
 

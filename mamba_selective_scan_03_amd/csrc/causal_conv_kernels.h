@@ -345,23 +345,24 @@ __global__ __launch_bounds__(conv::kThreads) void causal_conv_backward_kernel(
     }
 }
 
-// The sums of the work-groups' shares, 64 channels of one tap (or of the bias) a work-group: four waves take
-// every fourth share each.
+// The sums of the work-groups' shares, 64 channels of one tap (or of the bias) a work-group: sixteen waves take every
+// sixteenth share each.
 template <int W>
-__global__ __launch_bounds__(256) void conv_sum_kernel(const float *__restrict__ partial, float *__restrict__ dw,
-                                                       float *__restrict__ dbias, int64_t shares, int D) {
-    __shared__ float part[4][64];
+__global__ __launch_bounds__(1024) void conv_sum_kernel(const float *__restrict__ partial, float *__restrict__ dw,
+                                                        float *__restrict__ dbias, int64_t shares, int D) {
+    __shared__ float part[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, k = blockIdx.y;
     const int d = blockIdx.x * 64 + lane;
     float s = 0.0f;
     if (d < D) {
 #pragma unroll 8
-        for (int64_t p = wave; p < shares; p += 4) s += partial[(p * (W + 1) + k) * D + d];
+        for (int64_t p = wave; p < shares; p += 16) s += partial[(p * (W + 1) + k) * D + d];
     }
     part[wave][lane] = s;
     __syncthreads();
     if (wave > 0 || d >= D) return;
-    s = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += part[i][lane];
     if (k < W) dw[(int64_t)d * W + k] = s;
     else if (dbias) dbias[d] = s;
 }
