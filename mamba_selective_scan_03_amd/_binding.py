@@ -1234,7 +1234,7 @@ def rms_norm_backward(total, gain, dy, dtotal=None, eps=1e-6, dx=None, dgain=Non
     """Gradients of :func:`rms_norm` (``jscan_rms_norm_backward``) from its ``total`` (x where there was no residual): dy
     the gradient of y, dtotal that of total's other uses (None: zeros).  Returns ``(dx, dgain)``: dx the gradient of
     x and of residual alike, in their dtype; dgain ``[K]`` fp32.  A given ``dx`` may be dtotal itself."""
-    if any(t is not None and t.requires_grad for t in (total, gain, dy, dtotal)):
+    if total.requires_grad or gain.requires_grad or dy.requires_grad or (dtotal is not None and dtotal.requires_grad):
         _refuse_grad()
     K, lead = _check_norm(total, gain, "total")
     dev, M = total.device, lead.numel()

@@ -28,8 +28,10 @@ constexpr int64_t kMostGroups = (int64_t)1 << 20;   // of a launch
 // Work-groups of the forward call: a row each, more only beyond the largest launch.
 int64_t forward_groups(int64_t M) { return M < kMostGroups ? M : kMostGroups; }
 
-// Work-groups of the backward pass, each of which goes on to further rows and leaves a share of the gain's gradient.
+// Work-groups of the backward pass, each of which goes on to further rows and leaves a share of the gain's gradient; one
+// for a few rows, which writes that gradient itself (a second launch takes longer than they do).
 int64_t backward_groups(const Layout &l, int64_t M) {
+    if (M <= 8) return M > 0 ? 1 : 0;
     const int64_t each = l.chunks == 0 ? 1 : jscan::norm::rows_at_once(l.waves, l.chunks);
     const int64_t most = l.waves == 1 ? 1024 : l.waves == 4 ? 512 : 256;   // four, eight, sixteen waves a CU
     const int64_t rows = (M + each - 1) / each;
@@ -180,7 +182,7 @@ jscan_status jscan_rms_norm_quantize(const void *x, const void *residual, const 
 int64_t jscan_rms_norm_backward_workspace(int64_t M, int64_t K) {
     if (!sizes_ok(M, K, 0.0f)) return -1;
     const int64_t a = backward_groups(layout_for(K, 2), M), b = backward_groups(layout_for(K, 4), M);
-    return (a > b ? a : b) * K * 4;
+    return M <= 8 ? 0 : (a > b ? a : b) * K * 4;
 }
 
 jscan_status jscan_rms_norm_backward(const void *total, const float *gain, const void *dy, const void *dtotal, void *dx,
@@ -210,11 +212,13 @@ jscan_status jscan_rms_norm_backward(const void *total, const float *gain, const
     if (M > 0) {
         const Layout l = layout_for(K, es);
         a.groups = backward_groups(l, M);
+        if (a.groups == 1) a.partial = dgain;
         with_layout(l, [&](auto w, auto c) {
             if (dtype == JSCAN_BF16) launch_backward<jscan::BF16, decltype(w)::value, decltype(c)::value>(a);
             else launch_backward<jscan::F32, decltype(w)::value, decltype(c)::value>(a);
         });
         if (launch_status() != JSCAN_OK) return JSCAN_ERR_HIP;
+        if (a.groups == 1) return JSCAN_OK;
     }
     hipLaunchKernelGGL(jscan::norm_gain_kernel, dim3((unsigned)((K + 63) / 64)), dim3(1024), 0, a.stream, a.partial, dgain,
                        a.groups, (int)K);

@@ -362,7 +362,16 @@ __global__ __launch_bounds__(kWaves * 64) void rms_norm_backward_kernel(
                     o[i] = kAdd ? v + o[i] : v;
                     dg[j][i] = __builtin_fmaf(e[i], t_r, dg[j][i]);
                 }
-                norm::store<E, kNt>(dx.p + m * dx.ld + at.at[j], P::pack(o));
+                typename E::store_t *to = dx.p + m * dx.ld + at.at[j];
+                if (kAgain && j == kChunks - 1 && at.lo > 0) {
+                    // where dx is dtotal and rows are read again, the repeated elements may hold their gradient
+                    // already: only the thread that counts an element writes it
+#pragma unroll
+                    for (int i = 0; i < n; ++i)
+                        if (i >= at.lo) E::store(to + i, o[i]);
+                } else {
+                    norm::store<E, kNt>(to, P::pack(o));
+                }
             }
         }
     }

@@ -148,6 +148,19 @@ def test_in_place(K, dtype):
     assert dx2 is d and same(d, dx) and same(dgain, dgain2)
 
 
+@pytest.mark.parametrize("K", [16385, 16391, 16897, 24577, 24583])
+def test_gradient_added_into_where_long_rows_are_read_again(K):
+    """The last piece of such a row reaches back over elements that other threads have written already."""
+    M = 600
+    gain = (1 + 0.3 * normal(3, K)).cuda()
+    total, dy, dtotal = (normal(i, M, K).to(torch.bfloat16).cuda() for i in (1, 2, 4))
+    dx, dgain = jscan.rms_norm_backward(total, gain, dy, dtotal=dtotal)
+    for _ in range(3):
+        d = dtotal.clone()
+        dx2, dgain2 = jscan.rms_norm_backward(total, gain, dy, dtotal=d, dx=d)
+        assert dx2 is d and same(d, dx) and same(dgain, dgain2)
+
+
 @pytest.mark.parametrize("K", [48, 4096, 65536])
 def test_special_rows(K):
     M = 8
