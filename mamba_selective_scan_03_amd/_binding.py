@@ -931,33 +931,42 @@ def prefill_gate(x, delta, A, B, C, skip=None, z=None, h0=None, form="diagonal",
     ``form`` has it.  ``chunk`` None scans token by token (h_final is bit for bit :func:`prefill`'s); a segment length, or 0
     for an automatic one, scans as :func:`prefill_chunked` does (form "diagonal"; the others take 0 as None), with a
     ``workspace`` of :func:`chunked_workspace_bytes` or one that is allocated.  Autograd does not record the call."""
-    if any(t is not None and t.requires_grad for t in (x, delta, A, B, C, skip, z, h0)):
+    if x.requires_grad or delta.requires_grad or A.requires_grad or B.requires_grad or C.requires_grad or \
+            any(t is not None and t.requires_grad for t in (skip, z, h0)):
         _refuse_grad()
     code = A_FORMS.get(form)
     if code is None:
         _bad(f"form must be one of {tuple(A_FORMS)}")
-    batch, L, D = _check_prefill_args(x, delta, A, B, C, h0, scalar_a=form == "scalar")
+    if not x.is_cuda or x.dtype not in _DTYPES or x.dim() != 3 or not x.is_contiguous():
+        _bad("x must be a contiguous bfloat16 or float32 [batch, L, D] CUDA tensor")
+    shape, dev, dtype = x.shape, x.device, x.dtype
+    batch, L, D = shape
+    pairs = (batch, L, D_STATE)
+    _check_flat("delta", delta, shape, dtype, dev)
+    _check_flat("A", A, (D,) if form == "scalar" else (D, D_STATE), _F32, dev)
+    _check_flat("B", B, pairs, dtype, dev)
+    _check_flat("C", C, pairs, dtype, dev)
     if skip is None and z is None:
         _bad("skip or z is needed (prefill has neither)")
     if chunk is not None and chunk < 0:
         _bad("chunk must be None, 0 or a segment length")
-    dev = x.device
     _check_flat("skip", skip, (D,), _F32, dev)
-    ld_z = D if z is None else _token_rows("z", z, x, x.shape)
+    ld_z = D if z is None else _token_rows("z", z, x, shape)
     if y is None:
         y = torch.empty_like(x)
     else:
-        _check_flat("y", y, x.shape, x.dtype, dev)
+        _check_flat("y", y, shape, dtype, dev)
     state = (batch, D, D_STATE)
+    _check_flat("h0", h0, state, _F32, dev)
     if h_final is None:
-        h_final = torch.empty(state, dtype=_F32, device=dev)
+        h_final = torch.empty(batch, D, D_STATE, dtype=_F32, device=dev)
     else:
         _check_flat("h_final", h_final, state, _F32, dev)
     cut = chunk is not None and form == "diagonal"
     workspace, ws_bytes = _workspace(workspace, chunked_workspace_bytes(batch, L, D, chunk) if cut else 0, dev)
     _launch("jscan_prefill_gate", dev, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(h0),
             _addr(skip), _addr(z), y.data_ptr(), h_final.data_ptr(), batch, L, D, D_STATE, ld_z, -1 if chunk is None else chunk,
-            _addr(workspace), ws_bytes, code, _DTYPES[x.dtype])
+            _addr(workspace), ws_bytes, code, _DTYPES[dtype])
     return y, h_final
 
 
@@ -965,7 +974,8 @@ def step_gate(h, x_t, delta_t, A, B_t, C_t, skip=None, z_t=None, form="diagonal"
     """One decode token of :func:`prefill_gate` (``jscan_step_gate``): h ``[batch, D, 16]`` fp32 in place; x_t, delta_t
     and z_t ``[batch, D]``, B_t and C_t ``[batch, 16]`` (rows may be strided, x_t's and delta_t's alike and B_t's and C_t's
     alike).  Returns y_t ``[batch, D]``: a new contiguous tensor, or the given ``y_t``, whose rows may be strided too."""
-    if any(t is not None and t.requires_grad for t in (h, x_t, delta_t, A, B_t, C_t, skip, z_t)):
+    if h.requires_grad or x_t.requires_grad or delta_t.requires_grad or A.requires_grad or B_t.requires_grad or \
+            C_t.requires_grad or (skip is not None and skip.requires_grad) or (z_t is not None and z_t.requires_grad):
         _refuse_grad()
     code = A_FORMS.get(form)
     if code is None:
