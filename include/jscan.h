@@ -612,15 +612,16 @@ jscan_status jscan_causal_conv_step(void *state, const void *x_t, const float *w
 /*
  * The selective scan with what follows it in its layer, the skip and the output gate, in one pass:
  *     y_t[d] = (sum_n C_t[n] h_t[d,n] + skip[d] x_t[d]) silu(z_t[d])
- * in fp32, rounded once.  skip or z may be NULL (its part is left out; not both).  h is the scan's, bit for bit.
+ * in fp32, rounded once.  skip or z may be NULL (its part is left out; not both).  h is the scan's, bit for bit (see chunk).
  *   skip      [D] fp32
  *   z         batch * L token rows of D values in `dtype`, row stride ld_z >= D (a multiple of 8, at most 2^25), in the
  *             order of x's rows: z may be a half of a wider projection
- *   chunk     -1: token by token (jscan_prefill_resume, or the prefill of a_form); 0 or more: time-parallel as
- *             jscan_prefill_chunked (0 = automatic), for JSCAN_A_DIAGONAL; for the other forms 0 is
- *             token by token and a given length is JSCAN_ERR_FORM
- *   workspace jscan_prefill_chunked_workspace(batch, L, D, N, chunk) bytes where chunk >= 0 and a_form is
- *             JSCAN_A_DIAGONAL; else it may be NULL
+ *   chunk     -1: token by token (h is jscan_prefill_resume's, or that of a_form's prefill); above 0: in segments
+ *             of that many tokens (h is jscan_prefill_chunked's); 0: whichever way is expected to be fastest for this
+ *             shape.  Segments are for JSCAN_A_DIAGONAL: for the other forms 0 is token by token and a given
+ *             length is JSCAN_ERR_FORM
+ *   workspace jscan_prefill_gate_workspace(batch, L, D, N, chunk) bytes where a_form is JSCAN_A_DIAGONAL; else, and
+ *             where that is 0, it may be NULL
  *   h0        [batch][D][N] fp32 or NULL for zeros; may equal h_final
  * The other arguments and the errors are those of jscan_prefill_chunked.
  */
@@ -629,6 +630,9 @@ jscan_status jscan_prefill_gate(const void *x, const void *delta, const float *A
                                 void *y, float *h_final, int64_t batch, int64_t L, int64_t D, int64_t N,
                                 int64_t ld_z, int64_t chunk, void *workspace, int64_t workspace_bytes,
                                 jscan_a_form a_form, jscan_dtype dtype, void *stream);
+
+/* Workspace bytes of jscan_prefill_gate for this shape, or -1 if the shape or chunk is invalid.  Host-only. */
+int64_t jscan_prefill_gate_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t chunk);
 
 /*
  * One decode token of it for a batch: jscan_step (or the step of a_form) with the skip and the gate.  z_t's rows

@@ -61,6 +61,7 @@ from ._binding import (  # noqa: F401
     prefill_complex,
     prefill_fused,
     prefill_gate,
+    prefill_gate_workspace_bytes,
     prefill_mimo,
     prefill_mimo_trapezoid,
     prefill_scalar_a,

@@ -92,6 +92,8 @@ def library():
     lib.jscan_rms_norm_backward_workspace.restype = i64
     lib.jscan_prefill_gate.argtypes = [vp, vp, fp, vp, vp, fp, fp, vp, vp, fp, i64, i64, i64, i64, i64, i64, vp, i64, i32,
                                        i32, vp]
+    lib.jscan_prefill_gate_workspace.argtypes = [i64, i64, i64, i64, i64]
+    lib.jscan_prefill_gate_workspace.restype = i64
     lib.jscan_step_gate.argtypes = [fp, vp, vp, fp, vp, vp, fp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i32, i32, vp]
     lib.jscan_prefill_chunked_workspace.restype = i64
     for f in (lib.jscan_prefill, lib.jscan_prefill_resume, lib.jscan_step, lib.jscan_prefill_chunked,
@@ -923,14 +925,22 @@ def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
 # ---- scan with skip and output gate ----------------------------------------------------------
 
 
+def prefill_gate_workspace_bytes(batch: int, L: int, D: int, chunk: int = 0) -> int:
+    """Bytes of workspace ``prefill_gate`` needs (0 when it runs token by token)."""
+    n = library().jscan_prefill_gate_workspace(batch, L, D, D_STATE, chunk)
+    if n < 0:
+        raise ValueError(f"invalid shape or chunk: batch={batch} L={L} D={D} chunk={chunk}")
+    return n
+
+
 def prefill_gate(x, delta, A, B, C, skip=None, z=None, h0=None, form="diagonal", chunk=None, y=None, h_final=None,
                  workspace=None):
     """Selective scan with its skip and output gate in one pass (``jscan_prefill_gate``):
     ``y = (scan(x) + skip * x) * silu(z)``, with ``skip`` ``[D]`` fp32 and z ``[batch, L, D]`` in x's dtype (rows may be a
     half of a wider projection); either may be None.  Other arguments and results as for :func:`prefill`, A as the
-    ``form`` has it.  ``chunk`` None scans token by token (h_final is bit for bit :func:`prefill`'s); a segment length, or 0
-    for an automatic one, scans as :func:`prefill_chunked` does (form "diagonal"; the others take 0 as None), with a
-    ``workspace`` of :func:`chunked_workspace_bytes` or one that is allocated.  Autograd does not record the call."""
+    ``form`` has it.  ``chunk`` None scans token by token (h_final is bit for bit :func:`prefill`'s), a segment length as
+    :func:`prefill_chunked` does, and 0 whichever way is expected to be fastest (form "diagonal"; the others take 0 as None);
+    ``workspace`` of :func:`prefill_gate_workspace_bytes`, or one is allocated.  Autograd does not record the call."""
     if x.requires_grad or delta.requires_grad or A.requires_grad or B.requires_grad or C.requires_grad or \
             any(t is not None and t.requires_grad for t in (skip, z, h0)):
         _refuse_grad()
@@ -963,7 +973,7 @@ def prefill_gate(x, delta, A, B, C, skip=None, z=None, h0=None, form="diagonal",
     else:
         _check_flat("h_final", h_final, state, _F32, dev)
     cut = chunk is not None and form == "diagonal"
-    workspace, ws_bytes = _workspace(workspace, chunked_workspace_bytes(batch, L, D, chunk) if cut else 0, dev)
+    workspace, ws_bytes = _workspace(workspace, prefill_gate_workspace_bytes(batch, L, D, chunk) if cut else 0, dev)
     _launch("jscan_prefill_gate", dev, x.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(h0),
             _addr(skip), _addr(z), y.data_ptr(), h_final.data_ptr(), batch, L, D, D_STATE, ld_z, -1 if chunk is None else chunk,
             _addr(workspace), ws_bytes, code, _DTYPES[dtype])

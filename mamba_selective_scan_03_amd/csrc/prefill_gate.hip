@@ -11,7 +11,54 @@ using jscan::OutGate;
 
 namespace {
 
+// Whether the launches of a plan can be counted.
+bool gate_grids_fit(int64_t batch, int64_t D, const ChunkPlan &p) {
+    const int64_t pairs = (batch * D * JSCAN_D_STATE + jscan::carry::kPairs - 1) / jscan::carry::kPairs;
+    return chunk_grids_fit(batch, D, p) && batch * p.n_seg * ((D + 255) / 256) * 256 <= kMaxItems &&
+           pairs * jscan::carry::kThreads <= kMaxItems;
+}
+
 constexpr int64_t kMostGateStride = (int64_t)1 << 25;   // elements between rows of z (32-bit byte offsets of 8 rows)
+
+// How an automatic call scans: the way that is expected to take least, token by token or in segments of seg_len tokens.
+// Times in us, from one GPU of 256 CUs (bf16; fp32 takes much the same):
+//     rows kernel    a work-group a CU at a time, each 8 and 0.028 a token       (1 x 65536 x 8192 1849, 8 x 639 x 416 25)
+//     lane kernel    0.65 a token for few waves, 0.58 more for a wave a SIMD     (3 x 688 x 144 453, 24 x 847 x 5704 1508)
+//     segments       15, a token of both passes 0.66 to 1.25 with one to four waves a SIMD, which is what fits at a
+//                    time, and 700 bytes for a channel's states and A in each,
+//                    0.002 a channel more where the segments are more than 16    (1 x 65536 x 1024 in 256 345, in 512 384;
+//                    1 x 3932 x 32 in 16 26, in 256 179; 1 x 8192 x 1024 in 64 77; 24 x 847 x 5704 in 384 972)
+// Over 21 shapes the choice is at most 1.25 times the best segment length tried.  jscan_prefill_chunked's own rule
+// (segments of 256 tokens and more wherever channels are fewer than 8192) takes 220 us for 1 x 3932 x 32, 163 for 1 x
+// 8192 x 1024, and 165 for 1 x 512 x 4096, which takes 21 token by token.
+ChunkPlan plan_automatic(int64_t batch, int64_t L, int64_t D) {
+    const float channels = (float)batch * (float)D, tokens = (float)L;
+    float least;
+    if (jscan::rows_kernel_applies(batch, D)) {
+        const int64_t groups = batch * (D / jscan::rows::kCh);
+        least = (float)((groups + 255) / 256) * (0.028f * tokens + 8.0f);
+        if (groups > 256) least *= 0.7f;   // left only for a clear gain: 13 x 95 x 5664 takes 58, in segments 240
+    } else {
+        const float waves = (float)(batch * ((D + 63) / 64)) / 1024.0f;   // a SIMD
+        const float token = 0.55f + 0.58f * waves;
+        least = 8.0f + tokens * (token > 0.65f ? token : 0.65f);
+    }
+    ChunkPlan best;
+    best.seg_len = L;
+    for (const int64_t seg : {16, 32, 48, 64, 96, 128, 192, 256, 384, 512, 768, 1024, 2048, 4096}) {
+        if (seg >= L) break;
+        ChunkPlan p;
+        p.seg_len = seg;
+        p.n_seg = (L + seg - 1) / seg;
+        if (!gate_grids_fit(batch, D, p)) continue;
+        const float waves = (float)(batch * p.n_seg * ((D + 255) / 256)) / 256.0f;   // a SIMD
+        const float token = waves <= 1.0f ? 0.66f : waves <= 2.0f ? 0.70f : 1.25f * __builtin_ceilf(waves / 4.0f);
+        const float carry = p.n_seg > jscan::carry::kGroups ? 2.0e-3f * channels : 0.0f;
+        const float us = 15.0f + token * (float)seg + channels * (float)p.n_seg * 700.0f / 5.0e6f + carry;
+        if (us < least) least = us, best = p;
+    }
+    return best;
+}
 
 struct GateArgs {
     const void *x, *delta;
@@ -136,6 +183,14 @@ jscan_status check_gate(const float *skip, const void *z, int64_t ld_z, const vo
 
 extern "C" {
 
+int64_t jscan_prefill_gate_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t chunk) {
+    if (batch < 0 || L < 0 || D < 0 || N != JSCAN_D_STATE || D % 8 != 0 || D > (1 << 24) || batch > (1 << 20) || chunk < -1)
+        return -1;
+    if (batch == 0 || L == 0 || D == 0 || chunk < 0) return 0;
+    const ChunkPlan p = chunk > 0 ? plan_chunks(batch, L, D, chunk) : plan_automatic(batch, L, D);
+    return p.n_seg > 1 && !gate_grids_fit(batch, D, p) ? -1 : chunk_workspace_bytes(p, batch, D);
+}
+
 jscan_status jscan_prefill_gate(const void *x, const void *delta, const float *A, const void *B, const void *C,
                                 const float *h0, const float *skip, const void *z, void *y, float *h_final, int64_t batch,
                                 int64_t L, int64_t D, int64_t N, int64_t ld_z, int64_t chunk, void *workspace,
@@ -164,15 +219,12 @@ jscan_status jscan_prefill_gate(const void *x, const void *delta, const float *A
         return launch_status();
     }
     ChunkPlan p;
-    if (chunk >= 0 && af == AForm::Diagonal) p = plan_chunks(batch, L, D, chunk);
+    if (af == AForm::Diagonal && chunk >= 0) p = chunk > 0 ? plan_chunks(batch, L, D, chunk) : plan_automatic(batch, L, D);
     if (p.n_seg <= 1) {
         dispatch(dtype, af, [&](auto e, auto f) { launch_prefill<decltype(e), (AForm)decltype(f)::value>(a); });
         return launch_status();
     }
-    const int64_t pairs = (batch * D * N + jscan::carry::kPairs - 1) / jscan::carry::kPairs;
-    if (!chunk_grids_fit(batch, D, p) || batch * p.n_seg * ((D + 255) / 256) * 256 > kMaxItems ||
-        pairs * jscan::carry::kThreads > kMaxItems)
-        return JSCAN_ERR_SHAPE;
+    if (!gate_grids_fit(batch, D, p)) return JSCAN_ERR_SHAPE;
     const int64_t need = chunk_workspace_bytes(p, batch, D);
     if (!workspace) return JSCAN_ERR_NULL;
     if (workspace_bytes < need) return JSCAN_ERR_WORKSPACE;

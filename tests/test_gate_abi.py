@@ -51,6 +51,18 @@ def test_step_validation(kw, code):
     assert step(**kw) == code
 
 
+def test_workspace_sizes():
+    size = jscan.library().jscan_prefill_gate_workspace
+    assert size(1, 100, 12, 16, 0) == -1 and size(1, 100, 64, 8, 0) == -1 and size(1, 100, 64, 16, -2) == -1 and size(-1, 9, 64, 16, 0) == -1
+    assert size(1, 4096, 64, 16, -1) == 0 and size(0, 9, 64, 16, 0) == 0 and size(1, 1, 64, 16, 0) == 0
+    assert size(1, 65536, 8192, 16, 0) == 0                     # enough channels to go token by token
+    assert size(1, 4096, 64, 16, 256) == jscan.library().jscan_prefill_chunked_workspace(1, 4096, 64, 16, 256) > 0
+    assert size(1, 65536, 1024, 16, 0) > 0 and size(1, 3932, 32, 16, 0) > 0
+    # the limits: a plan that can be launched, or none
+    for shape in ((1 << 20, 1000, 8), (1, (1 << 31) - 1, 8), (64, 1 << 20, 1 << 20), (1 << 20, 4096, 1 << 10)):
+        assert size(*shape, 16, 0) >= 0
+
+
 X, A, B, H = torch.zeros(2, 4, 8), torch.zeros(8, 16), torch.zeros(2, 4, 16), torch.zeros(2, 8, 16)
 V = torch.zeros(8)
 

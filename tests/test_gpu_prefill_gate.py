@@ -81,14 +81,21 @@ def test_token_by_token(batch, L, D, dtype, form):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("batch,L,D,chunk", [(1, 1000, 64, 100), (2, 513, 40, 64), (1, 2048, 96, 0), (3, 777, 8, 0), (1, 300, 8192, 0),
+@pytest.mark.parametrize("batch,L,D,chunk", [(1, 1000, 64, 100), (2, 513, 40, 64), (1, 2048, 96, 0), (3, 777, 8, 0), (1, 300, 8192, 0), (1, 17, 40, 0),
+                                             (2, 3000, 24, 0), (1, 1, 8, 0), (5, 130, 1000, 0),
                                              (1, 1100, 264, 333), (2, 40, 32, 16)])
 def test_time_parallel(batch, L, D, chunk, dtype):
     c = inputs(batch, L, D, dtype, seed=L)
     out, h = jscan.prefill_gate(c["x"], c["delta"], c["A"], c["B"], c["C"], skip=c["skip"], z=c["z"], h0=c["h0"], chunk=chunk)
-    y, h_ref = plain(c, "diagonal", chunk)
-    assert torch.equal(bits(h), bits(h_ref))
-    assert_gated(out, y, c["x"], c["skip"], c["z"], "segments")
+    if chunk:
+        y, h_ref = plain(c, "diagonal", chunk)
+        assert torch.equal(bits(h), bits(h_ref))
+        assert_gated(out, y, c["x"], c["skip"], c["z"], "segments")
+    else:   # segments of the call's own choice, or none
+        y_ref, h_ref = oracle.prefill(*(c[k].cpu() for k in ("x", "delta", "A", "B", "C")), h0=c["h0"].cpu())
+        want = (y_ref + f64(c["skip"]) * f64(c["x"])) * O.activate(f64(c["z"]), "silu")
+        assert_parity(f64(out), want, DT[dtype], "automatic")
+        assert_parity(f64(h), h_ref, torch.float32, "state")
     for form in ("scalar", "complex"):   # automatic is token by token there
         c = inputs(batch, 130, 32, dtype, form, seed=L)
         a = jscan.prefill_gate(c["x"], c["delta"], c["A"], c["B"], c["C"], skip=c["skip"], z=c["z"], form=form, chunk=0)
@@ -174,7 +181,7 @@ def test_special_values_stay_in_their_channel():
 @pytest.mark.parametrize("D,chunk", [(64, None), (64, 0), (40, None)])
 def test_captured_and_replayed_and_on_another_stream(D, chunk):
     c = inputs(1, 1200, D, "bf16", seed=4)
-    n = jscan.chunked_workspace_bytes(1, 1200, D, 0)
+    n = jscan.prefill_gate_workspace_bytes(1, 1200, D, 0)
     ws = torch.empty(n, dtype=torch.uint8, device="cuda") if chunk is not None else None
     h = c["h0"].clone()
 
