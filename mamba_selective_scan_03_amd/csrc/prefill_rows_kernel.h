@@ -38,8 +38,7 @@
 // Modes (template parameters): delta computed on the load path from the low-rank projection
 // (kFused), the form of A (AF: diagonal, scaled identity, complex pairs), the skip and output gate
 // (kGate: the helper waves, which round y, have x and z of the same tokens at hand) and the
-// exponential-trapezoidal rule
-// (kTrap: the helper waves also stage the left-end weights and the previous token's B, and the
+// exponential-trapezoidal rule (kTrap: the helper waves also stage the left-end weights and the previous token's B, and the
 // scan lane takes the left end point in first, one more DPP-fused FMA per state element).
 #pragma once
 
