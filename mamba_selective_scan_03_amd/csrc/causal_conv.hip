@@ -14,8 +14,11 @@ constexpr int64_t kMostGroups = (int64_t)1 << 23;   // work-groups of one launch
 bool width_ok(int64_t W) { return W >= 2 && W <= 4; }
 bool activation_ok(jscan_activation a) { return a == JSCAN_ACT_NONE || a == JSCAN_ACT_SILU; }
 
-// Channels a thread takes: four, where a row has them.
+// Channels a thread takes: four, where a row has them; two in the backward pass of tensors that do not stream (us for four
+// with 1024 waves and two with 2048: 24 x 1000 x 500 bf16 27 and 24, 5 x 1001 x 1000 fp32 21 and 19, 1 x 16384 x 2048
+// bf16 53 and 50; 1 x 32768 x 2048, which streams, 82 and 103).
 int channels_of(int64_t D) { return D < 4 ? 1 : 4; }
+int backward_channels_of(int64_t D, bool streamed) { return D < 2 ? 1 : streamed ? 4 : 2; }
 
 // As long a run as leaves `least` waves, from 8 tokens to `most`; longer ones only where a launch could not count the
 // work-groups of one sequence.
@@ -34,24 +37,30 @@ jscan::conv::Split split_for(int64_t batch, int64_t L, int64_t D, int n, int64_t
 // Tensors beyond the last-level cache go by with the non-temporal hint (us, 8 x 4096 x 8192 bf16, without and with it:
 // forward 204 and 192, backward 329 and 298; from the cache the loads lose by it: 24 x 1000 x 500 11.6 and 14.8).
 constexpr int64_t kStreamBytes = (int64_t)256 << 20;
-bool streams(int64_t batch, int64_t L, int64_t D, int64_t es, int tensors, int n) {
-    return n > 1 && batch * L * D * es * tensors > kStreamBytes;
+bool streams(int64_t batch, int64_t L, int64_t D, int64_t es, int tensors) {
+    return D >= 4 && batch * L * D * es * tensors > kStreamBytes;
 }
 
 // Forward: runs of 64 tokens, 32 where the tensors stream (8 x 4096 x 8192: 204 us for 212; 1 x 32768 x 2048: 60 for 56).
 // Backward: a run computes W - 1 more tokens than it has, and its shares of the taps' gradients are written once (us
-// for 128 tokens, 256, 64: 8 x 4096 x 8192 329, 352, 378; with 1024 waves and with 2048: 24 x 1000 x 500 27 and 30,
-// 2 x 200 x 8192 14.3 and 15.4).
+// for 128 tokens, 256, 64: 8 x 4096 x 8192 329, 352, 378).
 constexpr int64_t kForwardWaves = 4096, kForwardRun = 64, kForwardStreamRun = 32;
-constexpr int64_t kBackwardWaves = 1024, kBackwardRun = 128;
+constexpr int64_t kBackwardWaves = 2048, kBackwardStreamWaves = 1024, kBackwardRun = 128;
 
-jscan::conv::Split backward_split(int64_t batch, int64_t L, int64_t D) {
-    return split_for(batch, L, D, channels_of(D), kBackwardWaves, kBackwardRun);
+jscan::conv::Split backward_split(int64_t batch, int64_t L, int64_t D, bool streamed) {
+    return split_for(batch, L, D, backward_channels_of(D, streamed), streamed ? kBackwardStreamWaves : kBackwardWaves,
+                     kBackwardRun);
 }
 
+// Room for the shares of either type: fp32 streams where bf16 does not.
 int64_t backward_workspace_bytes(int64_t batch, int64_t L, int64_t D, int64_t W) {
     if (batch == 0 || D == 0) return 0;
-    return batch * backward_split(batch, L, D).segs * (W + 1) * D * 4;
+    int64_t segs = backward_split(batch, L, D, false).segs;
+    if (D >= 4) {
+        const int64_t streamed = backward_split(batch, L, D, true).segs;
+        if (streamed > segs) segs = streamed;
+    }
+    return batch * segs * (W + 1) * D * 4;
 }
 
 struct ConvArgs {
@@ -101,11 +110,9 @@ template <typename E, int N, int W, Act A, bool kNt> void launch_forward(const C
     });
 }
 
-template <typename E, int N, int W, Act A, bool kNt> void launch_backward(const ConvArgs &a) {
+template <typename E, int N, int W, Act A> void launch_backward(const ConvArgs &a) {
     using T = typename E::store_t;
-    if constexpr (N > 1 && !kNt) {
-        if (a.streams) return launch_backward<E, N, W, A, true>(a);
-    }
+    constexpr bool kNt = N == 4;   // see backward_channels_of
     by_sequences(a, [&](int64_t b, dim3 grid) {
         hipLaunchKernelGGL((jscan::causal_conv_backward_kernel<E, N, W, A, kNt>), grid, dim3(jscan::conv::kThreads), 0,
                            a.stream, in_rows<T>(a.x, b * a.L), from<const T>(a.state, b * (W - 1) * a.D), a.w, a.bias,
@@ -116,8 +123,8 @@ template <typename E, int N, int W, Act A, bool kNt> void launch_backward(const 
     });
 }
 
-// Sequences a thread takes in a step: four where that leaves a wave for every SIMD (their taps are 80 bytes a thread, against 8
-// of each token).
+// Sequences a thread of the step takes: four where that leaves a wave for every SIMD (their taps are 40 bytes a thread, against
+// 4 of each token).  It takes two channels (us for four: 256 x 8192 bf16 6.9 and 7.7, fp32 14.4 and 14.6).
 constexpr int64_t kStepRows = 4, kStepWaves = 1024;
 
 template <typename E, int N, int W, Act A, int kRows>
@@ -141,7 +148,7 @@ void launch_step(void *state, const void *x, const float *w, const float *bias, 
     }
 }
 
-// Calls f<type, channels, width, activation>().
+// Calls f<type, channels, width, activation>(); channels is one of Ns.
 template <typename E, int N, int W, typename F> void with_activation(jscan_activation a, F f) {
     if (a == JSCAN_ACT_SILU) f(E{}, jscan::IntConst<N>{}, jscan::IntConst<W>{}, jscan::IntConst<(int)Act::Silu>{});
     else f(E{}, jscan::IntConst<N>{}, jscan::IntConst<W>{}, jscan::IntConst<(int)Act::None>{});
@@ -151,13 +158,12 @@ template <typename E, int N, typename F> void with_width(int64_t W, jscan_activa
     else if (W == 3) with_activation<E, N, 3>(a, f);
     else with_activation<E, N, 4>(a, f);
 }
-template <typename E, typename F> void with_channels(int n, int64_t W, jscan_activation a, F f) {
-    if (n == 4) with_width<E, 4>(W, a, f);
-    else with_width<E, 1>(W, a, f);
+template <typename E, int... Ns, typename F> void with_channels(int n, int64_t W, jscan_activation a, F f) {
+    ((n == Ns ? with_width<E, Ns>(W, a, f) : void()), ...);
 }
-template <typename F> void dispatch(jscan_dtype dtype, int n, int64_t W, jscan_activation a, F f) {
-    if (dtype == JSCAN_BF16) with_channels<jscan::BF16>(n, W, a, f);
-    else with_channels<jscan::F32>(n, W, a, f);
+template <int... Ns, typename F> void dispatch(jscan_dtype dtype, int n, int64_t W, jscan_activation a, F f) {
+    if (dtype == JSCAN_BF16) with_channels<jscan::BF16, Ns...>(n, W, a, f);
+    else with_channels<jscan::F32, Ns...>(n, W, a, f);
 }
 
 jscan_status check_kind(jscan_activation activation, jscan_dtype dtype) {
@@ -193,9 +199,9 @@ jscan_status jscan_causal_conv(const void *x, const void *state, const float *w,
     ConvArgs a{};
     a.x = {x, ld_x}, a.y = {y, ld_y}, a.state = state, a.state_out = state_out, a.w = w, a.bias = bias;
     a.lengths = lengths, a.batch = batch, a.L = L, a.D = D, a.stream = static_cast<hipStream_t>(stream);
-    a.streams = streams(batch, L, D, es, 2, n);
+    a.streams = n > 1 && streams(batch, L, D, es, 2);
     a.split = split_for(batch, L, D, n, kForwardWaves, a.streams ? kForwardStreamRun : kForwardRun);
-    dispatch(dtype, n, W, activation, [&](auto e, auto n_c, auto w_c, auto a_c) {
+    dispatch<4, 1>(dtype, n, W, activation, [&](auto e, auto n_c, auto w_c, auto a_c) {
         launch_forward<decltype(e), decltype(n_c)::value, decltype(w_c)::value, (Act)decltype(a_c)::value, false>(a);
     });
     return launch_status();
@@ -238,11 +244,11 @@ jscan_status jscan_causal_conv_backward(const void *x, const void *state, const 
     a.batch = batch, a.L = L, a.D = D, a.stream = static_cast<hipStream_t>(stream);
     int64_t shares = 0;   // none without a sequence: the gradients of taps and bias are then zeros
     if (batch > 0) {
-        a.split = backward_split(batch, L, D);
-        a.streams = streams(batch, L, D, es, 3, channels_of(D));
+        const bool streamed = streams(batch, L, D, es, 3);
+        a.split = backward_split(batch, L, D, streamed);
         shares = batch * a.split.segs;
-        dispatch(dtype, channels_of(D), W, activation, [&](auto e, auto n_c, auto w_c, auto a_c) {
-            launch_backward<decltype(e), decltype(n_c)::value, decltype(w_c)::value, (Act)decltype(a_c)::value, false>(a);
+        dispatch<4, 2, 1>(dtype, backward_channels_of(D, streamed), W, activation, [&](auto e, auto n_c, auto w_c, auto a_c) {
+            launch_backward<decltype(e), decltype(n_c)::value, decltype(w_c)::value, (Act)decltype(a_c)::value>(a);
         });
         if (launch_status() != JSCAN_OK) return JSCAN_ERR_HIP;
     }
@@ -269,7 +275,7 @@ jscan_status jscan_causal_conv_step(void *state, const void *x_t, const float *w
     const Rows in[] = {rows_of({x_t, ld_x}, batch, D, es), flat(w, D * W * 4), flat(bias, D * 4)};
     if (any_overlap(out, in)) return JSCAN_ERR_ALIAS;
     // the state is updated in place, so no two words may share a channel
-    dispatch(dtype, D % 4 == 0 ? 4 : 1, W, activation, [&](auto e, auto n_c, auto w_c, auto a_c) {
+    dispatch<2, 1>(dtype, D % 2 == 0 ? 2 : 1, W, activation, [&](auto e, auto n_c, auto w_c, auto a_c) {
         launch_step<decltype(e), decltype(n_c)::value, decltype(w_c)::value, (Act)decltype(a_c)::value, 1>(
             state, x_t, w, bias, y_t, batch, D, ld_x, ld_y, static_cast<hipStream_t>(stream));
     });

@@ -36,6 +36,11 @@ template <> struct Word<BF16, 4> {
         return raw{pack2(f[0], f[1]), pack2(f[2], f[3])};
     }
 };
+template <> struct Word<BF16, 2> {
+    typedef uint32_t raw __attribute__((aligned(2)));
+    static __device__ __forceinline__ void unpack(raw w, float (&f)[2]) { f[0] = bf16_lo(w), f[1] = bf16_hi(w); }
+    static __device__ __forceinline__ raw pack(const float (&f)[2]) { return pack2(f[0], f[1]); }
+};
 template <> struct Word<BF16, 1> {
     using raw = uint16_t;
     static __device__ __forceinline__ void unpack(raw w, float (&f)[1]) { f[0] = bf16_bits_to_f32(w); }
@@ -47,6 +52,11 @@ template <> struct Word<F32, 4> {
         f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
     }
     static __device__ __forceinline__ raw pack(const float (&f)[4]) { return raw{f[0], f[1], f[2], f[3]}; }
+};
+template <> struct Word<F32, 2> {
+    typedef float raw __attribute__((ext_vector_type(2), aligned(4)));
+    static __device__ __forceinline__ void unpack(raw w, float (&f)[2]) { f[0] = w.x, f[1] = w.y; }
+    static __device__ __forceinline__ raw pack(const float (&f)[2]) { return raw{f[0], f[1]}; }
 };
 template <> struct Word<F32, 1> {
     using raw = float;
