@@ -682,10 +682,8 @@ def _gated_workspace(workspace, batch, L, D, dev):
 
 def _workspace(workspace, need, dev):
     """The caller's workspace, or a new one of `need` bytes (None for 0), and its size."""
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is None:
-        return None, 0
+        return (torch.empty(need, dtype=torch.uint8, device=dev), need) if need > 0 else (None, 0)
     if workspace.device != dev or not workspace.is_contiguous():
         _bad(f"workspace must be contiguous and on {dev}")
     return workspace, workspace.numel() * workspace.element_size()
@@ -1099,7 +1097,8 @@ def causal_conv_backward(x, w, dy, bias=None, state=None, dstate_out=None, lengt
     results.  Returns ``(dx, dw, dbias, dstate)``: dx and dstate in x's dtype, dw ``[D, W]`` and dbias ``[D]`` fp32
     sums over all tokens; dbias is None without a bias and dstate without a state.  dx may be given as a slice of a
     wider gradient."""
-    if any(t is not None and t.requires_grad for t in (x, w, dy, bias, state, dstate_out)):
+    if x.requires_grad or w.requires_grad or dy.requires_grad or (bias is not None and bias.requires_grad) or \
+            (state is not None and state.requires_grad) or (dstate_out is not None and dstate_out.requires_grad):
         _refuse_grad()
     code = _conv_activation(activation)
     W = _check_conv(x, w, bias, state, lengths)
