@@ -10,7 +10,8 @@
 // channels' window of W - 1 tokens in registers and walks a run of tokens, so x is read once but for the
 // W - 1 tokens before each run (backward: and the W - 1 behind it).
 // Measured (bf16, four taps, SiLU; us, bytes that cross HBM over time): forward 16 x 4096 x 8192 359, 6.0 TB/s; 8 x
-// 4096 x 8192 forward 193, 5.6, backward 290 + 5 for the sums, 5.7; step 256 x 8192 7.2, 4.7 from the last-level cache.
+// 4096 x 8192 forward 193, 5.6, backward 288 + 5 for the sums, 5.7; step 256 x 8192 6.3 from the
+// last-level cache.
 #pragma once
 
 #include <type_traits>
