@@ -1,5 +1,6 @@
-"""fp64 oracle of what surrounds the recurrence in its layer: the short causal convolution and its gradients
-(numpy, tap by tap from the definition; shares no code with the GPU path), with bounds of the fp32 kernels' errors.
+"""fp64 oracle of what surrounds the recurrence in its layer: the short causal convolution and the root-mean-square
+norm with their gradients, and the activations (numpy, from the definitions; shares no code with the GPU path), with
+bounds of the fp32 kernels' errors.
 """
 from __future__ import annotations
 
