@@ -1043,10 +1043,13 @@ def _check_conv(x, w, bias, state, lengths):
     if w.dim() != 2 or not 2 <= w.shape[1] <= 4:
         _bad(f"w must be [D, W] with W = 2, 3 or 4, got {tuple(w.shape)}")
     W = w.shape[1]
-    _check_flat("w", w, (D, W), _F32, dev)
-    if bias is not None:
+    # the conditions of _check_flat, which says what is wrong: a call of it costs as much as they do
+    if w.dtype != _F32 or w.shape[0] != D or w.device != dev or not w.is_contiguous():
+        _check_flat("w", w, (D, W), _F32, dev)
+    if bias is not None and (bias.dtype != _F32 or bias.shape != (D,) or bias.device != dev or not bias.is_contiguous()):
         _check_flat("bias", bias, (D,), _F32, dev)
-    if state is not None:
+    if state is not None and (state.dtype != x.dtype or state.shape != (batch, W - 1, D) or state.device != dev or
+                              not state.is_contiguous()):
         _check_flat("state", state, (batch, W - 1, D), x.dtype, dev)
     if lengths is not None:
         _check_flat("lengths", lengths, (batch,), _I32, dev)
@@ -1170,21 +1173,28 @@ def causal_conv_step(state, x_t, w, bias=None, activation="silu", y_t=None):
 
 
 def _check_norm(x, gain, name="x"):
-    """The width and the leading shape of x."""
+    """The width and the number of x's rows."""
     if not x.is_cuda or x.dtype not in _DTYPES:
         _bad(f"{name} must be a bfloat16 or float32 CUDA tensor")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    shape = x.shape
+    if not shape or shape[-1] < 1:
         _bad(f"{name} must have a last dimension")
-    K, lead = x.shape[-1], x.shape[:-1]
-    _check_flat("gain", gain, (K,), _F32, x.device)
-    return K, lead
+    K = shape[-1]
+    if gain.shape != (K,) or gain.dtype != _F32 or gain.device != x.device or not gain.is_contiguous():
+        _check_flat("gain", gain, (K,), _F32, x.device)
+    return K, x.numel() // K
+
+
+def _new_rows(x):
+    """A contiguous tensor of x's shape, dtype and device."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(*x.shape, dtype=x.dtype, device=x.device)
 
 
 def _norm_rows(name, t, like):
     """The row stride of a tensor that has x's shape, dtype and device."""
-    if t is not like:
+    if t is not like and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
         _check_like(name, t, like.shape, like.dtype, like.device)
-    return _row_stride(name, t)
+    return like.shape[-1] if t.is_contiguous() else _row_stride(name, t)
 
 
 def _norm_total(x, residual, total):
@@ -1195,7 +1205,7 @@ def _norm_total(x, residual, total):
         return None, 0, 0
     ld_residual = _norm_rows("residual", residual, x)
     if total is None:
-        return torch.empty(*x.shape, dtype=x.dtype, device=x.device), ld_residual, x.shape[-1]
+        return _new_rows(x), ld_residual, x.shape[-1]
     return total, ld_residual, _norm_rows("total", total, x)
 
 
@@ -1207,15 +1217,15 @@ def rms_norm(x, gain, residual=None, eps=1e-6, y=None, total=None):
     (:func:`rms_norm_backward` has its gradients)."""
     if x.requires_grad or gain.requires_grad or (residual is not None and residual.requires_grad):
         _refuse_grad()
-    K, lead = _check_norm(x, gain)
-    ld_x = _row_stride("x", x)
+    K, M = _check_norm(x, gain)
+    ld_x = K if x.is_contiguous() else _row_stride("x", x)
     total, ld_residual, ld_total = _norm_total(x, residual, total)
     if y is None:
-        y, ld_y = torch.empty(*x.shape, dtype=x.dtype, device=x.device), K
+        y, ld_y = _new_rows(x), K
     else:
         ld_y = _norm_rows("y", y, x)
     _launch("jscan_rms_norm", x.device, x.data_ptr(), _addr(residual), gain.data_ptr(), y.data_ptr(), _addr(total),
-            lead.numel(), K, ld_x, ld_residual, ld_y, ld_total, eps, _DTYPES[x.dtype])
+            M, K, ld_x, ld_residual, ld_y, ld_total, eps, _DTYPES[x.dtype])
     return y, x if total is None else total
 
 
@@ -1224,8 +1234,8 @@ def rms_norm_quantize(x, gain, residual=None, eps=1e-6, q=None, scale=None, tota
     fp32, total)``, q and scale the first inputs of :func:`matmul_i8`.  K a multiple of 16."""
     if x.requires_grad or gain.requires_grad or (residual is not None and residual.requires_grad):
         _refuse_grad()
-    K, lead = _check_norm(x, gain)
-    dev = x.device
+    K, M = _check_norm(x, gain)
+    dev, lead = x.device, x.shape[:-1]
     ld_x = _row_stride("x", x)
     total, ld_residual, ld_total = _norm_total(x, residual, total)
     if q is None:
@@ -1237,7 +1247,7 @@ def rms_norm_quantize(x, gain, residual=None, eps=1e-6, q=None, scale=None, tota
     else:
         _check_flat("scale", scale, lead, _F32, dev)
     _launch("jscan_rms_norm_quantize", dev, x.data_ptr(), _addr(residual), gain.data_ptr(), q.data_ptr(), scale.data_ptr(),
-            _addr(total), lead.numel(), K, ld_x, ld_residual, ld_total, eps, _DTYPES[x.dtype])
+            _addr(total), M, K, ld_x, ld_residual, ld_total, eps, _DTYPES[x.dtype])
     return q, scale, x if total is None else total
 
 
@@ -1255,12 +1265,12 @@ def rms_norm_backward(total, gain, dy, dtotal=None, eps=1e-6, dx=None, dgain=Non
     x and of residual alike, in their dtype; dgain ``[K]`` fp32.  A given ``dx`` may be dtotal itself."""
     if total.requires_grad or gain.requires_grad or dy.requires_grad or (dtotal is not None and dtotal.requires_grad):
         _refuse_grad()
-    K, lead = _check_norm(total, gain, "total")
-    dev, M = total.device, lead.numel()
+    K, M = _check_norm(total, gain, "total")
+    dev = total.device
     ld_total, ld_dy = _row_stride("total", total), _norm_rows("dy", dy, total)
     ld_dtotal = 0 if dtotal is None else _norm_rows("dtotal", dtotal, total)
     if dx is None:
-        dx, ld_dx = torch.empty(*total.shape, dtype=total.dtype, device=dev), K
+        dx, ld_dx = _new_rows(total), K
     else:
         ld_dx = _norm_rows("dx", dx, total)
     if dgain is None:
