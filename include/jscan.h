@@ -23,7 +23,7 @@
  * other.  So the state that jscan_prefill returns is bit-identical to the state after L
  * calls of jscan_step on the same tokens, starting from +0.0.  y accumulates in fp32 and is
  * rounded to nearest even to the output dtype.  With bf16 output the prefill's sum over the
- * states runs on the matrix cores: its terms are rounded to bf16 once (2^-9 relative) and
+ * states runs on the matrix cores: its terms are rounded to bf16 once (2^-8 relative) and
  * summed in fp32 (the products C_t[n] h_t[d,n] with h rounded, or, in jscan_prefill_fused, the
  * lanes' fp32 partial sums over two states).  A NaN in a channel's state then also reaches
  * that channel's outputs earlier in the same 16-token group (a NaN term times a zero weight of
@@ -612,13 +612,17 @@ jscan_status jscan_causal_conv_step(void *state, const void *x_t, const float *w
 /*
  * The selective scan with what follows it in its layer, the skip and the output gate, in one pass:
  *     y_t[d] = (sum_n C_t[n] h_t[d,n] + skip[d] x_t[d]) silu(z_t[d])
- * in fp32, rounded once.  skip or z may be NULL (its part is left out; not both).  h is the scan's, bit for bit (see chunk).
+ * rounded once from fp32.  skip or z may be NULL (its part is left out; not both).  h is the scan's, bit for bit (see chunk).
+ * The sum over n is fp32, but for one case that the caller chooses by chunk: with bf16 and D a multiple of 32 a
+ * token-by-token call (chunk -1, or any call with another a_form) forms it as jscan_prefill does, each state rounded to
+ * bf16 on its way into the sum (see Arithmetic above).  What enters the skip and the gate is then off by up to
+ * 2^-8 sum_n |C_t[n] h_t[d,n]|, which stays where C h and skip x cancel, and a NaN reaches earlier tokens of its channel.
  *   skip      [D] fp32
  *   z         batch * L token rows of D values in `dtype`, row stride ld_z >= D (a multiple of 8, at most 2^25), in the
  *             order of x's rows: z may be a half of a wider projection
  *   chunk     -1: token by token (h is jscan_prefill_resume's, or that of a_form's prefill); above 0: in segments
  *             of that many tokens (h is jscan_prefill_chunked's); 0: whichever way is expected to be fastest for this
- *             shape.  Segments are for JSCAN_A_DIAGONAL: for the other forms 0 is token by token and a given
+ *             shape among those that sum in fp32.  Segments are for JSCAN_A_DIAGONAL: for the other forms 0 is token by token and a given
  *             length is JSCAN_ERR_FORM
  *   workspace jscan_prefill_gate_workspace(batch, L, D, N, chunk) bytes where a_form is JSCAN_A_DIAGONAL; else, and
  *             where that is 0, it may be NULL

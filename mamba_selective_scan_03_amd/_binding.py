@@ -937,7 +937,9 @@ def prefill_gate(x, delta, A, B, C, skip=None, z=None, h0=None, form="diagonal",
     ``y = (scan(x) + skip * x) * silu(z)``, with ``skip`` ``[D]`` fp32 and z ``[batch, L, D]`` in x's dtype (rows may be a
     half of a wider projection); either may be None.  Other arguments and results as for :func:`prefill`, A as the
     ``form`` has it.  ``chunk`` None scans token by token (h_final is bit for bit :func:`prefill`'s), a segment length as
-    :func:`prefill_chunked` does, and 0 whichever way is expected to be fastest (form "diagonal"; the others take 0 as None);
+    :func:`prefill_chunked` does, and 0 whichever way is expected to be fastest (form "diagonal"; the others take 0 as None).
+    The sum over the states is fp32, except that token by token in bf16 with D a multiple of 32 it is :func:`prefill`'s, which
+    rounds each state to bf16 first: of the diagonal form with ``chunk=None``, of the others always.
     ``workspace`` of :func:`prefill_gate_workspace_bytes`, or one is allocated.  Autograd does not record the call."""
     if x.requires_grad or delta.requires_grad or A.requires_grad or B.requires_grad or C.requires_grad or \
             any(t is not None and t.requires_grad for t in (skip, z, h0)):

@@ -2,7 +2,8 @@
 // sequences, token by token or time-parallel, and the decode step.  The kernels are those of the scan without
 // them, instantiated with kGate: the arithmetic of the scan bounds them as it does without, and the gate adds a logistic
 // function to a token's sixteen exponentials and a fourth tensor to the three.  Measured, bf16 (us, and without skip and
-// gate): 1 x 65536 x 8192 1849 (1766), 1 x 65536 x 1024 in segments 343 (328); step 256 x 8192 46.5, 6.1 TB/s.
+// gate): 1 x 65536 x 8192 token by token as the scan sums 1860 (1766), with fp32 sums (chunk 0) 2086; 1 x 65536 x 1024 in
+// segments 343 (328); step 256 x 8192 46.5, 6.1 TB/s.
 #include "prefill_host.h"
 #include "prefill_lane_kernel.h"
 #include "step_kernel.h"
@@ -23,8 +24,8 @@ bool gate_grids_fit(int64_t batch, int64_t D, const ChunkPlan &p) {
 constexpr int64_t kMostGateStride = (int64_t)1 << 25;   // elements between rows of z (32-bit byte offsets of 8 rows)
 
 // How an automatic call scans: the way that is expected to take least, token by token or in segments of seg_len tokens.
-// Times in us, from one GPU of 256 CUs (bf16; fp32 takes much the same):
-//     rows kernel    a work-group a CU at a time, each 8 and 0.028 a token       (1 x 65536 x 8192 1849, 8 x 639 x 416 25)
+// Times in us, from one GPU of 256 CUs (bf16 with fp32 sums; fp32 takes up to 1.1 times that):
+//     rows kernel    a work-group a CU at a time, each 8 and 0.031 a token       (1 x 65536 x 8192 2086, 8 x 639 x 416 24)
 //     lane kernel    0.65 a token for few waves, 0.58 more for a wave a SIMD     (3 x 688 x 144 453, 24 x 847 x 5704 1508)
 //     segments       15, a token of both passes 0.66 to 1.25 with one to four waves a SIMD, which is what fits at a
 //                    time, and 700 bytes for a channel's states and A in each,
@@ -38,8 +39,8 @@ ChunkPlan plan_automatic(int64_t batch, int64_t L, int64_t D) {
     float least;
     if (jscan::rows_kernel_applies(batch, D)) {
         const int64_t groups = batch * (D / jscan::rows::kCh);
-        least = (float)((groups + 255) / 256) * (0.028f * tokens + 8.0f);
-        if (groups > 256) least *= 0.7f;   // left only for a clear gain: 13 x 95 x 5664 takes 58, in segments of 32 77
+        least = (float)((groups + 255) / 256) * (0.031f * tokens + 8.0f);
+        if (groups > 256) least *= 0.7f;   // left only for a clear gain: 13 x 95 x 5664 takes 60, in segments of 32 77
     } else {
         const float waves = (float)(batch * ((D + 63) / 64)) / 1024.0f;   // a SIMD
         const float token = 0.55f + 0.58f * waves;
@@ -72,6 +73,7 @@ struct GateArgs {
     float *h_final;
     int64_t batch, L, D, ld_xd, ld_bc, ld_y;
     OutGate gate;
+    bool fp32_sum;   // with a chunk given or automatic: the precision must not depend on the way that the shape is scanned
     hipStream_t stream;
 };
 
@@ -100,9 +102,15 @@ template <typename E, AForm AF> void launch_sequences(const GateArgs &a) {
     const T *B = static_cast<const T *>(a.B), *C = static_cast<const T *>(a.C);
     T *y = static_cast<T *>(a.y);
     if (jscan::rows_kernel_applies(a.batch, a.D)) {
-        jscan::launch_prefill_rows<E, false, AF, false, true>(x, dl, a.A, B, C, a.h0, y, a.h_final, sg, a.batch, (int)a.D,
-                                                              a.stream, jscan::DeltaProj{nullptr, nullptr, nullptr},
-                                                              jscan::Trap{nullptr, nullptr, nullptr}, a.gate);
+        auto launch = [&](auto fp32_sum) {
+            jscan::launch_prefill_rows<E, false, AF, false, true, decltype(fp32_sum)::value != 0>(
+                x, dl, a.A, B, C, a.h0, y, a.h_final, sg, a.batch, (int)a.D, a.stream,
+                jscan::DeltaProj{nullptr, nullptr, nullptr}, jscan::Trap{nullptr, nullptr, nullptr}, a.gate);
+        };
+        if constexpr (sizeof(T) == 2 && AF == AForm::Diagonal) {
+            if (a.fp32_sum) return launch(jscan::IntConst<1>{});
+        }
+        launch(jscan::IntConst<0>{});
         return;
     }
     const int blocks = (int)((a.D + 63) / 64);
@@ -210,7 +218,7 @@ jscan_status jscan_prefill_gate(const void *x, const void *delta, const float *A
     if (st != JSCAN_OK) return st;
     GateArgs a{};
     a.x = x, a.delta = delta, a.A = A, a.B = B, a.C = C, a.h0 = h0, a.y = y, a.h_final = h_final;
-    a.batch = batch, a.L = L, a.D = D, a.gate = OutGate{skip, z, ld_z}, a.stream = static_cast<hipStream_t>(stream);
+    a.batch = batch, a.L = L, a.D = D, a.gate = OutGate{skip, z, ld_z}, a.fp32_sum = chunk >= 0, a.stream = static_cast<hipStream_t>(stream);
     if (L == 0) {
         const int64_t total = batch * D * jscan::kDState, each = (int64_t)1 << 31;
         for (int64_t i = 0; i < total; i += each) {

@@ -507,7 +507,7 @@ __device__ __forceinline__ void scan_half(const GroupRegs &g, float &h_0, float 
 // a half's partials are the A operand A[c][8r + j] = partial of row r, token j; the constant B
 // operand sel[0] is the one-hot B[8r + j][col] = (j == col) for col < 8, and sel[1] the same for
 // col = 8 + j.  The two MFMAs give D[c][tok] = sum over r of the token's partials, in the layout
-// of the contraction below.  The partials are rounded to bf16 once (2^-9 relative).
+// of the contraction below.  The partials are rounded to bf16 once (2^-8 relative).
 __device__ __forceinline__ void row_sum_operands(bf16x8_t (&sel)[2], int lane) {
     const int col = lane & 15;
 #pragma unroll
@@ -533,7 +533,7 @@ __device__ __forceinline__ void row_sum_operands(bf16x8_t (&sel)[2], int lane) {
 // (r, col) reads the table for its m and the zero block for the other three, at the same
 // offsets, so the reads need no per-lane selection.  Products of bf16 values are exact and the
 // MFMA sums in fp32, so y differs from the fp32 contraction by the rounding of h to bf16
-// (2^-9 relative per term), below y's own rounding to bf16.
+// (2^-8 relative per term): no more than y's own rounding to bf16 where the terms do not cancel.
 __device__ __forceinline__ void c_operand_bases(const uint32_t *(&selp)[4], const uint32_t *cs_s, int sh, int lane) {
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -636,8 +636,9 @@ __device__ __forceinline__ void write_final(const FinalRegs &F, typename E::stor
 // a scaled-identity A (AF), A is a[D] (one value per channel) instead of A[D][16]; with a
 // complex state, A[D][16] holds 8 complex entries per channel as (real, imaginary) pairs.  With
 // kTrap the exponential-trapezoidal rule replaces the Euler rule (extra inputs in tr); with kGate y
-// leaves through the skip and the gate (og).
-template <typename E, bool kFused = false, AForm AF = AForm::Diagonal, bool kTrap = false, bool kGate = false>
+// leaves through the skip and the gate (og).  kFp32Sum sums bf16 output like fp32 output, no state rounded.
+template <typename E, bool kFused = false, AForm AF = AForm::Diagonal, bool kTrap = false, bool kGate = false,
+          bool kFp32Sum = false>
 __global__ __launch_bounds__(rows::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void prefill_rows_kernel(
     const typename E::store_t *__restrict__ x, const typename E::store_t *__restrict__ dl,
     const float *__restrict__ A, const typename E::store_t *__restrict__ B,
@@ -654,7 +655,7 @@ __global__ __launch_bounds__(rows::kThreads) __attribute__((amdgpu_waves_per_eu(
     // (c_operand_bases()), or, with delta computed here, whose helper waves keep the matrix cores
     // busy with delta's MFMAs, only the 4-row sum of the lanes' partials (row_sum_operands(): half
     // the MFMAs).  fp32 output keeps the fp32 contraction, in-lane and by permlane swaps.
-    constexpr OutSum OS = sizeof(S) != 2 ? OutSum::Permlane : kFused ? OutSum::RowMma : OutSum::CMma;
+    constexpr OutSum OS = sizeof(S) != 2 || kFp32Sum ? OutSum::Permlane : kFused ? OutSum::RowMma : OutSum::CMma;
     constexpr bool kRowMma = OS != OutSum::Permlane;   // the row sums on the matrix cores
     constexpr bool kCOps = OS == OutSum::CMma;         // C operand tables in LDS
     __shared__ __attribute__((aligned(16))) float dx_s[2][rows::kDxSize];
@@ -954,7 +955,8 @@ __global__ __launch_bounds__(rows::kThreads) __attribute__((amdgpu_waves_per_eu(
 inline bool rows_kernel_applies(int64_t /*batch*/, int64_t D) { return D % rows::kCh == 0; }
 
 // Launches one work-group per 32 channels of each of the `nrows` rows described by sg.
-template <typename E, bool kFused = false, AForm AF = AForm::Diagonal, bool kTrap = false, bool kGate = false>
+template <typename E, bool kFused = false, AForm AF = AForm::Diagonal, bool kTrap = false, bool kGate = false,
+          bool kFp32Sum = false>
 void launch_prefill_rows(const typename E::store_t *x, const typename E::store_t *dl, const float *A,
                          const typename E::store_t *B, const typename E::store_t *C, const float *h0,
                          typename E::store_t *y, float *h_final, const Segments &sg, int64_t nrows,
@@ -963,7 +965,7 @@ void launch_prefill_rows(const typename E::store_t *x, const typename E::store_t
     const int blocks_per_row = D / rows::kCh;
     const int64_t blocks = nrows * blocks_per_row;
     const int xcd_stride = (blocks % 8 == 0) ? (int)(blocks / 8) : 0;
-    hipLaunchKernelGGL((prefill_rows_kernel<E, kFused, AF, kTrap, kGate>), dim3((unsigned)blocks),
+    hipLaunchKernelGGL((prefill_rows_kernel<E, kFused, AF, kTrap, kGate, kFp32Sum>), dim3((unsigned)blocks),
                        dim3(rows::kThreads), 0, stream, x, dl, A, B, C, h0, y, h_final, sg, D, blocks_per_row,
                        xcd_stride, dp, tr, og);
 }
