@@ -653,8 +653,8 @@ jscan_status jscan_step_gate(float *h, const void *x_t, const void *delta_t, con
  *     total = x + residual, rounded to `dtype` (the residual stream as it is kept)
  *     y = total gain / sqrt(mean_k total^2 + eps)
  * in fp32 (as (total gain) r with r = 1 / sqrt(...)), rounded once.  So the call on x and residual gives what the call on total
- * alone gives, bit for bit.  A row that holds a NaN or an infinity, or whose sum of squares overflows fp32, has no
- * norm; no other row is touched.
+ * alone gives, bit for bit.  A row that holds a NaN or an infinity, or whose mean square plus eps is no normal fp32
+ * number (the squares overflow, or eps is 0 and they vanish), has no norm: its y is NaN; no other row is touched.
  *   x, residual   M rows of K values in `dtype`, row strides ld_x, ld_residual >= K; residual may be NULL: total is then x
  *   gain          [K] fp32
  *   y             M rows out, stride ld_y
@@ -679,7 +679,8 @@ jscan_status jscan_rms_norm_quantize(const void *x, const void *residual, const 
 /*
  * Backward pass of jscan_rms_norm from total.  With r = 1 / sqrt(mean total^2 + eps) and g = dy gain,
  *     dx = r (g - total r mean_k(g total r)) + dtotal,   dgain = sum over rows of dy total r
- * dx is the gradient of x and of residual alike.  Sums are fp32, in a fixed order (no atomics).
+ * dx is the gradient of x and of residual alike.  Sums are fp32, in a fixed order (no atomics).  A row without a norm
+ * (see above) has NaN for its dx and makes dgain NaN.
  *   dtotal      M rows, the gradient that comes from total's other uses, or NULL for zeros
  *   dx          M rows out; may be dtotal itself;   dgain [K] fp32 out (zeros with M == 0)
  *   workspace   jscan_rms_norm_backward_workspace(M, K) bytes, 16-byte aligned, overlapping nothing else.  Contents on

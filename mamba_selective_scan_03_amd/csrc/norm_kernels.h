@@ -138,8 +138,11 @@ __device__ __forceinline__ void group_reduce(float (&a)[kRows], float (&b)[kRows
 constexpr int rows_at_once(int waves, int chunks) { return waves < 16 && chunks <= 2 ? 2 : 1; }
 constexpr bool fetches_ahead(int waves) { return waves < 16; }
 
+// 1 / sqrt(mean + eps).  Outside the normal numbers there is none that fp32 squares could give (they have overflowed or
+// lost their bits, or the row holds an infinity): NaN, so that every form of the call says so.
 __device__ __forceinline__ float rms_scale(float sum, int K, float eps) {
-    return __builtin_amdgcn_rsqf(sum / (float)K + eps);
+    const float v = sum / (float)K + eps;
+    return v >= 0x1.0p-126f && v < __builtin_inff() ? __builtin_amdgcn_rsqf(v) : __builtin_nanf("");
 }
 
 template <typename E, int kChunks> __device__ __forceinline__ void load_gain(float (&g)[kChunks][Piece<E>::n], const float *gain,
