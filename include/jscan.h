@@ -692,7 +692,7 @@ jscan_status jscan_rms_norm_backward(const void *total, const float *gain, const
                                      void *workspace, int64_t workspace_bytes, float eps,
                                      jscan_dtype dtype, void *stream);
 
-/* Workspace bytes of jscan_rms_norm_backward for this shape (0 for a few rows: it may then be NULL), or -1 if the
+/* Workspace bytes of jscan_rms_norm_backward for this shape (0 for a few short rows: it may then be NULL), or -1 if the
  * shape is invalid.  Host-only. */
 int64_t jscan_rms_norm_backward_workspace(int64_t M, int64_t K);
 

@@ -29,9 +29,13 @@ constexpr int64_t kMostGroups = (int64_t)1 << 20;   // of a launch
 int64_t forward_groups(int64_t M) { return M < kMostGroups ? M : kMostGroups; }
 
 // Work-groups of the backward pass, each of which goes on to further rows and leaves a share of the gain's gradient; one
-// for a few rows, which writes that gradient itself (a second launch takes longer than they do).
-int64_t backward_groups(const Layout &l, int64_t M) {
-    if (M <= 8) return M > 0 ? 1 : 0;
+// for a row, or for a few short ones, which writes that gradient itself and spares the launch that adds the shares, about
+// 4 us of the host's time.  On the GPU (us, one work-group and one a row with that launch; bf16): 8 x 64 5.5 and 4.6, 8 x
+// 2048 6.9 and 5.8, 4 x 4096 5.9 and 6.5, 2 x 8192 5.8 and 6.8; beyond the limit 8 x 4096 9.1 and 6.5, 8 x 16384 21 and
+// 9.7, 2 x 32768 37 and 29, 8 x 65536 271 and 41.
+constexpr int64_t kFewRows = 8, kFewValues = 16384;
+int64_t backward_groups(const Layout &l, int64_t M, int64_t K) {
+    if (M <= 1 || (M <= kFewRows && M * K <= kFewValues)) return M > 0 ? 1 : 0;
     const int64_t each = l.chunks == 0 ? 1 : jscan::norm::rows_at_once(l.waves, l.chunks);
     const int64_t most = l.waves == 1 ? 1024 : l.waves == 4 ? 512 : 256;   // four, eight, sixteen waves a CU
     const int64_t rows = (M + each - 1) / each;
@@ -181,8 +185,9 @@ jscan_status jscan_rms_norm_quantize(const void *x, const void *residual, const 
 // Room for the groups of either type: rows of fp32 take four waves where those of bf16 take one.
 int64_t jscan_rms_norm_backward_workspace(int64_t M, int64_t K) {
     if (!sizes_ok(M, K, 0.0f)) return -1;
-    const int64_t a = backward_groups(layout_for(K, 2), M), b = backward_groups(layout_for(K, 4), M);
-    return M <= 8 ? 0 : (a > b ? a : b) * K * 4;
+    const int64_t a = backward_groups(layout_for(K, 2), M, K), b = backward_groups(layout_for(K, 4), M, K);
+    const int64_t groups = a > b ? a : b;
+    return groups <= 1 ? 0 : groups * K * 4;
 }
 
 jscan_status jscan_rms_norm_backward(const void *total, const float *gain, const void *dy, const void *dtotal, void *dx,
@@ -211,7 +216,7 @@ jscan_status jscan_rms_norm_backward(const void *total, const float *gain, const
     a.stream = static_cast<hipStream_t>(stream);
     if (M > 0) {
         const Layout l = layout_for(K, es);
-        a.groups = backward_groups(l, M);
+        a.groups = backward_groups(l, M, K);
         if (a.groups == 1) a.partial = dgain;
         with_layout(l, [&](auto w, auto c) {
             if (dtype == JSCAN_BF16) launch_backward<jscan::BF16, decltype(w)::value, decltype(c)::value>(a);
