@@ -3,8 +3,10 @@ from __future__ import annotations
 
 import ctypes
 import os
+import types
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libjscan.so")
@@ -591,6 +593,9 @@ _F32, _I8, _I32 = torch.float32, torch.int8, torch.int32
 # Its private accessors where torch has them; the public ones build a Stream object and check the device's state.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+# The level of forward-mode differentiation (-1 outside of it), where torch shows it; unpack_dual finds it by itself.
+_dual = forward_ad if hasattr(forward_ad, "_current_level") else types.SimpleNamespace(_current_level=0)
+_forward_mode = getattr(torch._C, "_is_fwd_grad_enabled", None) or (lambda: True)
 
 
 def _launch(name, dev, *args):
@@ -619,6 +624,13 @@ def _refuse_grad():
     if torch.is_grad_enabled():
         _bad("autograd does not record this call: make it under torch.no_grad(), on detached tensors, or inside a "
              "torch.autograd.Function whose backward gives its gradients (gated_scan_backward for gated_scan, and so on)")
+
+
+def _refuse_tangents(*tensors):
+    """The same for forward mode: its tensors carry a tangent and do not require gradients, and no_grad does not stop it."""
+    if _forward_mode() and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        _bad("forward-mode differentiation does not pass through this call: make it on detached tensors, or inside a "
+             "torch.autograd.Function whose jvp gives the tangent")
 
 
 def _check_like(name, t, shape, dtype, dev):
@@ -719,6 +731,8 @@ def gated_scan(g, u, h0=None, lengths=None, form="decay", y=None, h_final=None, 
     call: tensors that require gradients are refused where it would (:func:`gated_scan_backward` has them)."""
     if g.requires_grad or u.requires_grad or (h0 is not None and h0.requires_grad):
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(g, u, h0)
     _check_gated(g, form, lengths)
     shape, dev = g.shape, g.device
     batch, L, D = shape
@@ -759,6 +773,8 @@ def gated_scan_backward(g, u, y, dy, h0=None, dh_final=None, lengths=None, form=
     in both forms, and y and h0 are not read (they may be None)."""
     if g.requires_grad or dy.requires_grad or any(t is not None and t.requires_grad for t in (u, y, h0, dh_final)):
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(g, u, y, dy, h0, dh_final)
     _check_gated(g, form, lengths)
     shape, dev = g.shape, g.device
     batch, L, D = shape
@@ -805,6 +821,8 @@ def gated_step(h, g_t, u_t, y_t=None, form="decay"):
     contiguous tensor, or the given ``y_t``, whose rows may be strided too."""
     if h.requires_grad or g_t.requires_grad or u_t.requires_grad:
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(h, g_t, u_t)
     code = GATE_FORMS.get(form)
     if code is None:
         _bad(f"form must be one of {tuple(GATE_FORMS)}")
@@ -855,6 +873,8 @@ def quantize_rows(x, q=None, scale=None):
     first input of :func:`matmul_i8`."""
     if x.requires_grad:
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(x)
     if not x.is_cuda or x.dtype not in _DTYPES:
         _bad("x must be a bfloat16 or float32 CUDA tensor")
     if x.dim() < 1:
@@ -884,6 +904,8 @@ def matmul_i8(q, q_scale, w, w_scale, bias=None, out=None, out_dtype=torch.bfloa
     if q_scale.requires_grad or w_scale.requires_grad or (bias is not None and bias.requires_grad) or \
             (residual is not None and residual.requires_grad):
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(q_scale, w_scale, bias, residual)
     code = ACTIVATIONS.get(activation)
     if code is None:
         _bad(f"activation must be one of {tuple(ACTIVATIONS)}")
@@ -944,6 +966,8 @@ def prefill_gate(x, delta, A, B, C, skip=None, z=None, h0=None, form="diagonal",
     if x.requires_grad or delta.requires_grad or A.requires_grad or B.requires_grad or C.requires_grad or \
             any(t is not None and t.requires_grad for t in (skip, z, h0)):
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(x, delta, A, B, C, skip, z, h0)
     code = A_FORMS.get(form)
     if code is None:
         _bad(f"form must be one of {tuple(A_FORMS)}")
@@ -987,6 +1011,8 @@ def step_gate(h, x_t, delta_t, A, B_t, C_t, skip=None, z_t=None, form="diagonal"
     if h.requires_grad or x_t.requires_grad or delta_t.requires_grad or A.requires_grad or B_t.requires_grad or \
             C_t.requires_grad or (skip is not None and skip.requires_grad) or (z_t is not None and z_t.requires_grad):
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(h, x_t, delta_t, A, B_t, C_t, skip, z_t)
     code = A_FORMS.get(form)
     if code is None:
         _bad(f"form must be one of {tuple(A_FORMS)}")
@@ -1069,6 +1095,8 @@ def causal_conv(x, w, bias=None, state=None, lengths=None, activation="silu", y=
     if x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or \
             (state is not None and state.requires_grad):
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(x, w, bias, state)
     code = _conv_activation(activation)
     W = _check_conv(x, w, bias, state, lengths)
     shape, dev, dtype = x.shape, x.device, x.dtype
@@ -1105,6 +1133,8 @@ def causal_conv_backward(x, w, dy, bias=None, state=None, dstate_out=None, lengt
     if x.requires_grad or w.requires_grad or dy.requires_grad or (bias is not None and bias.requires_grad) or \
             (state is not None and state.requires_grad) or (dstate_out is not None and dstate_out.requires_grad):
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(x, w, dy, bias, state, dstate_out)
     code = _conv_activation(activation)
     W = _check_conv(x, w, bias, state, lengths)
     shape, dev, dtype = x.shape, x.device, x.dtype
@@ -1147,6 +1177,8 @@ def causal_conv_step(state, x_t, w, bias=None, activation="silu", y_t=None):
     Returns y_t ``[batch, D]``: a new contiguous tensor, or the given ``y_t``, whose rows may be strided too."""
     if state.requires_grad or x_t.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad):
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(state, x_t, w, bias)
     code = _conv_activation(activation)
     if not state.is_cuda or state.dtype not in _DTYPES or state.dim() != 3 or not state.is_contiguous():
         _bad("state must be a contiguous bfloat16 or float32 [batch, W - 1, D] CUDA tensor")
@@ -1219,6 +1251,8 @@ def rms_norm(x, gain, residual=None, eps=1e-6, y=None, total=None):
     (:func:`rms_norm_backward` has its gradients)."""
     if x.requires_grad or gain.requires_grad or (residual is not None and residual.requires_grad):
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(x, gain, residual)
     K, M = _check_norm(x, gain)
     ld_x = K if x.is_contiguous() else _row_stride("x", x)
     total, ld_residual, ld_total = _norm_total(x, residual, total)
@@ -1236,6 +1270,8 @@ def rms_norm_quantize(x, gain, residual=None, eps=1e-6, q=None, scale=None, tota
     fp32, total)``, q and scale the first inputs of :func:`matmul_i8`.  K a multiple of 16."""
     if x.requires_grad or gain.requires_grad or (residual is not None and residual.requires_grad):
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(x, gain, residual)
     K, M = _check_norm(x, gain)
     dev, lead = x.device, x.shape[:-1]
     ld_x = _row_stride("x", x)
@@ -1267,6 +1303,8 @@ def rms_norm_backward(total, gain, dy, dtotal=None, eps=1e-6, dx=None, dgain=Non
     x and of residual alike, in their dtype; dgain ``[K]`` fp32.  A given ``dx`` may be dtotal itself."""
     if total.requires_grad or gain.requires_grad or dy.requires_grad or (dtotal is not None and dtotal.requires_grad):
         _refuse_grad()
+    if _dual._current_level >= 0:
+        _refuse_tangents(total, gain, dy, dtotal)
     K, M = _check_norm(total, gain, "total")
     dev = total.device
     ld_total, ld_dy = _row_stride("total", total), _norm_rows("dy", dy, total)
