@@ -323,11 +323,22 @@ constexpr int waves_per_simd(int waves, int lds_bytes) {
     return n < 1 ? 1 : n > 8 ? 8 : n;
 }
 
+// The results' address: with a residual, which may be out itself, a pointer like any other.
+namespace tiled {
+template <typename T, Finish F> struct OutPtrOf {
+    typedef T *__restrict__ type;
+};
+template <typename T> struct OutPtrOf<T, Finish::Residual> {
+    typedef T *type;
+};
+template <typename T, Finish F> using OutPtr = typename OutPtrOf<T, F>::type;
+}  // namespace tiled
+
 template <typename E, int BM, int BN, int WR, int WC, int KG, int kBufs, Finish F>
 __global__ __launch_bounds__(KG * WR * WC * 64,
                              waves_per_simd(KG * WR * WC, KG * kBufs * (BM + BN) * 128)) void matmul_i8_tiled_kernel(
     const int8_t *__restrict__ q, const float *__restrict__ sq, const int8_t *__restrict__ w,
-    const float *__restrict__ sw, const float *__restrict__ bias, typename E::store_t *__restrict__ out, int64_t M,
+    const float *__restrict__ sw, const float *__restrict__ bias, tiled::OutPtr<typename E::store_t, F> out, int64_t M,
     int64_t N, int64_t K, int64_t ld_out, int m_tiles, int n_tiles, int wide, Epilogue ep) {
     using namespace tiled;
     constexpr int MT = BM / WR / 16, NT = BN / WC / 16, kWaves = WR * WC;
