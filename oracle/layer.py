@@ -153,7 +153,10 @@ def rms_norm_backward(total, gain, dy, dtotal, eps):
         e_dx = e_dx + U * (np.abs(add) + np.abs(dx))
     terms = np.abs(dy * n).reshape(rows, K)
     dgain = (dy * n).reshape(rows, K).sum(0)
-    e_gain = terms.sum(0) * ((e_r + 2 * U) + min(rows, 600 + rows) * U)
+    # one addition a row of a work-group, of which there are 256 at least where rows are many (taken two at a time), and
+    # over the work-groups, at most 1024, a sixteenth of them and sixteen
+    chain = min(rows, -(-rows // 256) + 2 + 1024 // 16 + 16)
+    e_gain = terms.sum(0) * ((e_r + 2 * U) + chain * U)
     return dx, dgain, e_dx, e_gain
 
 
