@@ -566,7 +566,7 @@ typedef enum { JSCAN_ACT_NONE = 0, JSCAN_ACT_SILU = 1, JSCAN_ACT_GELU_TANH = 2 }
  *   state      [batch][W-1][D] in `dtype`, the tokens before the first (oldest first), or NULL for zeros
  *   w, bias    [D][W] and [D] fp32; bias may be NULL
  *   lengths    [batch] int32 or NULL, as for jscan_gated_scan: later rows of x are not read, later rows of y are
- *              set to zero
+ *              set to zero (a selective scan behind this call takes no lengths: see jscan_prefill_gate)
  *   state_out  [batch][W-1][D] out, the last W - 1 tokens of every sequence (the starting state's among them where
  *              it is shorter), or NULL when it is not wanted; may equal state
  * With L == 0, x and y may be NULL.  Errors as above.
@@ -627,6 +627,9 @@ jscan_status jscan_causal_conv_step(void *state, const void *x_t, const float *w
  *   workspace jscan_prefill_gate_workspace(batch, L, D, N, chunk) bytes where a_form is JSCAN_A_DIAGONAL; else, and
  *             where that is 0, it may be NULL
  *   h0        [batch][D][N] fp32 or NULL for zeros; may equal h_final
+ * There are no lengths.  In a padded batch the caller sets delta to zero behind every sequence, where x, B and C must be
+ * finite (jscan_causal_conv leaves zeros there; a delta projected from them is not zero): such a token leaves the
+ * state as it is.  y's rows there are not zero.
  * The other arguments and the errors are those of jscan_prefill_chunked.
  */
 jscan_status jscan_prefill_gate(const void *x, const void *delta, const float *A, const void *B,

@@ -962,7 +962,8 @@ def prefill_gate(x, delta, A, B, C, skip=None, z=None, h0=None, form="diagonal",
     :func:`prefill_chunked` does, and 0 whichever way is expected to be fastest (form "diagonal"; the others take 0 as None).
     The sum over the states is fp32, except that token by token in bf16 with D a multiple of 32 it is :func:`prefill`'s, which
     rounds each state to bf16 first: of the diagonal form with ``chunk=None``, of the others always.
-    ``workspace`` of :func:`prefill_gate_workspace_bytes`, or one is allocated.  Autograd does not record the call."""
+    ``workspace`` of :func:`prefill_gate_workspace_bytes`, or one is allocated.  There are no lengths: in a padded batch
+    ``delta`` has to be zero behind every sequence, which keeps its state.  Autograd does not record the call."""
     if x.requires_grad or delta.requires_grad or A.requires_grad or B.requires_grad or C.requires_grad or \
             any(t is not None and t.requires_grad for t in (skip, z, h0)):
         _refuse_grad()
@@ -1089,7 +1090,8 @@ def causal_conv(x, w, bias=None, state=None, lengths=None, activation="silu", y=
     a scan: ``y_t = act(bias + sum_k w[:, k] x_{t - (W - 1) + k})``.  x ``[batch, L, D]`` (bf16 or fp32; rows may be
     slices of a wider projection), w ``[D, W]`` and bias ``[D]`` fp32 with W = 2, 3 or 4, ``activation`` "silu" or
     "none".  ``state`` ``[batch, W - 1, D]`` in x's dtype are the tokens before the first, oldest first (None: zeros);
-    ``lengths`` int32 ``[batch]`` for padded sequences (y is zero in the padding).  Returns ``(y, state_out)``:
+    ``lengths`` int32 ``[batch]`` for padded sequences (y is zero in the padding; :func:`prefill_gate` behind it needs delta
+    zero there).  Returns ``(y, state_out)``:
     ``state_out`` holds each sequence's last W - 1 tokens, for the next call or :func:`causal_conv_step`, and may be
     ``state`` itself.  Autograd does not record the call (:func:`causal_conv_backward` has its gradients)."""
     if x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or \
