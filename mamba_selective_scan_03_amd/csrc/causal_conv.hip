@@ -194,7 +194,10 @@ jscan_status jscan_causal_conv(const void *x, const void *state, const float *w,
     const Rows in[] = {rows_of({x, ld_x}, rows, D, es), flat(state == state_out ? nullptr : state, state_bytes),
                        flat(w, D * W * 4), flat(bias, D * 4), flat(lengths, batch * 4)};
     if (any_overlap(out, in)) return JSCAN_ERR_ALIAS;
-    // a state updated in place: the last word of four channels would read what the one before it has written
+    // A state updated in place at a D that four does not divide: the last word of a row would read what the word before it
+    // has written, so a thread takes one channel, without the non-temporal hint (us, with a state of its own for the
+    // output, four channels, and in place: 16 x 4096 x 8193 bf16 501 and 536, 8 x 4096 x 8193 249 and 255, 24 x 1000 x 501
+    // 11.9 both, 5 x 1001 x 1001 fp32 8.0 and 7.7).
     const int n = state && state == state_out && D % 4 != 0 ? 1 : channels_of(D);
     ConvArgs a{};
     a.x = {x, ld_x}, a.y = {y, ld_y}, a.state = state, a.state_out = state_out, a.w = w, a.bias = bias;
