@@ -283,7 +283,7 @@ template <int NT> __device__ __forceinline__ int w_row(int t, int r) { return (r
 // shortens the chain of stages where tiles are too few to fill the chip. 16384 x 16384 x 4096 with 256 x
 // 256 tiles in 0.95 ms, 2.3 POP/s: the power limit holds the clock at about 1.6 GHz, and the matrix cores
 // are busy for 57 to 60% of it.  1 x 16384 x 4096 in 17.6 us with w read from memory, 3.8 TB/s (11.9 us from the
-// last-level cache).  77 x 4096 x 8192 in 14.5 us (13.0): the latency of the stages.  A stage's rows of q and w
+// last-level cache).  77 x 4096 x 8192 in 14.5 us (13.0): a CU stages 786 KB.  A stage's rows of q and w
 // go from memory straight into LDS, kBufs - 1 stages (one to three) ahead of the products.  A row's eight 16-byte
 // chunks are permuted by (row / 2) % 8, so that the 16 rows of one operand read fall on distinct banks.
 namespace tiled {

@@ -5,9 +5,12 @@
 //     y = (t gain) r;   in 8 bits  s = max(max_k |y| (1 / 127), 2^-126),  q = rint(y (1 / s))
 //     backward, with g = dy gain:   dt = r (g - t r mean_k(g t r)) + dtotal,   dgain = sum over rows of dy t r
 //
-// Memory bounds them (bf16: 8, 7 and 8 bytes an element for about 15 instructions): a row stays in the registers of
-// one work-group between its sums and its outputs, so every byte moves once; work-groups go on to further rows
-// and have the next one on its way while they finish one, the gain (and its gradient) in registers.
+// Memory bounds them (bf16: 8, 7 and 8 bytes an element for about 15 instructions): up to 4096 pieces of 16 bytes a row
+// stays in the registers of one work-group between its sums and its outputs, so every byte moves once.  Forward a
+// work-group takes one row (more only beyond 2^20 rows).  Backward it goes on to further rows, with the gain and its
+// gradient in registers and, with one or four waves, the next rows on their way while it finishes some; with sixteen the
+// registers hold one row and none ahead, and the longest rows are read again (kAgain).  Rows shorter than a piece and
+// longer ones go element by element and are read twice.
 // Measured (bf16 with a residual; us, bytes that cross HBM over time): 16384 x 4096 forward 92, 5.8 TB/s, backward 90 + 5
 // for the gain's sum, 6.1; 65536 x 4096 into 8 bits 309, 6.1; one row of 4096 2.4.
 #pragma once
@@ -295,7 +298,8 @@ __global__ __launch_bounds__(kWaves * 64) void rms_norm_backward_kernel(
     constexpr int n = P::n, kRows = norm::rows_at_once(kWaves, kChunks);
     constexpr bool kAhead = norm::fetches_ahead(kWaves);
     // the longest rows are read again for their gradients, from the caches: 128 registers do not hold them beside
-    // the gain and its gradient (us: 8000 x 30000 bf16 704, with spills 857; 8000 x 20000 255 and 307)
+    // the gain and its gradient (us, and where they are held and spill: 8000 x 30000 bf16 740, 857; 8000 x 20000 257, 307).
+    // Four pieces of bf16 spill even so, about 60 registers of gain and gradient; three up to 4
     constexpr bool kAgain = kWaves == 16 && kChunks * n > 16;
     __shared__ float2 part[2][kRows][kWaves];
     const norm::Place<E, kWaves, kChunks> at(K);

@@ -25,7 +25,8 @@
 // sequence's first segment, which starts from the caller's state, the output sums the states
 // in the order of the kernel the sequential prefill uses for the same D (kRowsOrder: the
 // row-mapped kernel's pairs and halves when D is a multiple of 32), so that segment
-// reproduces the sequential prefill bit for bit.  Other segments, and every segment when D is
+// reproduces the sequential prefill bit for bit (that one's fp32 sums: in bf16 at such a D its
+// states are rounded on their way into the sum).  Other segments, and every segment when D is
 // not a multiple of 32, sum with one fma per state in state order (7 fewer instructions a
 // token than the pairs and halves).
 #pragma once
