@@ -73,7 +73,7 @@ struct GateArgs {
     float *h_final;
     int64_t batch, L, D, ld_xd, ld_bc, ld_y;
     OutGate gate;
-    bool fp32_sum;   // with a chunk given or automatic: the precision must not depend on the way that the shape is scanned
+    bool fp32_sum;   // with a chunk given or 0, so that the precision does not follow the way that the shape is scanned
     hipStream_t stream;
 };
 
@@ -218,7 +218,8 @@ jscan_status jscan_prefill_gate(const void *x, const void *delta, const float *A
     if (st != JSCAN_OK) return st;
     GateArgs a{};
     a.x = x, a.delta = delta, a.A = A, a.B = B, a.C = C, a.h0 = h0, a.y = y, a.h_final = h_final;
-    a.batch = batch, a.L = L, a.D = D, a.gate = OutGate{skip, z, ld_z}, a.fp32_sum = chunk >= 0, a.stream = static_cast<hipStream_t>(stream);
+    a.batch = batch, a.L = L, a.D = D, a.gate = OutGate{skip, z, ld_z}, a.stream = static_cast<hipStream_t>(stream);
+    a.fp32_sum = chunk >= 0;
     if (L == 0) {
         const int64_t total = batch * D * jscan::kDState, each = (int64_t)1 << 31;
         for (int64_t i = 0; i < total; i += each) {
