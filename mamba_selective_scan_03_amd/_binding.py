@@ -1249,7 +1249,8 @@ def rms_norm(x, gain, residual=None, eps=1e-6, y=None, total=None):
     """Root-mean-square norm with the residual's addition in front of it (``jscan_rms_norm``): ``total = x + residual``
     (rounded to x's dtype), ``y = total * gain / sqrt(mean(total ** 2) + eps)`` over the last dimension.  x and residual
     ``[..., K]`` (bf16 or fp32; slices of wider tensors too), gain ``[K]`` fp32.  Returns ``(y, total)``; without a
-    residual ``total`` is x.  A given ``total`` may be x or residual itself.  Autograd does not record the call
+    residual ``total`` is x.  A given ``total`` may be x or residual itself.  A row with a NaN or an infinity, or whose squares
+    overflow (or vanish, with ``eps`` 0), is NaN.  Autograd does not record the call
     (:func:`rms_norm_backward` has its gradients)."""
     if x.requires_grad or gain.requires_grad or (residual is not None and residual.requires_grad):
         _refuse_grad()
@@ -1302,7 +1303,8 @@ def rms_norm_workspace_bytes(M: int, K: int) -> int:
 def rms_norm_backward(total, gain, dy, dtotal=None, eps=1e-6, dx=None, dgain=None, workspace=None):
     """Gradients of :func:`rms_norm` (``jscan_rms_norm_backward``) from its ``total`` (x where there was no residual): dy
     the gradient of y, dtotal that of total's other uses (None: zeros).  Returns ``(dx, dgain)``: dx the gradient of
-    x and of residual alike, in their dtype; dgain ``[K]`` fp32.  A given ``dx`` may be dtotal itself."""
+    x and of residual alike, in their dtype; dgain ``[K]`` fp32.  A given ``dx`` may be dtotal itself.  A row that has no norm makes its dx
+    and all of dgain NaN."""
     if total.requires_grad or gain.requires_grad or dy.requires_grad or (dtotal is not None and dtotal.requires_grad):
         _refuse_grad()
     if _dual._current_level >= 0:
