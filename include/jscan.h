@@ -622,8 +622,8 @@ jscan_status jscan_causal_conv_step(void *state, const void *x_t, const float *w
  *             order of x's rows: z may be a half of a wider projection
  *   chunk     -1: token by token (h is jscan_prefill_resume's, or that of a_form's prefill); above 0: in segments
  *             of that many tokens (h is jscan_prefill_chunked's); 0: whichever way is expected to be fastest for this
- *             shape among those that sum in fp32.  Segments are for JSCAN_A_DIAGONAL: for the other forms 0 is token by token and a given
- *             length is JSCAN_ERR_FORM
+ *             shape among those that sum in fp32.  Segments are for JSCAN_A_DIAGONAL: for the other forms 0 is token
+ *             by token and a given length is JSCAN_ERR_FORM
  *   workspace jscan_prefill_gate_workspace(batch, L, D, N, chunk) bytes where a_form is JSCAN_A_DIAGONAL; else, and
  *             where that is 0, it may be NULL
  *   h0        [batch][D][N] fp32 or NULL for zeros; may equal h_final

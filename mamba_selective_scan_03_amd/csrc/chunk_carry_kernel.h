@@ -98,9 +98,9 @@ static __global__ __launch_bounds__(carry::kThreads) void chunk_carry_kernel(flo
 }
 
 // The same for at most kGroups segments, where a group is one segment and the walk above a plain one: a lane has four
-// states of a channel and walks their segments in order, to the same values wherever the maps are finite.  The kernel above reads sixteen
-// segments a group, used or not, so that it pays for many channels: 19 sequences of 40 tokens and 6656 channels in three
-// segments take 363 us with it and 76 with this, the scans' two passes included.
+// states of a channel and walks their segments in order, to the same values wherever the maps are finite.  The kernel
+// above reads sixteen segments a group, used or not, so that it pays for many channels: 19 sequences of 40 tokens and
+// 6656 channels in three segments take 363 us with it and 76 with this, the scans' two passes included.
 static __global__ __launch_bounds__(256) void chunk_carry_few_kernel(float *__restrict__ hbuf,
                                                                      const float *__restrict__ dsum,
                                                                      const float *__restrict__ A,

@@ -24,7 +24,7 @@ bool gate_grids_fit(int64_t batch, int64_t D, const ChunkPlan &p) {
 constexpr int64_t kMostGateStride = (int64_t)1 << 25;   // elements between rows of z (32-bit byte offsets of 8 rows)
 
 // How an automatic call scans: the way that is expected to take least, token by token or in segments of seg_len tokens.
-// Times in us, from one GPU of 256 CUs (bf16 with fp32 sums; fp32 takes up to 1.1 times that):
+// Times in us, from one GPU of 256 CUs (bf16 with fp32 sums; fp32 takes up to 1.13 times that):
 //     rows kernel    a work-group a CU at a time, each 8 and 0.031 a token       (1 x 65536 x 8192 2086, 8 x 639 x 416 24)
 //     lane kernel    0.65 a token for few waves, 0.58 more for a wave a SIMD     (3 x 688 x 144 453, 24 x 847 x 5704 1508)
 //     segments       15, a token of both passes 0.66 to 1.25 with one to four waves a SIMD, which is what fits at a
